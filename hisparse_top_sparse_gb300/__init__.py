@@ -32,6 +32,8 @@ HS_LOGITS_F32 = 0
 HS_LOGITS_BF16 = 1
 LATENT_DIM = 576
 VALUE_DIM = 512
+Q8_ROW_BYTES = 656                      # a quantised latent row (hs_quant_rows)
+ATTN_Q8_WORKSPACE_BYTES = 32 << 20      # enough for every hs_sparse_attn_decode_q8 call
 
 EXPORTS = (
     "hs_buffer_create", "hs_buffer_destroy", "hs_request_reset", "hs_get_status",
@@ -40,7 +42,8 @@ EXPORTS = (
     "hs_verify_accept_noalloc", "hs_swap_apply_plan", "hs_backup_pages", "hs_reclaim_resident",
     "hs_sparse_attn_decode_mixed", "hs_backup_rows", "hs_backup_indexer",
     "hs_buffer_set_copy_sms", "hs_swap_in_attn_decode", "hs_step_groups",
-    "hs_step_overlap_fits",
+    "hs_step_overlap_fits", "hs_quant_rows", "hs_dequant_rows", "hs_sparse_attn_decode_q8",
+    "hs_verify_sample", "hs_verify_sample_finalize",
 )
 
 
@@ -103,6 +106,13 @@ def lib() -> ctypes.CDLL:
             "hs_backup_rows": (_I, [_I, _P, _P, _P, _P, _I, _I, _I64, _I64, _P, _P]),
             "hs_backup_indexer": (_I, [_I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _I64, _P,
                                        _P]),
+            "hs_quant_rows": (_I, [_P, _I, _I64, _I64, _P, _I64, _P, _P, _I, _P, _P]),
+            "hs_dequant_rows": (_I, [_P, _I64, _P, _I, _I64, _I64, _P, _P, _I, _P, _P]),
+            "hs_sparse_attn_decode_q8": (_I, [_P, _P, _I64, _P, _I, _I, _I, ctypes.c_float, _P, _P,
+                                              _P, ctypes.c_size_t, _P, _P]),
+            "hs_verify_sample": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+            "hs_verify_sample_finalize": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P,
+                                               _P, _P, _P, _P, _P]),
             "hs_backup_pages": (_I, [_I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _I64, _P, _P]),
         }
         for name, (res, args) in sig.items():
@@ -509,3 +519,170 @@ def hs_backup_indexer(src_caches, dst_caches, src_slots, host_slots, positions,
         int(compress_ratio), tb, src_caches[0].shape[0], dst_caches[0].shape[0],
         _ptr(status, "status", torch.int32, (1,), allow_none=True), _stream(stream)),
         "hs_backup_indexer")
+
+
+# ------------------------------------------------- quantised latent rows --
+
+def _on_current_device(**tensors) -> None:
+    """Every CUDA tensor given must be on the current device: the call launches
+    there, on that device's current stream."""
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{cur}")
+
+
+def _host_or_device(t, name) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda and not t.is_pinned():
+        raise ValueError(f"{name} must be a CUDA tensor or pinned host memory")
+
+
+def _q8_cache(t, name) -> int:
+    _host_or_device(t, name)
+    if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[1] != Q8_ROW_BYTES or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 [rows][{Q8_ROW_BYTES}] tensor")
+    return t.data_ptr()
+
+
+def _wide_rows(t, name):
+    """(pointer, dtype code, row stride) of bf16 / f32 rows of 576 values, the
+    rows any distance apart."""
+    _host_or_device(t, name)
+    if t.dim() != 2 or t.shape[1] != LATENT_DIM or (t.shape[0] > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows][{LATENT_DIM}] with contiguous rows")
+    if t.dtype == torch.float32:
+        dt = HS_LOGITS_F32
+    elif t.dtype == torch.bfloat16:
+        dt = HS_LOGITS_BF16
+    else:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    return t.data_ptr(), dt, t.stride(0) if t.shape[0] > 1 else LATENT_DIM
+
+
+def _slots(src_slots, dst_slots, src_rows, dst_rows) -> int:
+    """Entries of a row call: the slot lists' length, else every source row
+    (which the destination must hold)."""
+    given = [t for t in (src_slots, dst_slots) if t is not None]
+    for t in given:
+        if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape != given[0].shape:
+            raise ValueError("src_slots and dst_slots must be int32 [n] tensors of one length")
+    n = given[0].shape[0] if given else src_rows
+    if (src_slots is None and n > src_rows) or (dst_slots is None and n > dst_rows):
+        raise ValueError(f"{n} entries do not fit {src_rows} source / {dst_rows} destination rows")
+    return n
+
+
+def hs_quant_rows(src, cache, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
+    """Row dst_slots[i] of the q8 cache (uint8 [rows][656]) = row src_slots[i]
+    of src (bf16 / f32 [rows][576]), quantised; without a list entry i is row
+    i, negative slots are skipped."""
+    sp, dt, stride = _wide_rows(src, "src")
+    dp = _q8_cache(cache, "cache")
+    n = _slots(src_slots, dst_slots, src.shape[0], cache.shape[0])
+    _on_current_device(src=src, cache=cache, src_slots=src_slots, dst_slots=dst_slots,
+                       status=status)
+    _check(lib().hs_quant_rows(
+        sp, dt, stride, src.shape[0], dp, cache.shape[0],
+        _ptr(src_slots, "src_slots", torch.int32, allow_none=True),
+        _ptr(dst_slots, "dst_slots", torch.int32, allow_none=True), n,
+        _ptr(status, "status", torch.int32, (1,), allow_none=True), _stream(stream)),
+        "hs_quant_rows")
+
+
+def hs_dequant_rows(cache, dst, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
+    """Row dst_slots[i] of dst (bf16 / f32 [rows][576]) = the values of row
+    src_slots[i] of the q8 cache."""
+    sp = _q8_cache(cache, "cache")
+    dp, dt, stride = _wide_rows(dst, "dst")
+    n = _slots(src_slots, dst_slots, cache.shape[0], dst.shape[0])
+    _on_current_device(cache=cache, dst=dst, src_slots=src_slots, dst_slots=dst_slots,
+                       status=status)
+    _check(lib().hs_dequant_rows(
+        sp, cache.shape[0], dp, dt, stride, dst.shape[0],
+        _ptr(src_slots, "src_slots", torch.int32, allow_none=True),
+        _ptr(dst_slots, "dst_slots", torch.int32, allow_none=True), n,
+        _ptr(status, "status", torch.int32, (1,), allow_none=True), _stream(stream)),
+        "hs_dequant_rows")
+
+
+def hs_sparse_attn_decode_q8(q, kv, idx, scale: float, out, lse=None, workspace=None, status=None,
+                             stream=None) -> None:
+    """hs_sparse_attn_decode over a q8 cache (uint8 [rows][656]). workspace:
+    uint8 CUDA tensor (ATTN_Q8_WORKSPACE_BYTES is enough for every call) with
+    which few rows run split over the SMs; one per call in flight."""
+    R, H, D = q.shape
+    if D != LATENT_DIM:
+        raise ValueError("q must be [R][H][576]")
+    if kv.dim() != 2 or kv.shape[1] != Q8_ROW_BYTES:
+        raise ValueError(f"kv must be [rows][{Q8_ROW_BYTES}]")
+    if idx.dim() != 2:
+        raise ValueError("idx must be [R][K]")
+    K = idx.shape[1]
+    _on_current_device(q=q, kv=kv, idx=idx, out=out, lse=lse, workspace=workspace, status=status)
+    _check(lib().hs_sparse_attn_decode_q8(
+        _ptr(q, "q", torch.bfloat16), _ptr(kv, "kv", torch.uint8), kv.shape[0],
+        _ptr(idx, "idx", torch.int32, (R, K)), R, H, K, float(scale),
+        _ptr(out, "out", torch.bfloat16, (R, H, VALUE_DIM)),
+        _ptr(lse, "lse", torch.float32, (R, H), allow_none=True),
+        _ptr(workspace, "workspace", torch.uint8, allow_none=True),
+        workspace.numel() if workspace is not None else 0,
+        _ptr(status, "status", torch.int32, (1,), allow_none=True),
+        _stream(stream)), "hs_sparse_attn_decode_q8")
+
+
+# --------------------------------------------- verification by sampling --
+
+def _sample_args(logits, temperature, draft_tokens, draft_probs, uniforms, noise, accept_len,
+                 next_token, logprob):
+    """The C arguments shared by the two calls, checked."""
+    B, d1, V = logits.shape
+    d = d1 - 1
+    if logits.dtype == torch.float32:
+        dt = HS_LOGITS_F32
+    elif logits.dtype == torch.bfloat16:
+        dt = HS_LOGITS_BF16
+    else:
+        raise TypeError("logits must be float32 or bfloat16")
+    _on_current_device(logits=logits, temperature=temperature, draft_tokens=draft_tokens,
+                       draft_probs=draft_probs, uniforms=uniforms, noise=noise,
+                       accept_len=accept_len, next_token=next_token, logprob=logprob)
+    f32, i32 = torch.float32, torch.int32
+    head = (_ptr(logits, "logits"), dt, B, d, V, _ptr(temperature, "temperature", f32, (B,)),
+            _ptr(draft_tokens, "draft_tokens", i32, (B, d), allow_none=(d == 0)),
+            _ptr(draft_probs, "draft_probs", f32, (B, d, V), allow_none=True),
+            _ptr(uniforms, "uniforms", f32, (B, d), allow_none=(d == 0)),
+            _ptr(noise, "noise", f32, (B, V)))
+    tail = (_ptr(accept_len, "accept_len", i32, (B,)), _ptr(next_token, "next_token", i32, (B,)),
+            _ptr(logprob, "logprob", f32, (B, d1), allow_none=True))
+    return head, tail
+
+
+def hs_verify_sample(logits, temperature, draft_tokens, draft_probs, uniforms, noise, accept_len,
+                     next_token, logprob=None, status=None, stream=None) -> None:
+    """Drafts accepted against the target's probabilities with given random
+    numbers (temperature 0: greedily); draft_probs None: the drafts were
+    chosen outright. See include/hisparse.h."""
+    head, tail = _sample_args(logits, temperature, draft_tokens, draft_probs, uniforms, noise,
+                              accept_len, next_token, logprob)
+    _on_current_device(status=status)
+    _check(lib().hs_verify_sample(
+        *head, *tail, _ptr(status, "status", torch.int32, (1,), allow_none=True),
+        _stream(stream)), "hs_verify_sample")
+
+
+def hs_verify_sample_finalize(buf: HsBuffer, logits, temperature, draft_tokens, draft_probs,
+                              uniforms, noise, step_kv, kv_len, accept_len, next_token,
+                              logprob=None, req_ids=None, stream=None) -> None:
+    """hs_verify_sample and the commit of the accepted prefix's KV."""
+    head, tail = _sample_args(logits, temperature, draft_tokens, draft_probs, uniforms, noise,
+                              accept_len, next_token, logprob)
+    B, d1, _ = logits.shape
+    _on_current_device(step_kv=step_kv, req_ids=req_ids, kv_len=kv_len)
+    _check(lib().hs_verify_sample_finalize(
+        buf.handle, *head, _ptr(step_kv, "step_kv", torch.bfloat16, (B, d1, LATENT_DIM)),
+        _ptr(req_ids, "req_ids", torch.int32, (B,), allow_none=True),
+        _ptr(kv_len, "kv_len", torch.int32, (buf.max_reqs,)), *tail, _stream(stream)),
+        "hs_verify_sample_finalize")

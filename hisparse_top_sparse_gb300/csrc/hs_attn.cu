@@ -62,7 +62,7 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
-#include "hs_internal.cuh"
+#include "hs_q8.cuh"
 
 namespace {
 
@@ -86,7 +86,10 @@ constexpr int THREADS = 480;
 // attention. 4 x 96 x 32 + 2 x 56 x 32 = 15,872; at 98 (rounded to 104) it
 // no longer fits and the copies wait for whole SMs.
 #define ATTN_MAX_REGS 96
-static_assert(THREADS * ATTN_MAX_REGS <= 65536, "register budget");
+// The q8 kernel runs beside no copies: as many as the register file gives
+// 15 warps, for the rows that its gather warps hold in registers.
+#define Q8_MAX_REGS 128
+static_assert(THREADS * ATTN_MAX_REGS <= 65536 && THREADS * Q8_MAX_REGS <= 65536, "register budget");
 constexpr int NPROD = 256;
 constexpr float REF_SLACK = 30.0f;        // P <= 2^30 on the shared reference
 
@@ -286,6 +289,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
                "r"(valid ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void st_shared16(uint32_t dst, const uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
@@ -414,14 +422,25 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity)
   return __all_sync(0xffffffffu, bar_wait_cluster(bar, parity));
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(ATTN_MAX_REGS)
+// What a cluster of the q8 kernel does of its row: keys [s * keys, (s + 1) * keys)
+// for s = cluster % n, of the row's K. n > 1: O / l in f32 and the log-sum-exp of the
+// part go to o and lse (part s of row r, head h at index (s * R + r) * H + h),
+// which k_attn_join joins.
+struct Parts {
+  int32_t n, keys, R;
+  float *o, *lse;
+};
+
+template <bool Q8>
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MAX_REGS)
     k_attn_pair(const __grid_constant__ CUtensorMap tmap_q,
                 const char *__restrict__ q,
                 const char *__restrict__ kv_res, int64_t n_res, const char *__restrict__ kv_hot,
                 int64_t n_hot, const int32_t *__restrict__ row_req,
                 const int32_t *__restrict__ fully_resident, int32_t n_reqs,
-                const int32_t *__restrict__ idx, int32_t H, int32_t K, float scale_log2,
-                __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, uint32_t *status) {
+                const int32_t *__restrict__ idx, int32_t H, int32_t K_row, float scale_log2,
+                __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, uint32_t *status,
+                const __grid_constant__ Parts parts) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -439,13 +458,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(ATTN_MAX_REGS)
   const int c = (int)cluster_rank();                // value half; own tiles t = c mod 2
   const uint32_t peer = (uint32_t)(c ^ 1);
   const int n_hg = (H + HG - 1) / HG;
-  const int rg = blockIdx.x >> 1;
+  const int part = Q8 ? (int)(blockIdx.x >> 1) % parts.n : 0;
+  const int rg = Q8 ? (int)(blockIdx.x >> 1) / parts.n : blockIdx.x >> 1;
+  const int K = Q8 ? min(parts.keys, K_row - part * parts.keys) : K_row;
   const int r = rg / n_hg;
   const int h0 = (rg % n_hg) * HG;
   const int T = (K + NK - 1) / NK;
   const int n_own = T > c ? (T - c + 1) / 2 : 0;
   const int n_peer = T - n_own;
-  const int32_t *idx_row = idx + (int64_t)r * K;
+  const int32_t *idx_row = idx + (int64_t)r * K_row + (Q8 ? part * parts.keys : 0);
   // Position i of the tile sequence that the gathers and the P V issuer walk:
   // every pair of tiles with this CTA's own tile first (CTA 1 swaps the
   // pairs), so that an own tile's P V never waits behind the peer's P.
@@ -543,7 +564,113 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(ATTN_MAX_REGS)
   if (!req_ok && status && tid == 0 && c == 0) atomicOr(status, HS_STATUS_INDEX);
 
 
-  if (warp >= 4 && warp < 12) {
+  if (Q8 && warp >= 4 && warp < 12) {
+    // ------------------------- gather producers, q8 rows made bf16 tiles ----
+    // The same steps and slots as the bf16 gather below, but a thread loads
+    // its part of a row into registers one step ahead, and then decodes it
+    // into the slot: thread `sub` of a key takes 16-code chunks sub + 8 k
+    // (scale byte sub / 2 of word k of the row's exponents), rope chunk sub,
+    // and of a peer tile the two code chunks in this CTA's value half.
+    const int p = tid - 128;
+    const int key = p >> 3;
+    const int sub = p & 7;
+    auto load_id = [&](int t) -> int32_t {
+      const int j = t * NK + key;
+      return (t < T && j < K) ? __ldg(idx_row + j) : -1;
+    };
+    struct Chunks {
+      uint4 code[4], rope, scale;
+    };
+    auto load_row = [&](int t, int32_t id, Chunks &x) {
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x.code[k] = zero;
+      x.rope = x.scale = zero;
+      if (id < 0 || id >= n_kv) return;
+      const uint4 *row = reinterpret_cast<const uint4 *>(kv + (int64_t)id * HS_Q8_ROW_BYTES);
+      x.scale = __ldg(row + Q8_SCALE_OFF / 16);
+      if ((t & 1) == c) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x.code[k] = __ldg(row + sub + 8 * k);
+        x.rope = __ldg(row + Q8_ROPE_OFF / 16 + sub);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) x.code[k] = __ldg(row + 16 * c + sub + 8 * k);
+      }
+    };
+    // 16 codes into two chunks of a swizzled 64-dim block; the threads of the
+    // second half of a key write their upper chunk first, so that a quarter
+    // warp's eight stores fall into different banks
+    auto put = [&](uint32_t block, const uint4 w, uint32_t byte) {
+      const float s = q8_scale(byte & 0xFFu);
+      const uint2 a = q8_decode4_bf16(w.x, s), b = q8_decode4_bf16(w.y, s);
+      const uint2 d = q8_decode4_bf16(w.z, s), e = q8_decode4_bf16(w.w, s);
+      const bool up = sub >= 4;
+      const uint32_t j = 2 * (sub & 3);
+      st_shared16(block + sw128(key, j + up), up ? make_uint4(d.x, d.y, e.x, e.y)
+                                                 : make_uint4(a.x, a.y, b.x, b.y));
+      st_shared16(block + sw128(key, j + !up), up ? make_uint4(a.x, a.y, b.x, b.y)
+                                                  : make_uint4(d.x, d.y, e.x, e.y));
+    };
+    int ig = 0, jg = 0;
+    for (int pass = 0; pass < 2 && !timed_out; ++pass) {
+      if (pass == 1) {
+        if (!bar_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
+        if (!*s_redo) break;
+      }
+      int la = 0, lb = 0;
+      auto step = [&](int &a, int &b) -> int {
+        if (a < n_own && (b >= n_peer || a < b + PEER_LAG + 1)) return 2 * (a++) + c;
+        if (b < n_peer) return 2 * (b++) + (1 - c);
+        return T;
+      };
+      int t1 = step(la, lb), t2 = step(la, lb);
+      int32_t id2 = load_id(t2);
+      Chunks next;
+      load_row(t1, load_id(t1), next);
+      for (int i = 0; i < T; ++i) {
+        const int t = t1;
+        const Chunks x = next;
+        t1 = t2;
+        load_row(t1, id2, next);
+        t2 = step(la, lb);
+        id2 = load_id(t2);
+        const uint32_t sw[4] = {x.scale.x, x.scale.y, x.scale.z, x.scale.w};
+        const int sh = 8 * (sub >> 1);
+        if ((t & 1) == c) {
+          const int sa = ig % RA_SLOTS, so = ig % VO_SLOTS;
+          if ((ig == 1 && !bar_wait(bar(B_QSTAGED), 0)) ||
+              (ig >= RA_SLOTS && !bar_wait(bar(B_EMPTYA + sa), ((ig / RA_SLOTS) - 1) & 1)) ||
+              (ig >= VO_SLOTS && !bar_wait(bar(B_EMPTYVO + so), ((ig / VO_SLOTS) - 1) & 1))) {
+            timed_out = true;
+            break;
+          }
+          const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
+          const uint32_t rv = sbase + VO_OFF + so * V_SLOT_BYTES;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            put(kv_block(ra, rv, c, 2 * k + (sub >> 2)), x.code[k], sw[k] >> sh);
+          st_shared16(kv_block(ra, rv, c, 8) + sw128(key, sub), x.rope);
+          fence_proxy_async();
+          bar_arrive(bar(B_FULLA + sa));
+          ++ig;
+        } else {
+          const int sp = jg % VP_SLOTS;
+          if (jg >= VP_SLOTS && !bar_wait(bar(B_EMPTYVP + sp), ((jg / VP_SLOTS) - 1) & 1)) {
+            timed_out = true;
+            break;
+          }
+          const uint32_t rv = sbase + VP_OFF + sp * V_SLOT_BYTES;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            put(rv + (2 * k + (sub >> 2)) * KV_BLOCK_BYTES, x.code[k], (c ? sw[2 + k] : sw[k]) >> sh);
+          fence_proxy_async();
+          bar_arrive(bar(B_FULLVP + sp));
+          ++jg;
+        }
+      }
+    }
+  } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------ gather producers ----
     const int p = tid - 128;          // 0..255
     const int key = p >> 3;           // 32 keys per tile, 8 threads per key
@@ -861,8 +988,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(ATTN_MAX_REGS)
     const int h = h0 + hrow;
     const float lt = l + l_peer;
     reinterpret_cast<volatile float *>(sm + XMAX_OFF)[hrow] = lt > 0.f ? 1.0f / lt : 0.f;
-    if (lse && c == 0 && h < H)
-      lse[(int64_t)r * H + h] = lt > 0.f ? (ref + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
+    float *lse_to = Q8 && parts.n > 1 ? parts.lse + (int64_t)part * parts.R * H : lse;
+    if (lse_to && c == 0 && h < H)
+      lse_to[(int64_t)r * H + h] = lt > 0.f ? (ref + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
     if (tid == 0) *s_last = (uint32_t)last_pass;
     own_sent = ig;
   }
@@ -885,6 +1013,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(ATTN_MAX_REGS)
     fence_after();
     const int q4 = warp & 3, half = warp >> 2;
     const int row = q4 * 32 + lane;
+    const bool f32_out = Q8 && parts.n > 1;
     const float inv = ok ? reinterpret_cast<volatile float *>(sm + XMAX_OFF)[row] : 0.f;
     const uint32_t lane_q = tmem + ((uint32_t)(q4 * 32) << 16);
 #pragma unroll 1
@@ -898,6 +1027,20 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(ATTN_MAX_REGS)
       } else {
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[0][k] = o[1][k] = 0u;
+      }
+      if (f32_out) {
+        // a part of the row: O / l in f32, a thread's 64 dims as 256 bytes
+        if (h0 + row < H) {
+          float *dst = parts.o + (((int64_t)part * parts.R + r) * H + h0 + row) * DV + 256 * c + 32 * p0;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t *v = &o[k >> 3][4 * (k & 7)];
+            *reinterpret_cast<float4 *>(dst + 4 * k) =
+                make_float4(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv,
+                            __uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
+          }
+        }
+        continue;
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -919,11 +1062,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(ATTN_MAX_REGS)
     // 2 half + ((l >> 3) & 1) of row 8 it + 2 w + (l >> 4), so one warp
     // store writes two whole 256-byte row segments; nothing waits for the
     // stores, and the shared memory is free once it has been read
-    if (half == 0)
+    if (f32_out)
+      ;
+    else if (half == 0)
       named_bar_sync(2, 128);
     else
       named_bar_sync(3, 128);
-    {
+    if (!f32_out) {
       const int wq = warp & 3, b = 2 * half + ((lane >> 3) & 1), j = lane & 7;
       const unsigned char *src = sm + O_STG_OFF + b * (HG * 128);
       __nv_bfloat16 *dst_row = out + ((int64_t)r * H + h0) * DV + 256 * c + 64 * b + 8 * j;
@@ -986,7 +1131,9 @@ static int set_attn_attributes() {
   HS_CUDA_TRY(cudaGetDevice(&dev));
   static bool attr_done[64] = {false};
   if (dev >= 64 || !attr_done[dev]) {
-    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     SMEM_ALLOC));
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      SMEM_ALLOC));
     if (dev < 64) attr_done[dev] = true;
   }
@@ -996,7 +1143,7 @@ static int set_attn_attributes() {
 int hs_attn_block_attrs(cudaFuncAttributes *attr, int *threads, size_t *dyn_smem) {
   int rc = set_attn_attributes();
   if (rc) return rc;
-  HS_CUDA_TRY(cudaFuncGetAttributes(attr, k_attn_pair));
+  HS_CUDA_TRY(cudaFuncGetAttributes(attr, k_attn_pair<false>));
   *threads = THREADS;
   *dyn_smem = SMEM_ALLOC;
   return HS_OK;
@@ -1021,7 +1168,7 @@ int hs_attn_wave_rows(int32_t H, int32_t *rows) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    HS_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_attn_pair, &cfg));
+    HS_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_attn_pair<false>, &cfg));
     if (n < 1) n = 1;
     if (dev < 64) clusters[dev] = n;
   }
@@ -1041,11 +1188,14 @@ extern "C" int hs_sparse_attn_decode_mixed(const void *q, const void *kv_residen
                         n_reqs, idx, R, H, K, scale, out, lse, status, true, stream);
 }
 
-int hs_attn_launch(const void *q, const void *kv_resident, int64_t n_resident, const void *kv_hot,
-                   int64_t n_hot, const int32_t *row_req, const int32_t *fully_resident,
-                   int32_t n_reqs, const int32_t *idx, int32_t R, int32_t H, int32_t K,
-                   float scale, void *out, float *lse, uint32_t *status, bool pdl,
-                   cudaStream_t stream) {
+// Checks the arguments and launches k_attn_pair<Q8> (parts: the q8 kernel's
+// split of the rows' keys, chosen by the caller after the same size checks).
+template <bool Q8>
+static int attn_launch(const void *q, const void *kv_resident, int64_t n_resident,
+                       const void *kv_hot, int64_t n_hot, const int32_t *row_req,
+                       const int32_t *fully_resident, int32_t n_reqs, const int32_t *idx, int32_t R,
+                       int32_t H, int32_t K, float scale, void *out, float *lse, uint32_t *status,
+                       const Parts &parts, bool pdl, cudaStream_t stream) {
   if (R < 0 || H < 1 || H > 1024 || K < 0 || n_resident < 0 || n_hot < 0 ||
       (fully_resident && n_reqs < 0))
     return hs_set_error(HS_ERR_INVALID_ARG, "bad sizes R=%d H=%d (1..1024) K=%d n_kv=%lld/%lld",
@@ -1060,7 +1210,7 @@ int hs_attn_launch(const void *q, const void *kv_resident, int64_t n_resident, c
   if (!(scale == scale)) return hs_set_error(HS_ERR_INVALID_ARG, "scale is NaN");
   int rc = set_attn_attributes();
   if (rc) return rc;
-  const int64_t blocks = (int64_t)R * ((H + HG - 1) / HG) * 2;
+  const int64_t blocks = (int64_t)R * ((H + HG - 1) / HG) * 2 * parts.n;
   if (blocks > INT32_MAX) return hs_set_error(HS_ERR_UNSUPPORTED, "R*H too large");
   // q as a [R][H][576] bf16 tensor for the prologue's tensor copies
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -1096,12 +1246,22 @@ int hs_attn_launch(const void *q, const void *kv_resident, int64_t n_resident, c
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   HS_CUDA_TRY(cudaLaunchKernelEx(
-      &cfg, k_attn_pair, tmap, reinterpret_cast<const char *>(q),
+      &cfg, k_attn_pair<Q8>, tmap, reinterpret_cast<const char *>(q),
       reinterpret_cast<const char *>(kv_resident), n_resident,
       reinterpret_cast<const char *>(kv_hot), n_hot, row_req, fully_resident, n_reqs, idx, H, K,
-      scale * 1.4426950408889634f, reinterpret_cast<__nv_bfloat16 *>(out), lse, status));
+      scale * 1.4426950408889634f, reinterpret_cast<__nv_bfloat16 *>(out), lse, status, parts));
   HS_LAUNCH_CHECK("k_attn_pair");
   return HS_OK;
+}
+
+int hs_attn_launch(const void *q, const void *kv_resident, int64_t n_resident, const void *kv_hot,
+                   int64_t n_hot, const int32_t *row_req, const int32_t *fully_resident,
+                   int32_t n_reqs, const int32_t *idx, int32_t R, int32_t H, int32_t K,
+                   float scale, void *out, float *lse, uint32_t *status, bool pdl,
+                   cudaStream_t stream) {
+  const Parts whole = {1, K, R, nullptr, nullptr};
+  return attn_launch<false>(q, kv_resident, n_resident, kv_hot, n_hot, row_req, fully_resident,
+                            n_reqs, idx, R, H, K, scale, out, lse, status, whole, pdl, stream);
 }
 
 extern "C" int hs_sparse_attn_decode(const void *q, const void *kv, int64_t n_kv_rows,
@@ -1110,4 +1270,92 @@ extern "C" int hs_sparse_attn_decode(const void *q, const void *kv, int64_t n_kv
                                      hs_stream_t stream) {
   return hs_sparse_attn_decode_mixed(q, kv, n_kv_rows, nullptr, 0, nullptr, nullptr, 0, idx, R,
                                      H, K, scale, out, lse, status, stream);
+}
+
+// ---- attention over a q8 cache ----------------------------------------------
+
+namespace {
+
+// Joins the parts of every (row, head): with L = max_s lse_s and w_s =
+// exp(lse_s - L), out = sum_s w_s O_s / sum_s w_s and lse = L + ln(sum_s w_s).
+// A block per (row, head), four dims per thread; parts without a valid key
+// have lse_s = -inf and weigh nothing.
+__global__ void __launch_bounds__(DV / 4) k_attn_join(const float *__restrict__ o,
+                                                      const float *__restrict__ part_lse, int32_t n,
+                                                      int64_t rows, __nv_bfloat16 *__restrict__ out,
+                                                      float *__restrict__ lse) {
+  // a programmatic dependent launch of the kernel that writes the parts
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int64_t row = blockIdx.x;
+  const float4 *src = reinterpret_cast<const float4 *>(o + row * DV) + threadIdx.x;
+  float top = -INFINITY;
+  for (int s = 0; s < n; ++s) top = fmaxf(top, part_lse[s * rows + row]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float w_sum = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float w = exp2f((part_lse[s * rows + row] - ref) * 1.4426950408889634f);
+    const float4 v = src[s * rows * (DV / 4)];
+    w_sum += w;
+    a.x += w * v.x;
+    a.y += w * v.y;
+    a.z += w * v.z;
+    a.w += w * v.w;
+  }
+  const float inv = w_sum == 0.f ? 0.f : 1.f / w_sum;
+  reinterpret_cast<uint2 *>(out + row * DV)[threadIdx.x] =
+      make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+  if (lse && threadIdx.x == 0) lse[row] = w_sum == 0.f ? -INFINITY : ref + logf(w_sum);
+}
+
+constexpr int PART_MIN_TILES = 4;   // tiles of 32 keys, at least, in a part of a row
+
+}  // namespace
+
+extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n_kv_rows,
+                                        const int32_t *idx, int32_t R, int32_t H, int32_t K,
+                                        float scale, void *out, float *lse, void *workspace,
+                                        size_t workspace_bytes, uint32_t *status,
+                                        hs_stream_t stream) {
+  if ((uintptr_t)workspace & 15)
+    return hs_set_error(HS_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  Parts parts = {1, K, R, nullptr, nullptr};
+  if (R > 0 && H >= 1 && H <= 1024 && K > 0 && workspace) {
+    // Few rows leave most of the SMs idle and walk their keys one after the
+    // other: the keys of a row are split while the wave has clusters left.
+    int clusters = 0;
+    int rc = hs_attn_wave_rows(1, &clusters);
+    if (rc) return rc;
+    const int64_t base = (int64_t)R * ((H + HG - 1) / HG), rows = (int64_t)R * H;
+    const int tiles = (K + NK - 1) / NK;
+    int64_t n = clusters / base;
+    if (n > tiles / PART_MIN_TILES) n = tiles / PART_MIN_TILES;
+    const int64_t room = (int64_t)(workspace_bytes / (rows * (DV + 1) * sizeof(float)));
+    if (n > room) n = room;
+    if (n > 1) {
+      const int per = (int)((tiles + n - 1) / n);
+      parts.n = (tiles + per - 1) / per;      // every part has keys
+      parts.keys = per * NK;
+      parts.o = reinterpret_cast<float *>(workspace);
+      parts.lse = parts.o + parts.n * rows * DV;
+    }
+    if (parts.n == 1) parts.keys = K;
+  }
+  int rc = attn_launch<true>(q, kv, n_kv_rows, nullptr, 0, nullptr, nullptr, 0, idx, R, H, K, scale,
+                             out, lse, status, parts, true, stream);
+  if (rc || parts.n == 1) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(R * H));
+  cfg.blockDim = dim3(DV / 4);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  HS_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_attn_join, (const float *)parts.o, (const float *)parts.lse,
+                                 parts.n, (int64_t)R * H, reinterpret_cast<__nv_bfloat16 *>(out), lse));
+  HS_LAUNCH_CHECK("k_attn_join");
+  return HS_OK;
 }

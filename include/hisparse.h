@@ -76,6 +76,10 @@ enum hs_status_code {
 #define HS_LOGITS_F32 0
 #define HS_LOGITS_BF16 1
 
+#define HS_Q8_ROW_BYTES 656 /* a quantised latent row, see hs_quant_rows   */
+#define HS_ATTN_Q8_WORKSPACE_BYTES 33554432 /* enough for every call of
+                                hs_sparse_attn_decode_q8               */
+
 /* ------------------------------------------------------------------------ */
 /* Hot buffer ([MTP] section 1 and core state maps; [VLLM] HiSparseHotSpec)  */
 /* ------------------------------------------------------------------------ */
@@ -257,6 +261,75 @@ int hs_sparse_attn_decode(const void *q, const void *kv, int64_t n_kv_rows,
                           const int32_t *idx, int32_t R, int32_t H, int32_t K,
                           float scale, void *out, float *lse, uint32_t *status,
                           hs_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* q8: a quantised latent cache, written, read back and attended over        */
+/*     ("vllm 分析(十二) HiSparse 下篇", section c4a kv cache 写入: the        */
+/*     compressor quantises a cache's entries as it stores them)             */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A q8 row holds one latent row in 656 bytes, 16-byte aligned:
+ *   [0, 512)    e4m3 codes of dims 0..511
+ *   [512, 640)  dims 512..575 (rope) in bf16
+ *   [640, 656)  16 bytes e + 127, one for each 32 dims of the first 512;
+ * the value of a code is code * 2^e. e is the smallest integer in
+ * [-112, 120] with max |x| <= 448 * 2^e over the group's finite values, and
+ * the code is x / 2^e rounded to nearest, ties to even: within 1/16 of x, or
+ * 2^(e-10) for the smallest. Every value of a row is a bf16 number, so reading
+ * rows back, in bf16 or f32, and attending over them rounds nothing. NaN stays
+ * NaN; an infinity (and a magnitude past 248 * 2^120) reads back as an
+ * infinity of its sign, the group then having e = 120. A row of zero bytes is
+ * a row of zeros.
+ *
+ * hs_swap_apply_plan, hs_backup_pages and hs_backup_rows move such rows with
+ * row_bytes = 656; the slot table of an hs_swap_in indexes a q8 follower cache
+ * for hs_sparse_attn_decode_q8.
+ */
+
+/*
+ * For every i < n with src_slots[i] >= 0 and dst_slots[i] >= 0: row
+ * src_slots[i] of src, quantised, becomes row dst_slots[i] of dst. A negative
+ * slot means "no entry" and is skipped; one at or past src_rows / dst_rows is
+ * skipped and sets HS_STATUS_INDEX in status. Rows that no entry names stay as
+ * they were. Destination slots are distinct within a call.
+ *   src         [src_rows] rows of 576 values, src_stride values from row to
+ *               row, bf16 or f32 (src_dtype HS_LOGITS_BF16 / HS_LOGITS_F32)
+ *   dst         q8 rows [dst_rows][656]
+ *               both in device memory or page-locked mapped host memory
+ *   src_slots, dst_slots  device int32 [n] or NULL (entry i is row i)
+ *   status      device uint32 or NULL
+ * Requirements: n >= 0, src_stride >= 576, src, dst and src_stride in bytes
+ * multiples of 16.
+ */
+int hs_quant_rows(const void *src, int32_t src_dtype, int64_t src_stride, int64_t src_rows,
+                  void *dst, int64_t dst_rows, const int32_t *src_slots,
+                  const int32_t *dst_slots, int32_t n, uint32_t *status, hs_stream_t stream);
+
+/* The other way: q8 rows of src into rows of 576 bf16 or f32 values of dst
+ * (exact); slots, status and requirements as hs_quant_rows. */
+int hs_dequant_rows(const void *src, int64_t src_rows, void *dst, int32_t dst_dtype,
+                    int64_t dst_stride, int64_t dst_rows, const int32_t *src_slots,
+                    const int32_t *dst_slots, int32_t n, uint32_t *status, hs_stream_t stream);
+
+/*
+ * hs_sparse_attn_decode over a q8 cache: the same arguments, formulas, skipped
+ * entries and launch, with kv [n_kv_rows][656]. The values enter the products
+ * as bf16 (exactly), the softmax numerators are rounded to bf16 as there.
+ *   workspace   device memory, 16-byte aligned, or NULL: with few rows the
+ *               keys of a row are split over the idle SMs and the parts'
+ *               outputs joined by a second kernel; the parts (f32) go here.
+ *               workspace_bytes bounds the number of parts
+ *               (HS_ATTN_Q8_WORKSPACE_BYTES is enough for every call; NULL or
+ *               too little runs each row in one part). It carries nothing
+ *               from call to call; calls that may run at the same time
+ *               (other streams, captured graphs replayed side by side) need
+ *               one each.
+ */
+int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n_kv_rows,
+                             const int32_t *idx, int32_t R, int32_t H, int32_t K, float scale,
+                             void *out, float *lse, void *workspace, size_t workspace_bytes,
+                             uint32_t *status, hs_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* a2-a6 in one call: swap-in and attention of a decode step, with the host  */
@@ -563,6 +636,65 @@ int hs_verify_accept_noalloc(const void *logits, int32_t logits_dtype, int32_t B
                              int32_t d, int32_t V, const int32_t *draft_tokens,
                              int32_t *accept_len, int32_t *next_token,
                              hs_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Verification by sampling (beside [KVF] ④, which verifies greedily)         */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * For batch entry b with temperature T = temperature[b] > 0:
+ *   p_i = softmax(logits[b][i] / T) for i = 0..d, q_i = draft_probs[b][i];
+ *   draft i, x = draft_tokens[b][i], is accepted while
+ *     uniforms[b][i] * q_i(x) < p_i(x);
+ *   accept_len[b] = m, the number of drafts accepted before the first refusal;
+ *   next_token[b] = the v with the largest w(v) / noise[b][v] (the lowest v
+ *     on ties) among those with w(v) > 0, where w = max(p_m - q_m, 0) when
+ *     m < d (p_m itself if that is 0 everywhere) and w = p_d when m = d.
+ * With uniforms uniform in [0, 1) and noise exponentially distributed (mean
+ * 1), all independent of the drafts, the tokens are distributed as if sampled
+ * from p one by one. draft_probs NULL: the drafts were chosen outright, q_i is
+ * 1 at the draft and 0 elsewhere.
+ * T <= 0 (or NaN) verifies the entry greedily, as hs_verify_finalize does; its
+ * numbers are not used.
+ * Logits of -inf (or NaN) are masked tokens: never accepted, never drawn.
+ * +inf counts as the type's largest finite value. A row with no other logit
+ * accepts nothing and gives next_token -1. A draft outside [0, V) is refused
+ * and sets HS_STATUS_INDEX.
+ *   logits        device [B][d+1][V], fp32 or bf16 (logits_dtype)
+ *   temperature   device float [B]
+ *   draft_tokens  device int32 [B][d]
+ *   draft_probs   device float [B][d][V] or NULL
+ *   uniforms      device float [B][d]
+ *   noise         device float [B][V], > 0
+ *   accept_len, next_token  device int32 [B]
+ *   logprob       device float [B][d+1] or NULL: ln p_i of each token given
+ *                 (the accepted drafts, then next_token), 0 behind them; for a
+ *                 greedy entry under softmax(logits)
+ *   status        device uint32 or NULL
+ * One launch, no scratch, nothing allocated, nothing carried over: calls may
+ * overlap and be captured in a graph.
+ * Requirements: B >= 1, 0 <= d <= 255, 1 <= V <= 2^30, arrays aligned to their
+ * elements.
+ */
+int hs_verify_sample(const void *logits, int32_t logits_dtype, int32_t B, int32_t d, int32_t V,
+                     const float *temperature, const int32_t *draft_tokens,
+                     const float *draft_probs, const float *uniforms, const float *noise,
+                     int32_t *accept_len, int32_t *next_token, float *logprob, uint32_t *status,
+                     hs_stream_t stream);
+
+/*
+ * hs_verify_sample, then the commit of hs_verify_finalize (step_kv, req_ids,
+ * kv_len, capacity and status as there; the status goes to the buffer's word).
+ * One launch. Not for stream capture (HS_ERR_UNSUPPORTED): a commit is told
+ * from a repeated one by the buffer's host-side clock.
+ * Requirements: those of both calls.
+ */
+int hs_verify_sample_finalize(hs_buffer *buf, const void *logits, int32_t logits_dtype,
+                              int32_t B, int32_t d, int32_t V, const float *temperature,
+                              const int32_t *draft_tokens, const float *draft_probs,
+                              const float *uniforms, const float *noise, const void *step_kv,
+                              const int32_t *req_ids, int32_t *kv_len, int32_t *accept_len,
+                              int32_t *next_token, float *logprob, hs_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Measurement helper (no counterpart on the pages)                           */

@@ -622,3 +622,165 @@ def compress_slot_mapping(host_slots, positions, storage_block_size: int,
         entry = (int(p) % lbs) // compress_ratio
         out[i] = block * storage_block_size + entry
     return out
+
+
+# --------------------------------------------------------------------------
+# Quantised latent rows: 512 e4m3 codes, 64 bf16 rope dims, 16 exponents
+# --------------------------------------------------------------------------
+
+Q8_ROW = 656
+Q8_GROUP = 32
+Q8_E_MIN, Q8_E_MAX = -112, 120
+
+
+def e4m3_value(code: int) -> float:
+    """The number an e4m3 byte stands for: sign, four exponent bits (bias 7),
+    three fraction bits; no infinities, 0x7F / 0xFF are NaN."""
+    if code & 0x7F == 0x7F:
+        return float("nan")
+    ex, frac = (code >> 3) & 15, code & 7
+    mag = frac * 2.0 ** -9 if ex == 0 else (8 + frac) * 2.0 ** (ex - 10)
+    return -mag if code & 0x80 else mag
+
+
+E4M3_VALUES = np.array([e4m3_value(c) for c in range(256)])
+_E4M3_MAGS = E4M3_VALUES[:127]                     # 0 .. 448, ascending with the code
+# midpoints of neighbouring magnitudes, for rounding to the nearest
+_E4M3_MIDS = (_E4M3_MAGS[:-1] + _E4M3_MAGS[1:]) / 2
+
+
+def e4m3_encode(x) -> np.ndarray:
+    """Nearest e4m3 code of each number, ties to the even code, magnitudes
+    past 448 to 448, NaN to 0x7F."""
+    x = np.asarray(x, np.float64)
+    a = np.abs(x)
+    lo = np.searchsorted(_E4M3_MIDS, a, side="left")        # a midpoint goes down ...
+    tie = (lo < 126) & (a == _E4M3_MIDS[np.minimum(lo, 125)])
+    code = np.where(tie & (lo % 2 == 1), lo + 1, lo)        # ... or up, to the even code
+    code = np.where(np.signbit(x), code + 128, code)
+    return np.where(np.isnan(x), 0x7F, code).astype(np.uint8)
+
+
+def f64_to_bf16_bits(x) -> np.ndarray:
+    """f32 values (given as float64) rounded to bf16, ties to even."""
+    u = np.asarray(x, np.float64).astype(np.float32).view(np.uint32).astype(np.uint64)
+    r = ((u + 0x7FFF + ((u >> 16) & 1)) >> 16).astype(np.uint16)
+    return np.where(np.isnan(x), np.uint16(0x7FC0), r)
+
+
+def q8_quantise(x) -> np.ndarray:
+    """Latent rows [n][576] (float64 of bf16 or f32 values) -> uint8 [n][656].
+    Per group of 32 dims: e is the smallest integer with the largest finite
+    magnitude at most 448 * 2**e, within [-112, 120] (120 beside an infinity)."""
+    x = np.asarray(x, np.float64)
+    n = x.shape[0]
+    out = np.zeros((n, Q8_ROW), np.uint8)
+    v = x[:, :VALUE_DIM].reshape(n, -1, Q8_GROUP)
+    amax = np.nanmax(np.where(np.isnan(v), 0.0, np.abs(v)), axis=2)
+    e = np.full(amax.shape, Q8_E_MIN, np.int64)
+    for k in range(Q8_E_MIN, Q8_E_MAX):            # the definition, one exponent at a time
+        e = np.where(amax > 448.0 * 2.0 ** k, k + 1, e)
+    out[:, :VALUE_DIM] = e4m3_encode(v * 2.0 ** -e[:, :, None].astype(np.float64)).reshape(n, -1)
+    out[:, VALUE_DIM:640] = f64_to_bf16_bits(x[:, VALUE_DIM:]).view(np.uint8).reshape(n, -1)
+    out[:, 640:] = (e + 127).astype(np.uint8)
+    return out
+
+
+def q8_values(rows) -> np.ndarray:
+    """float64 values [n][576] of q8 rows; what passes the largest f32 is inf."""
+    rows = np.ascontiguousarray(rows)
+    scale = 2.0 ** (rows[:, 640:].astype(np.float64) - 127)
+    v = E4M3_VALUES[rows[:, :VALUE_DIM]] * np.repeat(scale, Q8_GROUP, axis=1)
+    v = np.where(np.abs(v) >= 2.0 ** 128, np.copysign(np.inf, v), v)
+    rope = bf16_bits_to_f64(np.ascontiguousarray(rows[:, VALUE_DIM:640]).view(np.uint16))
+    return np.concatenate([v, rope], axis=1)
+
+
+# --------------------------------------------------------------------------
+# Verification by sampling, from given random numbers
+# --------------------------------------------------------------------------
+
+def verify_sample(logits, temperature, drafts, probs, uniforms, noise):
+    """Per request, one draft after the other: draft ``i`` = x is accepted
+    while ``uniforms[i] * q_i(x) < p_i(x)``, p the softmax of logits / T, q the
+    draft probabilities (1 at the draft when ``probs`` is None). The next token
+    is argmax ``w / noise`` (lowest index on ties, w > 0 only), ``w = max(p -
+    q, 0)`` at the refused draft (p itself if that vanishes), p past the last.
+    T <= 0 or NaN: greedy. Masked logits (-inf, NaN) have p = 0, +inf counts as
+    ``logits_max``; a row of masked ones accepts nothing and gives -1.
+
+    Returns ``(accept, token, logprob [B][d+1], margin [B])``: margin is the
+    smallest relative distance between two numbers that a decision compared.
+    """
+    if isinstance(logits, torch.Tensor):
+        top = float(torch.finfo(logits.dtype).max)
+        logits = logits.detach().cpu().double().numpy()
+    else:
+        top = float(np.finfo(np.float32).max)
+        logits = np.asarray(logits, np.float64)
+    as64 = lambda t: None if t is None else np.asarray(t.detach().cpu() if isinstance(t, torch.Tensor) else t, np.float64)
+    T, q, u, E = as64(temperature), as64(probs), as64(uniforms), as64(noise)
+    dr = _np_i64(drafts)
+    B, d1, V = logits.shape
+    d = d1 - 1
+    acc, tok = np.zeros(B, np.int32), np.zeros(B, np.int32)
+    lps, margins = np.zeros((B, d1)), np.full(B, np.inf)
+
+    def near(b, x, y):
+        m = max(abs(x), abs(y))
+        if m > 0:
+            margins[b] = min(margins[b], abs(x - y) / m)
+
+    for b in range(B):
+        greedy = not T[b] > 0
+        t = 1.0 if greedy else T[b]
+        m, given = 0, []
+        while True:
+            l = np.where(np.isnan(logits[b, m]), -np.inf, np.minimum(logits[b, m], top))
+            empty = l.max() == -np.inf
+            with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+                z = np.where(l == -np.inf, -np.inf, (l - l.max()) / t)
+                p = np.exp(z)
+                s = p.sum()
+                p = p / s
+                lp = z - np.log(s)
+            if m == d or empty:
+                break
+            x = int(dr[b, m])
+            if x < 0 or x >= V:
+                break
+            if greedy:
+                if x != int(np.argmax(l)):
+                    break
+            else:
+                bar = u[b, m] * (q[b, m, x] if q is not None else 1.0)
+                if p[x] > 0:
+                    near(b, bar, p[x])
+                if not bar < p[x]:
+                    break
+            given.append(lp[x])
+            m += 1
+        if empty:
+            x, last = -1, -np.inf
+        else:
+            if greedy:
+                x = int(np.argmax(l))
+            else:
+                w = p
+                if m < d and q is not None:
+                    w = np.maximum(p - q[b, m], 0.0)
+                elif m < d and 0 <= dr[b, m] < V:
+                    w = p.copy()
+                    w[dr[b, m]] = 0.0
+                if not (w > 0).any():
+                    w = p
+                r = np.where(w > 0, w / E[b], -1.0)
+                x = int(np.argmax(r))
+                rest = np.delete(r, x)
+                if rest.size and rest.max() > 0:
+                    near(b, r[x], rest.max())
+            last = lp[x]
+        acc[b], tok[b] = m, x
+        lps[b, :m] = given
+        lps[b, m] = last
+    return acc, tok, lps, margins
