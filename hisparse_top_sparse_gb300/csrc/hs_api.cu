@@ -12,6 +12,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "hs_internal.cuh"
 
@@ -26,6 +27,19 @@ int hs_set_error(int code, const char *fmt, ...) {
 }
 
 extern "C" const char *hs_last_error_string(void) { return g_err; }
+
+int hs_sm_count(int *sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  HS_CUDA_TRY(cudaGetDevice(&dev));
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    HS_CUDA_TRY(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev));
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  *sms = n;
+  return HS_OK;
+}
 
 int hs_check_device_ptr(const void *p, const char *name, bool allow_null) {
   if (!p && !allow_null)

@@ -70,6 +70,9 @@ int hs_set_error(int code, const char *fmt, ...);
                           cudaGetErrorString(e_));                             \
   } while (0)
 
+// Multiprocessors of the current device (looked up once per device).
+int hs_sm_count(int *sms);
+
 int hs_check_device_ptr(const void *p, const char *name, bool allow_null);
 // The device-accessible alias of p (device memory, or page-locked host memory
 // mapped into the device's address space); `align`-byte alignment required.

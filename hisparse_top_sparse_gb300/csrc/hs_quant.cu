@@ -228,9 +228,9 @@ int check_rows(const void *wide, int32_t dtype, int64_t wide_stride, int64_t wid
 // Blocks for n rows: a warp per row up to eight blocks (64 warps, the SM's
 // limit) on every SM.
 int row_blocks(int32_t n, int *blocks) {
-  int dev = 0, sms = 0;
-  HS_CUDA_TRY(cudaGetDevice(&dev));
-  HS_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  int sms = 0;
+  int rc = hs_sm_count(&sms);
+  if (rc) return rc;
   const int64_t want = ((int64_t)n + QT_THREADS / 32 - 1) / (QT_THREADS / 32);
   *blocks = (int)(want < (int64_t)sms * 8 ? want : (int64_t)sms * 8);
   return HS_OK;

@@ -13,22 +13,28 @@
 //   needs one pass and no running sum over the vocabulary, so that the order
 //   of additions cannot move the answer.
 //
-// One cluster of 1 to 8 blocks per request takes the request's rows one after
-// the other and stops at the first refusal: the logits of later inputs, and
-// the draft probabilities and noise of every row but the last one, are never
-// read. HBM bounds it: each logits row is streamed once for (M, S), and the
-// row that yields the token a second time, beside q and E, mostly from L2.
-// M and S come in one pass (a thread rescales its sum when a batch of its
-// values brings a new maximum). The sums are f32, each of a thread's few
-// hundred terms, then joined as a tree in a fixed order: results do not
-// depend on scheduling.
+// One cluster of 1 to 8 blocks per request takes the request's rows in order,
+// one or a few at a time, and stops at the first refusal: the logits behind it,
+// and the draft probabilities of every row but the last, are never read. HBM
+// bounds it: each logits row is streamed once for (M, S), and the row that
+// yields the token a second time, beside q and E, mostly from L2. M and S
+// come in one pass (a thread rescales its sum when a batch of its values
+// brings a new maximum). The sums are f32, each of a thread's few hundred
+// terms, then joined as a tree in a fixed order: results do not depend on
+// scheduling. A thread copies its values ahead into places of its own in
+// shared memory (cp.async), so no barrier stands between loading and using.
 //
 // The blocks of a cluster exchange (M, S) and the race's winner through
-// distributed shared memory, each pulling all blocks' figures and joining
-// them in the same order; the request's drafts, numbers and temperature are
-// read once by the first block and pulled by the others. So every block takes
-// the same decisions from the same bits, and the barriers match even if a
-// caller overwrites the inputs during the call.
+// distributed shared memory, every warp joining all warps' figures in the
+// same order; the request's drafts, numbers and temperature are read once by
+// the first block and pushed to the others. So every block takes the same
+// decisions from the same bits, and the barriers match even if a caller
+// overwrites the inputs during the call.
+//
+// Measured (bf16 logits, draft probabilities given): 256 requests x 3 drafts,
+// V = 129280: 92 us, 62 % of what the 385 MB it has to move take at the
+// measured copy rate (requests of unlike lengths leave SMs idle at the end);
+// 64 x 3: 34 us; 2 x 3, V = 1024 f32: 6.4 us, latency.
 
 #include <float.h>
 
@@ -36,8 +42,13 @@
 
 namespace {
 
-constexpr int NT = 512;             // threads per block
-constexpr int NB = 8;               // 16-byte loads of a thread in flight
+constexpr int NT = 256;             // threads per block
+constexpr int MIN_BLOCKS = 4;       // blocks per SM, at least
+constexpr int WARPS = NT / 32;
+constexpr int RING = 12;            // 16-byte places of a thread's ring of copies in flight
+constexpr int BATCH = 4;            // vectors of a row taken together
+constexpr int NB = 8;               // values of a thread in flight where rows are not aligned
+constexpr size_t RING_BYTES = (size_t)RING * NT * 16;
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX_DRAFTS = 255;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -51,6 +62,8 @@ struct SampleArgs {
   int32_t *accept_len, *next_token;
   float *logprob;
   uint32_t *status;
+  uint32_t log_rows;       // 2^log_rows rows side by side in a cluster, at most its blocks
+  bool aligned;            // rows of logits, probs and noise all start on 16 bytes
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -63,17 +76,38 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(r));
   return r;
 }
-// every thread of the cluster: writes before it are seen by reads after it
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
-                   : "memory");
+// the cluster barrier: writes before a thread's arrival are seen by every
+// thread that has waited
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
 }
-// a word of block `rank`'s shared memory, at the place p has in this block's
-__device__ __forceinline__ uint32_t pull(const void *p, uint32_t rank) {
-  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), v;
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// 4 / 8 bytes into block `rank`'s shared memory, at the place p has in this
+// block's
+__device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
   asm volatile("mapa.shared::cluster.u32 %0, %0, %1;\n" : "+r"(a) : "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(a) : "memory");
-  return v;
+  return a;
+}
+__device__ __forceinline__ void push(const void *p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(remote(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void push2(const void *p, uint32_t rank, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};\n" ::"r"(remote(p, rank)), "r"(a), "r"(b)
+               : "memory");
+}
+// a thread's 16-byte copies into its own ring places
+__device__ __forceinline__ void copy16(uint4 *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -115,6 +149,15 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// part `rank` of `total` things among 2^log_n
+__device__ __forceinline__ int32_t part_of(int32_t total, uint32_t rank, uint32_t log_n) {
+  return (int32_t)(((int64_t)total * rank) >> log_n);
+}
 
 // Running (maximum, sum of exp2((x - max) * c)) of one thread, and the batch
 // at which the maximum was first reached.
@@ -129,60 +172,67 @@ __device__ __forceinline__ void join(float &m, float &s, float om, float os, flo
   m = t;
 }
 
-// One slice of a row: its 16-byte vectors [lo, hi) by all threads of the
-// block, batch k of a thread being vectors k .. k + (NB - 1) NT.
+// One slice of a row: the 16-byte vectors [lo, hi) of its aligned body, taken
+// by all threads of the block, and the fewer than 2 PER values outside the
+// body, all the first slice's.
 template <int DTYPE>
 struct Slice {
-  const uint4 *body;
-  int32_t lo, hi, head, V;     // `head` unaligned values before the body
   static constexpr int PER = DTYPE == HS_LOGITS_F32 ? 4 : 8;
+  const uint4 *body;
+  int32_t lo, hi, head, tail, rest;
 
-  __device__ __forceinline__ Slice(const char *row, int32_t V_, uint32_t rank, uint32_t n) {
+  __device__ __forceinline__ Slice(const char *row, int32_t V, uint32_t rank, uint32_t log_n) {
     constexpr int elem = DTYPE == HS_LOGITS_F32 ? 4 : 2;
-    V = V_;
     head = (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / elem);
     if (head > V) head = V;
     const int32_t vecs = (V - head) / PER;
     body = reinterpret_cast<const uint4 *>(row + (int64_t)head * elem);
-    lo = (int32_t)((int64_t)vecs * rank / n);
-    hi = (int32_t)((int64_t)vecs * (rank + 1) / n);
-    if (rank == 0) rest = head + (V - head - vecs * PER); else rest = 0;
-    tail0 = head + vecs * PER;
+    lo = part_of(vecs, rank, log_n);
+    hi = part_of(vecs, rank + 1, log_n);
+    tail = head + vecs * PER;
+    rest = rank == 0 ? head + (V - tail) : 0;
   }
-  // the values outside the body (fewer than 2 PER), all the first block's
-  int32_t rest, tail0;
   __device__ __forceinline__ int32_t rest_index(int32_t j) const {
-    return j < head ? j : tail0 + (j - head);
-  }
-  __device__ __forceinline__ void load(int32_t k, uint4 (&w)[NB]) const {
-    const uint32_t none = DTYPE == HS_LOGITS_F32 ? 0xff800000u : 0xff80ff80u;
-#pragma unroll
-    for (int u = 0; u < NB; ++u)
-      w[u] = k + u * NT < hi ? __ldg(body + k + u * NT) : make_uint4(none, none, none, none);
-#pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      uint32_t *x = reinterpret_cast<uint32_t *>(&w[u]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (DTYPE == HS_LOGITS_F32) {
-          x[j] = __float_as_uint(clean<DTYPE>(__uint_as_float(x[j])));
-        } else {
-          __nv_bfloat162 &h = reinterpret_cast<__nv_bfloat162 &>(x[j]);
-          const uint32_t lowest = 0xff80ff80u, most = 0x7f7f7f7fu;
-          h = __hmin2(__hmax2(h, reinterpret_cast<const __nv_bfloat162 &>(lowest)),
-                      reinterpret_cast<const __nv_bfloat162 &>(most));
-        }
-      }
-    }
+    return j < head ? j : tail + (j - head);
   }
 };
 
+// the values of a vector as they count
 template <int DTYPE>
-__device__ __forceinline__ float batch_max(const uint4 (&w)[NB]) {
+__device__ __forceinline__ uint4 clean16(uint4 w) {
+  uint32_t *x = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (DTYPE == HS_LOGITS_F32) {
+      x[j] = __float_as_uint(clean<DTYPE>(__uint_as_float(x[j])));
+    } else {
+      __nv_bfloat162 &h = reinterpret_cast<__nv_bfloat162 &>(x[j]);
+      const uint32_t lowest = 0xff80ff80u, most = 0x7f7f7f7fu;
+      h = __hmin2(__hmax2(h, reinterpret_cast<const __nv_bfloat162 &>(lowest)),
+                  reinterpret_cast<const __nv_bfloat162 &>(most));
+    }
+  }
+  return w;
+}
+template <int DTYPE>
+__device__ __forceinline__ uint4 masked16() {
+  const uint32_t none = DTYPE == HS_LOGITS_F32 ? 0xff800000u : 0xff80ff80u;
+  return make_uint4(none, none, none, none);
+}
+// value j of a vector
+template <int DTYPE>
+__device__ __forceinline__ float value(const uint4 &w, int j) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  if (DTYPE == HS_LOGITS_F32) return __uint_as_float(x[j & 3]);
+  return __uint_as_float((j & 1) ? x[j >> 1] & 0xFFFF0000u : x[j >> 1] << 16);
+}
+
+template <int DTYPE>
+__device__ __forceinline__ float batch_max(const uint4 (&w)[BATCH]) {
   if (DTYPE == HS_LOGITS_F32) {
     float t = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < NB; ++u)
+    for (int u = 0; u < BATCH; ++u)
       t = fmaxf(t, fmaxf(fmaxf(__uint_as_float(w[u].x), __uint_as_float(w[u].y)),
                          fmaxf(__uint_as_float(w[u].z), __uint_as_float(w[u].w))));
     return t;
@@ -190,42 +240,91 @@ __device__ __forceinline__ float batch_max(const uint4 (&w)[NB]) {
   const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(w);
   __nv_bfloat162 t = h[0];
 #pragma unroll
-  for (int u = 1; u < 4 * NB; ++u) t = __hmax2(t, h[u]);
+  for (int u = 1; u < 4 * BATCH; ++u) t = __hmax2(t, h[u]);
   return fmaxf(__low2float(t), __high2float(t));
 }
 
+// A batch into the running statistics.
 template <int DTYPE>
-__device__ __forceinline__ Stat row_stat(const Slice<DTYPE> &sl, const void *row, float c) {
+__device__ __forceinline__ void take_batch(Stat &st, const uint4 (&w)[BATCH], int32_t k, float c) {
+  const float t = batch_max<DTYPE>(w);
+  if (t > st.m) {
+    st.s *= ex2((st.m - t) * c);
+    st.m = t;
+    st.at = k;
+  }
+  if (st.m == -INFINITY) return;
+  const uint64_t nm = pack2(-st.m, -st.m), cc = pack2(c, c);
+  uint64_t acc[2] = {0, 0};                  // four partial sums
+#pragma unroll
+  for (int u = 0; u < BATCH; ++u) {
+#pragma unroll
+    for (int j = 0; j < Slice<DTYPE>::PER; j += 2) {
+      float a, b;
+      unpack2(mul2(add2(pack2(value<DTYPE>(w[u], j), value<DTYPE>(w[u], j + 1)), nm), cc), a, b);
+      acc[(j >> 1) & 1] = add2(acc[(j >> 1) & 1], pack2(ex2(a), ex2(b)));
+    }
+  }
+  float a, b;
+  unpack2(add2(acc[0], acc[1]), a, b);
+  st.s += a + b;
+}
+
+// The slice's statistics: batches of BATCH vectors through this thread's own
+// ring places (its column of `ring`), RING / BATCH of them in flight; no
+// thread reads another's, so nothing but the copies is waited for. The values
+// are taken as they are: a NaN or +inf among them makes the sum NaN, and the
+// thread then goes through its part once more, cleaning each value.
+// `meanwhile` runs while the first copies are on their way.
+template <int DTYPE, typename F>
+__device__ __forceinline__ Stat row_stat(const Slice<DTYPE> &sl, const void *row, float c, uint4 *ring,
+                                         const F &meanwhile) {
+  constexpr int DEPTH = RING / BATCH, STEP = BATCH * NT;
   Stat st = {-INFINITY, 0.f, -1};
-  const uint64_t cc = pack2(c, c);
-  for (int32_t k = sl.lo + (int)threadIdx.x; k < sl.hi; k += NB * NT) {
-    uint4 w[NB];
-    sl.load(k, w);
-    const float t = batch_max<DTYPE>(w);
-    if (t > st.m) {
-      st.s *= ex2((st.m - t) * c);
-      st.m = t;
-      st.at = k;
-    }
-    if (st.m == -INFINITY) continue;
-    const uint64_t nm = pack2(-st.m, -st.m);
-    uint64_t acc[4] = {0, 0, 0, 0};            // eight partial sums
+  const int32_t k0 = sl.lo + (int)threadIdx.x;
+  const int32_t full = sl.hi - (BATCH - 1) * NT;        // batches before it are whole
+  auto issue = [&](int32_t k, int place) {
+    uint4 *to = ring + place * STEP;
+    if (k < full) {
 #pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      for (int u = 0; u < BATCH; ++u) copy16(to + u * NT, sl.body + k + u * NT);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 4; j += DTYPE == HS_LOGITS_F32 ? 2 : 1) {
-        const uint64_t v = DTYPE == HS_LOGITS_F32
-                               ? pack2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]))
-                               : pack2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
-        float a, b;
-        unpack2(mul2(add2(v, nm), cc), a, b);
-        acc[j] = add2(acc[j], pack2(ex2(a), ex2(b)));
-      }
+      for (int u = 0; u < BATCH - 1; ++u)
+        if (k + u * NT < sl.hi) copy16(to + u * NT, sl.body + k + u * NT);
     }
-    float a, b;
-    unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), a, b);
-    st.s += a + b;
+    copy_commit();
+  };
+#pragma unroll
+  for (int p = 0; p < DEPTH; ++p) issue(k0 + p * STEP, p);
+  meanwhile();
+  int place = 0;
+  for (int32_t k = k0; k < sl.hi; k += STEP) {
+    copy_wait<DEPTH - 1>();
+    uint4 w[BATCH];
+    const uint4 *from = ring + place * STEP;
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) w[u] = from[u * NT];
+    if (k >= full) {
+#pragma unroll
+      for (int u = 1; u < BATCH; ++u)
+        if (k + u * NT >= sl.hi) w[u] = masked16<DTYPE>();
+    }
+    issue(k + DEPTH * STEP, place);
+    place = place + 1 == DEPTH ? 0 : place + 1;
+    take_batch<DTYPE>(st, w, k, c);
+  }
+  copy_wait<0>();
+  if (st.s != st.s) {
+    st = {-INFINITY, 0.f, -1};
+#pragma unroll 1
+    for (int32_t k = k0; k < sl.hi; k += STEP) {
+      uint4 w[BATCH];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u)
+        w[u] = k + u * NT < sl.hi ? clean16<DTYPE>(__ldg(sl.body + k + u * NT)) : masked16<DTYPE>();
+      take_batch<DTYPE>(st, w, k, c);
+    }
   }
   for (int32_t j = threadIdx.x; j < sl.rest; j += NT) {
     const float x = logit_at<DTYPE>(row, sl.rest_index(j));
@@ -242,21 +341,14 @@ __device__ __forceinline__ int32_t row_first(const Slice<DTYPE> &sl, const void 
   int32_t best = INT32_MAX;
   if (st.m != top) return best;
   if (st.at >= 0) {
-    uint4 w[NB];
-    sl.load(st.at, w);
+#pragma unroll 1
+    for (int u = 0; u < BATCH; ++u) {
+      const int32_t k = st.at + u * NT;
+      if (k >= sl.hi) break;
+      const uint4 w = clean16<DTYPE>(__ldg(sl.body + k));
 #pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-      const int32_t i0 = sl.head + (st.at + u * NT) * Slice<DTYPE>::PER;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (DTYPE == HS_LOGITS_F32) {
-          if (__uint_as_float(x[j]) == top) best = min(best, i0 + j);
-        } else {
-          if (__uint_as_float(x[j] << 16) == top) best = min(best, i0 + 2 * j);
-          if (__uint_as_float(x[j] & 0xFFFF0000u) == top) best = min(best, i0 + 2 * j + 1);
-        }
-      }
+      for (int j = 0; j < Slice<DTYPE>::PER; ++j)
+        if (value<DTYPE>(w, j) == top) best = min(best, sl.head + k * Slice<DTYPE>::PER + j);
     }
   }
   for (int32_t j = threadIdx.x; j < sl.rest; j += NT)
@@ -265,203 +357,343 @@ __device__ __forceinline__ int32_t row_first(const Slice<DTYPE> &sl, const void 
 }
 
 struct Shared {
-  // of the first block, pulled by the others at the start
+  // the first block's reading of the request, pushed to every block
   float temperature;
   float draft_logit[MAX_DRAFTS], draft_bar[MAX_DRAFTS];     // l_i(x_i); u_i q_i(x_i)
   int32_t draft[MAX_DRAFTS];
-  // per warp, per block (two alternating places) and per cluster
-  float wa[NT / 32];
-  uint32_t wb[NT / 32];
-  uint32_t part[2][2];
-  float a;
-  uint32_t b;
+  // a pair from every warp of the cluster, at two alternating places
+  uint2 pair[2][MAX_CLUSTER * WARPS];
 };
 
-// Joins a pair of words of every thread of the cluster: within the warps and
-// the block by `op` on (float, word), over the blocks in rank order. Every
-// thread gets the result. `turn` alternates between the two exchange places;
-// the barrier inside keeps a place from being written while it is read.
+// Joins a (float, word) pair of every thread of the cluster by `op`, apart
+// for each of the G = 2^log_g rows (row g the blocks of ranks g n / G and up).
+// Each warp joins its own threads' pairs and pushes the result to every block;
+// behind the cluster's barrier every warp joins all warps' pairs, in the same
+// order everywhere. On return lane g * 32 / G holds row g's. A place of `pair`
+// is written again two calls later, behind the barrier of the call between,
+// by when it has been read.
 template <typename Op>
-__device__ __forceinline__ void cluster_join(Shared &sh, float &a, uint32_t &b, uint32_t n, int &turn,
-                                             const Op &op) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float oa = __shfl_xor_sync(0xffffffffu, a, o);
-    const uint32_t ob = __shfl_xor_sync(0xffffffffu, b, o);
-    op(a, b, oa, ob);
-  }
-  if (lane == 0) {
-    sh.wa[warp] = a;
-    sh.wb[warp] = b;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    a = sh.wa[lane & (NT / 32 - 1)];
-    b = sh.wb[lane & (NT / 32 - 1)];
-#pragma unroll
-    for (int o = NT / 64; o; o >>= 1) {
-      const float oa = __shfl_xor_sync(0xffffffffu, a, o);
-      const uint32_t ob = __shfl_xor_sync(0xffffffffu, b, o);
-      op(a, b, oa, ob);
-    }
-    if (lane == 0) {
-      sh.part[turn][0] = __float_as_uint(a);
-      sh.part[turn][1] = b;
-      sh.a = a;
-      sh.b = b;
-    }
-  }
+__device__ __forceinline__ void cluster_join(Shared &sh, float &a, uint32_t &b, uint32_t rank,
+                                             uint32_t n, uint32_t log_g, int &turn, const Op &op) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  op.across(a, b, 32);
+  uint2 *pairs = sh.pair[turn];
   if (n == 1) {
+    if (lane == 0) pairs[warp] = make_uint2(__float_as_uint(a), b);
     __syncthreads();
   } else {
-    cluster_sync();
-    if (warp == 0) {
-      const uint32_t from = (uint32_t)lane < n ? lane : 0;
-      const uint32_t pa = pull(&sh.part[turn][0], from), pb = pull(&sh.part[turn][1], from);
-      a = __uint_as_float(__shfl_sync(0xffffffffu, pa, 0));
-      b = __shfl_sync(0xffffffffu, pb, 0);
-      for (uint32_t r = 1; r < n; ++r)
-        op(a, b, __uint_as_float(__shfl_sync(0xffffffffu, pa, r)), __shfl_sync(0xffffffffu, pb, r));
-      if (lane == 0) {
-        sh.a = a;
-        sh.b = b;
+    if (lane < n) push2(pairs + rank * WARPS + warp, lane, __float_as_uint(a), b);
+    cluster_arrive();
+    cluster_wait();
+  }
+  turn ^= 1;
+  op.empty(a, b);
+  // 32 / G lanes for the pairs of each row
+  const uint32_t lanes = 32u >> log_g, count = (n >> log_g) * WARPS, row = lane / lanes;
+  for (uint32_t k = lane & (lanes - 1); k < count; k += lanes) {
+    const uint2 p = pairs[row * count + k];
+    op.two(a, b, __uint_as_float(p.x), p.y);
+  }
+  op.across(a, b, lanes);
+}
+
+// (maximum, sum of exp2((x - maximum) c))
+struct StatOp {
+  float c;
+  __device__ __forceinline__ void empty(float &m, uint32_t &s) const {
+    m = -INFINITY;
+    s = 0u;
+  }
+  __device__ __forceinline__ void two(float &m, uint32_t &s, float om, uint32_t os) const {
+    float t = __uint_as_float(s);
+    join(m, t, om, __uint_as_float(os), c);
+    s = __float_as_uint(t);
+  }
+  // over groups of `width` lanes: the maximum first, then each sum on it
+  __device__ __forceinline__ void across(float &m, uint32_t &s, uint32_t width) const {
+    float top = m, t = __uint_as_float(s);
+    for (uint32_t o = 1; o < width; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (m != -INFINITY) t *= ex2((m - top) * c);
+    for (uint32_t o = 1; o < width; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    m = top;
+    s = __float_as_uint(t);
+  }
+};
+// the lowest index
+struct MinOp {
+  __device__ __forceinline__ void empty(float &, uint32_t &i) const { i = INT32_MAX; }
+  __device__ __forceinline__ void two(float &, uint32_t &i, float, uint32_t oi) const { i = min(i, oi); }
+  __device__ __forceinline__ void across(float &, uint32_t &i, uint32_t width) const {
+    for (uint32_t o = 1; o < width; o <<= 1) i = min(i, __shfl_xor_sync(0xffffffffu, i, o));
+  }
+};
+// the largest value, the lowest index of it
+struct BestOp {
+  __device__ __forceinline__ void empty(float &v, uint32_t &i) const {
+    v = 0.f;
+    i = INT32_MAX;
+  }
+  __device__ __forceinline__ void two(float &v, uint32_t &i, float ov, uint32_t oi) const {
+    if (ov > v || (ov == v && oi < i)) {
+      v = ov;
+      i = oi;
+    }
+  }
+  __device__ __forceinline__ void across(float &v, uint32_t &i, uint32_t width) const {
+    for (uint32_t o = 1; o < width; o <<= 1) {
+      const float ov = __shfl_xor_sync(0xffffffffu, v, o);
+      const uint32_t oi = __shfl_xor_sync(0xffffffffu, i, o);
+      two(v, i, ov, oi);
+    }
+  }
+};
+
+// The race over the row that yields the token: the largest w(v) / E(v) of this
+// thread's values and its v (INT32_MAX: none). `barred`: a token without weight.
+//
+// A value is divided only when it may win: p / E > best, rounded, needs
+// p > h E for h a little below best (2^-21, past the two roundings). t = p - h E
+// is one fused operation with the sign of the exact difference, and a group
+// of values whose largest t is negative is passed over. `best` is first that of
+// the thread's warp so far, so few groups are looked into.
+struct Race {
+  float best;
+  uint32_t at;
+  float h;
+  // (a logit of +inf, which counts as the row's maximum, has come out infinite)
+  __device__ __forceinline__ void look(float p, float e, float w, float inv, int32_t v, int32_t barred) {
+    if (p == INFINITY) p = inv - w;
+    if (p > 0.f && v != barred) {
+      const float r = p / e;
+      if (r > best) {                  // a thread's indices ascend: the lowest stays
+        best = r;
+        at = (uint32_t)v;
       }
     }
-    __syncthreads();
   }
-  a = sh.a;
-  b = sh.b;
-  turn ^= 1;
-  __syncthreads();      // wa, wb, a and b may be written again
+  __device__ __forceinline__ void share() {        // by the whole warp
+    h = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(best))) * 0.9999995f;
+  }
+};
+
+template <int DTYPE, bool VEC>
+__device__ __forceinline__ Race race(const char *row, const float *q, const float *E, int32_t V,
+                                     uint32_t rank, uint32_t log_n, float top, float c, float inv,
+                                     int32_t barred, uint4 *ring) {
+  Race ra = {0.f, INT32_MAX, 0.f};
+  if (VEC) {
+    // units of 16 bytes of logits and as many values of q and E, through the
+    // thread's ring places as in row_stat
+    constexpr int PER = Slice<DTYPE>::PER, QV = PER / 4, SLOTS = 1 + 2 * QV, DEPTH = RING / SLOTS;
+    const int32_t units = V / PER;
+    const int32_t lo = part_of(units, rank, log_n), hi = part_of(units, rank + 1, log_n);
+    auto issue = [&](int32_t k, int place) {
+      uint4 *to = ring + place * SLOTS * NT;
+      if (k < hi) {
+        copy16(to, reinterpret_cast<const uint4 *>(row) + k);
+#pragma unroll
+        for (int j = 0; j < QV; ++j) {
+          copy16(to + (1 + j) * NT, reinterpret_cast<const uint4 *>(E) + QV * k + j);
+          if (q) copy16(to + (1 + QV + j) * NT, reinterpret_cast<const uint4 *>(q) + QV * k + j);
+        }
+      }
+      copy_commit();
+    };
+#pragma unroll
+    for (int p = 0; p < DEPTH; ++p) issue(lo + p * NT + (int)threadIdx.x, p);
+    const uint64_t nm = pack2(-top, -top), cc = pack2(c, c), ii = pack2(inv, inv);
+    int place = 0;
+    for (int32_t k0 = lo; k0 < hi; k0 += NT) {
+      const int32_t k = k0 + (int)threadIdx.x;
+      copy_wait<DEPTH - 1>();
+      if (k < hi) {
+        const uint4 *from = ring + place * SLOTS * NT;
+        const uint4 x = from[0];
+        float p[PER], e[PER], t[PER];
+        const uint64_t nh = pack2(-ra.h, -ra.h);
+#pragma unroll
+        for (int j = 0; j < QV; ++j) {
+          const uint4 e4 = from[(1 + j) * NT];
+          const uint4 w4 = q ? from[(1 + QV + j) * NT] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const int o = 4 * j + i;
+            e[o] = value<HS_LOGITS_F32>(e4, i);
+            e[o + 1] = value<HS_LOGITS_F32>(e4, i + 1);
+            float a, b;
+            // (a NaN among the logits makes its p NaN, which never wins)
+            unpack2(mul2(add2(pack2(value<DTYPE>(x, o), value<DTYPE>(x, o + 1)), nm), cc), a, b);
+            const uint64_t pp = fma2(pack2(ex2(a), ex2(b)), ii,
+                                     pack2(-value<HS_LOGITS_F32>(w4, i), -value<HS_LOGITS_F32>(w4, i + 1)));
+            unpack2(pp, p[o], p[o + 1]);
+            unpack2(fma2(nh, pack2(e[o], e[o + 1]), pp), t[o], t[o + 1]);
+          }
+        }
+        float big = t[0];
+#pragma unroll
+        for (int j = 1; j < PER; ++j) big = fmaxf(big, t[j]);
+        if (big >= 0.f) {
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            if (t[j] >= 0.f)
+              ra.look(p[j], e[j], q ? value<HS_LOGITS_F32>(from[(1 + QV + j / 4) * NT], j) : 0.f, inv,
+                      k * PER + j, barred);
+        }
+      }
+      issue(k + DEPTH * NT, place);
+      place = place + 1 == DEPTH ? 0 : place + 1;
+      ra.share();
+    }
+    copy_wait<0>();
+  } else {
+    const int32_t lo = part_of(V, rank, log_n), hi = part_of(V, rank + 1, log_n);
+    for (int32_t k0 = lo; k0 < hi; k0 += NB * NT) {
+      float p[NB], e[NB], w[NB];
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        const int32_t v = k0 + u * NT + (int)threadIdx.x;
+        p[u] = -INFINITY;
+        e[u] = 1.f;
+        w[u] = 0.f;
+        if (v < hi) {
+          p[u] = DTYPE == HS_LOGITS_F32
+                     ? __ldg(reinterpret_cast<const float *>(row) + v)
+                     : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(row) + v) << 16);
+          e[u] = __ldcs(E + v);
+          if (q) w[u] = __ldcs(q + v);
+        }
+      }
+      float big = -1.f;
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        p[u] = fmaf(ex2((p[u] - top) * c), inv, -w[u]);
+        big = fmaxf(big, fmaf(-ra.h, e[u], p[u]));
+      }
+      if (big >= 0.f) {
+#pragma unroll
+        for (int u = 0; u < NB; ++u) ra.look(p[u], e[u], w[u], inv, k0 + u * NT + (int)threadIdx.x, barred);
+      }
+      ra.share();
+    }
+  }
+  return ra;
 }
 
 template <int DTYPE, bool COMMIT>
-__global__ void __launch_bounds__(NT) k_verify_sample(const __grid_constant__ SampleArgs sa,
-                                                      const __grid_constant__ CommitArgs ca) {
+__global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_constant__ SampleArgs sa,
+                                                                  const __grid_constant__ CommitArgs ca) {
+  extern __shared__ uint4 ring_base[];
   __shared__ Shared sh;
+  uint4 *ring = ring_base + threadIdx.x;
   const uint32_t rank = cluster_rank(), n = cluster_size();
+  if (n > 1) cluster_arrive();       // waited for before the first push: every block runs by then
   const int b = (int)(blockIdx.x / n);
   const int32_t d = sa.d, V = sa.V;
   const int tid = threadIdx.x;
   const int64_t row_bytes = (int64_t)V * (DTYPE == HS_LOGITS_F32 ? 4 : 2);
   const char *rows = reinterpret_cast<const char *>(sa.logits) + (int64_t)b * (d + 1) * row_bytes;
 
-  if (rank == 0) {
-    bool bad = false;
-    for (int i = tid; i < d; i += NT) {
-      const int64_t k = (int64_t)b * d + i;
-      const int32_t x = __ldg(sa.drafts + k);
-      const bool ok = x >= 0 && x < V;         // any other token is refused
-      bad |= !ok;
-      sh.draft[i] = ok ? x : -1;
-      sh.draft_logit[i] = ok ? logit_at<DTYPE>(rows + i * row_bytes, x) : -INFINITY;
-      sh.draft_bar[i] = __ldg(sa.uniforms + k) * (sa.probs && ok ? __ldg(sa.probs + k * V + x) : 1.f);
-    }
-    if (tid == 0) sh.temperature = __ldg(sa.temperature + b);
-    if (bad && sa.status) atomicOr(sa.status, HS_STATUS_INDEX);
-  }
-  if (n > 1) {
-    cluster_sync();
-    if (rank != 0) {
-      for (int i = tid; i < d; i += NT) {
-        sh.draft[i] = (int32_t)pull(&sh.draft[i], 0);
-        sh.draft_logit[i] = __uint_as_float(pull(&sh.draft_logit[i], 0));
-        sh.draft_bar[i] = __uint_as_float(pull(&sh.draft_bar[i], 0));
-      }
-      if (tid == 0) sh.temperature = __uint_as_float(pull(&sh.temperature, 0));
-    }
-  }
-  __syncthreads();
-  const bool greedy = !(sh.temperature > 0.f);
-  const float T = greedy ? 1.f : sh.temperature;
+  // What decides is read once, by the first block, and pushed to the others
+  // before the first exchange; this reading of the temperature only scales
+  // the first rows' sums.
+  static_assert(MAX_DRAFTS <= NT, "a thread per draft");
+  int32_t x = -1;
+  float x_logit = -INFINITY, x_bar = 0.f;
+  const float t_read = __ldg(sa.temperature + b);
   // within the normal floats: products with it are never 0 * inf
-  const float c = fminf(fmaxf(LOG2E / T, FLT_MIN), FLT_MAX);
+  float c = fminf(fmaxf(LOG2E / (t_read > 0.f ? t_read : 1.f), FLT_MIN), FLT_MAX);
 
+  // Rows m0 .. m0 + G - 1 at a time, n / G blocks a row.
+  const uint32_t log_n = 31 - __clz(n), log_g = sa.log_rows, G = 1u << log_g, per_row = n >> log_g;
   int turn = 0, m = 0;
-  float top, sum;
-  int32_t token = -1;
-  for (;; ++m) {
-    const char *row = rows + m * row_bytes;
-    const Slice<DTYPE> sl(row, V, rank, n);
-    const Stat st = row_stat<DTYPE>(sl, row, c);
-    top = st.m;
-    uint32_t s_bits = __float_as_uint(st.s);
-    cluster_join(sh, top, s_bits, n, turn, [c](float &am, uint32_t &as, float bm, uint32_t bs) {
-      float s = __uint_as_float(as);
-      join(am, s, bm, __uint_as_float(bs), c);
-      as = __float_as_uint(s);
+  float top = -INFINITY, sum = 0.f, T = 1.f;
+  uint32_t first = INT32_MAX;
+  bool greedy = false, done = false;
+  for (int m0 = 0; !done; m0 += (int)G) {
+    const int mine = m0 + (int)(rank >> (log_n - log_g));
+    const char *row = rows + (mine <= d ? mine : d) * row_bytes;
+    const Slice<DTYPE> sl(row, mine <= d ? V : 0, rank & (per_row - 1), log_n - log_g);
+    const Stat st = row_stat<DTYPE>(sl, row, c, ring, [&]() {
+      if (m0 != 0 || rank != 0 || tid >= d) return;
+      const int64_t k = (int64_t)b * d + tid;
+      x = __ldg(sa.drafts + k);
+      const bool ok = x >= 0 && x < V;         // any other token is refused
+      if (!ok) {
+        x = -1;
+        if (sa.status) atomicOr(sa.status, HS_STATUS_INDEX);
+      }
+      x_logit = ok ? logit_at<DTYPE>(rows + tid * row_bytes, x) : -INFINITY;
+      x_bar = __ldg(sa.uniforms + k) * (sa.probs && ok ? __ldg(sa.probs + k * V + x) : 1.f);
     });
-    sum = __uint_as_float(s_bits);
-    if (greedy) {
-      float unused = 0.f;
-      uint32_t first = top == -INFINITY ? INT32_MAX : (uint32_t)row_first<DTYPE>(sl, row, st, top);
-      cluster_join(sh, unused, first, n, turn,
-                   [](float &, uint32_t &ai, float, uint32_t bi) { ai = min(ai, bi); });
-      token = first == INT32_MAX ? -1 : (int32_t)first;
+    if (m0 == 0) {
+      if (n > 1) cluster_wait();
+      if (rank == 0) {
+        for (uint32_t r = 0; r < n; ++r) {
+          if (tid < d) {
+            push(sh.draft + tid, r, (uint32_t)x);
+            push(sh.draft_logit + tid, r, __float_as_uint(x_logit));
+            push(sh.draft_bar + tid, r, __float_as_uint(x_bar));
+          }
+          if (tid == 0) push(&sh.temperature, r, __float_as_uint(t_read));
+        }
+      }
     }
-    if (m == d) break;
-    const float lx = sh.draft_logit[m];
-    // an empty row (top = -inf) accepts nothing
-    bool take;
-    if (greedy)
-      take = token >= 0 && sh.draft[m] == token;
-    else
-      take = lx != -INFINITY && sh.draft_bar[m] < ex2((lx - top) * c) / sum;
-    if (!take) break;
-    if (sa.logprob && rank == 0 && tid == 0)
-      sa.logprob[(int64_t)b * (d + 1) + m] = (lx - top) / T - logf(sum);
+    float tops = st.m;
+    uint32_t sums = __float_as_uint(st.s);
+    cluster_join(sh, tops, sums, rank, n, log_g, turn, StatOp{c});
+    if (m0 == 0) {
+      greedy = !(sh.temperature > 0.f);
+      T = greedy ? 1.f : sh.temperature;
+      c = fminf(fmaxf(LOG2E / T, FLT_MIN), FLT_MAX);
+    }
+    uint32_t firsts = INT32_MAX;
+    if (greedy) {
+      const float own = __shfl_sync(0xffffffffu, tops, (rank >> (log_n - log_g)) * (32 >> log_g));
+      if (own != -INFINITY) firsts = (uint32_t)row_first<DTYPE>(sl, row, st, own);
+      float unused = 0.f;
+      cluster_join(sh, unused, firsts, rank, n, log_g, turn, MinOp{});
+    }
+    for (uint32_t g = 0; g < G && !done; ++g) {
+      top = __shfl_sync(0xffffffffu, tops, g * (32 >> log_g));
+      sum = __uint_as_float(__shfl_sync(0xffffffffu, sums, g * (32 >> log_g)));
+      first = __shfl_sync(0xffffffffu, firsts, g * (32 >> log_g));
+      const float lx = m < d ? sh.draft_logit[m] : -INFINITY;
+      // (an empty row accepts nothing: lx is -inf too)
+      const bool take = greedy ? m < d && first != INT32_MAX && sh.draft[m] == (int32_t)first
+                               : lx != -INFINITY && sh.draft_bar[m] < ex2((lx - top) * c) / sum;
+      if (take) {
+        if (sa.logprob && rank == 0 && tid == 0)
+          sa.logprob[(int64_t)b * (d + 1) + m] = (lx - top) / T - logf(sum);
+        ++m;
+      } else {
+        done = true;
+      }
+    }
   }
 
   const char *row = rows + m * row_bytes;
-  if (!greedy && top != -INFINITY) {
+  int32_t token = -1;
+  if (greedy) {
+    token = first == INT32_MAX ? -1 : (int32_t)first;
+  } else if (top != -INFINITY) {
     const float inv = 1.f / sum;
     const float *E = sa.noise + (int64_t)b * V;
     const float *q = sa.probs && m < d ? sa.probs + ((int64_t)b * d + m) * V : nullptr;
     int32_t barred = !sa.probs && m < d ? sh.draft[m] : -1;   // a sure draft's own token
-    const int32_t lo = (int32_t)((int64_t)V * rank / n), hi = (int32_t)((int64_t)V * (rank + 1) / n);
-    uint32_t winner;
-    for (int again = 0; again < 2; ++again) {
-      float best = -1.f;
-      winner = INT32_MAX;
-      for (int32_t v0 = lo + tid; v0 < hi; v0 += NB * NT) {
-        float x[NB], e[NB], w[NB];
-#pragma unroll
-        for (int u = 0; u < NB; ++u) {
-          const int32_t v = v0 + u * NT;
-          x[u] = -INFINITY;
-          e[u] = 1.f;
-          w[u] = 0.f;
-          if (v < hi) {
-            x[u] = logit_at<DTYPE>(row, v);
-            e[u] = __ldcs(E + v);
-            if (q) w[u] = __ldcs(q + v);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < NB; ++u) {
-          const int32_t v = v0 + u * NT;
-          const float p = ex2((x[u] - top) * c) * inv - w[u];
-          const float r = p / e[u];
-          if (p > 0.f && v != barred && r > best) {    // a thread's indices ascend: the lowest stays
-            best = r;
-            winner = (uint32_t)v;
-          }
-        }
+    for (;;) {
+      Race ra = sa.aligned ? race<DTYPE, true>(row, q, E, V, rank, log_n, top, c, inv, barred, ring)
+                           : race<DTYPE, false>(row, q, E, V, rank, log_n, top, c, inv, barred, ring);
+      cluster_join(sh, ra.best, ra.at, rank, n, 0, turn, BestOp{});
+      if (ra.at != INT32_MAX) {
+        token = (int32_t)ra.at;
+        break;
       }
-      cluster_join(sh, best, winner, n, turn, [](float &av, uint32_t &ai, float bv, uint32_t bi) {
-        if (bv > av || (bv == av && bi < ai)) {
-          av = bv;
-          ai = bi;
-        }
-      });
+      if (!q && barred < 0) break;
       // nothing left of the target past the draft's probabilities (they are
       // equal, up to rounding): the target's own
-      if (winner != INT32_MAX || (!q && barred < 0)) break;
       q = nullptr;
       barred = -1;
     }
-    token = winner == INT32_MAX ? -1 : (int32_t)winner;
   }
 
   if (rank == 0) {
@@ -476,7 +708,6 @@ __global__ void __launch_bounds__(NT) k_verify_sample(const __grid_constant__ Sa
       for (int i = m + 1 + tid; i <= d; i += NT) sa.logprob[(int64_t)b * (d + 1) + i] = 0.f;
     if (COMMIT) commit_rows(b, m, ca);
   }
-  if (n > 1) cluster_sync();      // no block leaves while another may read its shared memory
 }
 
 int check_sample(const void *logits, int32_t dtype, int32_t B, int32_t d, int32_t V,
@@ -497,27 +728,49 @@ int check_sample(const void *logits, int32_t dtype, int32_t B, int32_t d, int32_
   return HS_OK;
 }
 
-// Blocks per request: enough to give every SM one, while a block's part of a
-// row stays at least 2048 values.
-int cluster_blocks(int32_t B, int32_t V, int *n) {
-  int dev = 0, sms = 0;
-  HS_CUDA_TRY(cudaGetDevice(&dev));
-  HS_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+// Blocks per request and rows side by side.
+//
+// A cluster that takes its rows one after the other reads no row behind the
+// refusal, but each row costs a few microseconds of latency (the first loads,
+// the joins). So while few blocks run, up to four rows are taken side by side
+// (2 x 3 drafts, V = 1024: 7.1 us against 10.5; 33 x 5, V = 50257: 16.0 against
+// 22.8); at half of the resident blocks two (64 x 3, V = 129280: 33.6 against
+// 36.9 for one and 35.2 for four); with the device full, one. The blocks
+// of a request grow while all of them fit at once and a part keeps 2048
+// values, and past that (a second wave of blocks evens out requests of
+// different lengths) while a part keeps 16384 (256 x 3, V = 129280: 91 us with
+// four blocks, 97 with two; V = 32000: 45 with four, 33 with two).
+int cluster_shape(int32_t B, int32_t d, int32_t V, int *n, int *g) {
+  int sms = 0;
+  int rc = hs_sm_count(&sms);
+  if (rc) return rc;
+  const int64_t at_once = (int64_t)sms * MIN_BLOCKS;
+  const int most = d >= 2 ? 4 : d + 1;           // rows side by side
   int k = 1;
-  while (k < MAX_CLUSTER && (int64_t)B * k < sms && V / (2 * k) >= 2048) k *= 2;
+  while (k < MAX_CLUSTER && (int64_t)B * 2 * k <= at_once && (k < most || (int64_t)V * most / (2 * k) >= 2048))
+    k *= 2;
+  while (k < MAX_CLUSTER && (int64_t)B * 2 * k <= 2 * at_once && V / (2 * k) >= 16384) k *= 2;
+  int r = (int64_t)B * k <= at_once / 2 ? most : (int64_t)B * k <= at_once ? 2 : 1;
+  if (r > most) r = most;
+  if (r > k) r = k;
   *n = k;
+  *g = r;
   return HS_OK;
 }
 
 template <bool COMMIT>
-int launch(const SampleArgs &sa, int32_t dtype, int32_t B, const CommitArgs &ca, cudaStream_t stream) {
-  int n = 1;
-  int rc = cluster_blocks(B, sa.V, &n);
+int launch(SampleArgs &sa, int32_t dtype, int32_t B, const CommitArgs &ca, cudaStream_t stream) {
+  int n = 1, g = 1;
+  int rc = cluster_shape(B, sa.d, sa.V, &n, &g);
   if (rc) return rc;
   if ((int64_t)B * n > INT32_MAX) return hs_set_error(HS_ERR_UNSUPPORTED, "B too large");
+  sa.log_rows = 31 - __builtin_clz((unsigned)g);
+  sa.aligned = sa.V % (dtype == HS_LOGITS_F32 ? 4 : 8) == 0 &&
+               (((uintptr_t)sa.logits | (uintptr_t)sa.probs | (uintptr_t)sa.noise) & 15) == 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * n));
   cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = RING_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -526,6 +779,16 @@ int launch(const SampleArgs &sa, int32_t dtype, int32_t B, const CommitArgs &ca,
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  int dev = 0;
+  HS_CUDA_TRY(cudaGetDevice(&dev));
+  static bool attr_done[64] = {false};
+  if (dev >= 64 || !attr_done[dev]) {
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_verify_sample<HS_LOGITS_F32, COMMIT>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES));
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_verify_sample<HS_LOGITS_BF16, COMMIT>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES));
+    if (dev < 64) attr_done[dev] = true;
+  }
   if (dtype == HS_LOGITS_F32)
     HS_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_verify_sample<HS_LOGITS_F32, COMMIT>, sa, ca));
   else
@@ -544,8 +807,8 @@ extern "C" int hs_verify_sample(const void *logits, int32_t logits_dtype, int32_
   int rc = check_sample(logits, logits_dtype, B, d, V, temperature, draft_tokens, draft_probs,
                         uniforms, noise, accept_len, next_token);
   if (rc) return rc;
-  const SampleArgs sa = {logits,   d,     V,          temperature, draft_tokens, draft_probs,
-                         uniforms, noise, accept_len, next_token,  logprob,      status};
+  SampleArgs sa = {logits,   d,     V,          temperature, draft_tokens, draft_probs,
+                         uniforms, noise, accept_len, next_token,  logprob,      status, 0, false};
   return launch<false>(sa, logits_dtype, B, CommitArgs{}, stream);
 }
 
@@ -574,7 +837,7 @@ extern "C" int hs_verify_sample_finalize(hs_buffer *buf, const void *logits, int
   if (cap != cudaStreamCaptureStatusNone)
     return hs_set_error(HS_ERR_UNSUPPORTED, "hs_verify_sample_finalize cannot be captured in a graph");
   buf->clock += 1;
-  const SampleArgs sa = {logits,   d,     V,          temperature, draft_tokens, draft_probs,
-                         uniforms, noise, accept_len, next_token,  logprob,      buf->status};
+  SampleArgs sa = {logits,   d,     V,          temperature, draft_tokens, draft_probs,
+                         uniforms, noise, accept_len, next_token,  logprob,      buf->status, 0, false};
   return launch<true>(sa, logits_dtype, B, commit_args(buf, d, step_kv, req_ids, kv_len), stream);
 }
