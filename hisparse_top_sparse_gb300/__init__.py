@@ -130,7 +130,7 @@ def _check(rc: int, what: str) -> None:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -521,55 +521,84 @@ def hs_backup_indexer(src_caches, dst_caches, src_slots, host_slots, positions,
         "hs_backup_indexer")
 
 
+# The calls below take microseconds, and so must their checks: one test of all
+# that is wanted of a tensor, and the reasons only once it has failed. Every
+# CUDA tensor must be on the current device, where the call launches.
+
+def _on(t, name, dtype, shape, cur, none=False):
+    """Pointer of a contiguous CUDA tensor of the current device."""
+    if t is None and none:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == cur and t.is_contiguous() and \
+                (shape is None or t.shape == shape):
+            return t.data_ptr() if t.numel() > 0 else None
+    except AttributeError:
+        pass
+    p = _ptr(t, name, dtype, shape)
+    if t.get_device() != cur:
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{cur}")
+    return p
+
+
+def _on_stream(stream, cur):
+    return torch._C._cuda_getCurrentRawStream(cur) if stream is None else _stream(stream)
+
+
 # ------------------------------------------------- quantised latent rows --
 
-def _on_current_device(**tensors) -> None:
-    """Every CUDA tensor given must be on the current device: the call launches
-    there, on that device's current stream."""
-    cur = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != cur:
-            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{cur}")
+def _device() -> int:
+    """The current CUDA device; -2 where there is none (no tensor's device)."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
 
 
-def _host_or_device(t, name) -> None:
+def _host_or_device(t, name, cur) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda and not t.is_pinned():
-        raise ValueError(f"{name} must be a CUDA tensor or pinned host memory")
+    if t.get_device() != cur:
+        if t.is_cuda:
+            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{cur}")
+        if cur < 0 or not t.is_pinned():
+            raise ValueError(f"{name} must be a CUDA tensor or pinned host memory")
 
 
-def _q8_cache(t, name) -> int:
-    _host_or_device(t, name)
-    if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[1] != Q8_ROW_BYTES or \
+def _q8_cache(t, name, cur) -> int:
+    _host_or_device(t, name, cur)
+    if t.dtype is not torch.uint8 or t.dim() != 2 or t.shape[1] != Q8_ROW_BYTES or \
             not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous uint8 [rows][{Q8_ROW_BYTES}] tensor")
     return t.data_ptr()
 
 
-def _wide_rows(t, name):
+_WIDE = {torch.float32: HS_LOGITS_F32, torch.bfloat16: HS_LOGITS_BF16}
+
+
+def _wide_rows(t, name, cur):
     """(pointer, dtype code, row stride) of bf16 / f32 rows of 576 values, the
     rows any distance apart."""
-    _host_or_device(t, name)
-    if t.dim() != 2 or t.shape[1] != LATENT_DIM or (t.shape[0] > 0 and t.stride(1) != 1):
+    _host_or_device(t, name, cur)
+    n = t.shape[0] if t.dim() == 2 else 0
+    if t.dim() != 2 or t.shape[1] != LATENT_DIM or (n > 0 and t.stride(1) != 1):
         raise ValueError(f"{name} must be [rows][{LATENT_DIM}] with contiguous rows")
-    if t.dtype == torch.float32:
-        dt = HS_LOGITS_F32
-    elif t.dtype == torch.bfloat16:
-        dt = HS_LOGITS_BF16
-    else:
+    if t.dtype not in _WIDE:
         raise TypeError(f"{name} must be float32 or bfloat16")
-    return t.data_ptr(), dt, t.stride(0) if t.shape[0] > 1 else LATENT_DIM
+    return t.data_ptr(), _WIDE[t.dtype], t.stride(0) if n > 1 else LATENT_DIM
 
 
 def _slots(src_slots, dst_slots, src_rows, dst_rows) -> int:
     """Entries of a row call: the slot lists' length, else every source row
     (which the destination must hold)."""
-    given = [t for t in (src_slots, dst_slots) if t is not None]
-    for t in given:
-        if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape != given[0].shape:
-            raise ValueError("src_slots and dst_slots must be int32 [n] tensors of one length")
-    n = given[0].shape[0] if given else src_rows
+    n = -1
+    for t in (src_slots, dst_slots):
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or t.dim() != 1 or n not in (-1, t.shape[0]):
+                raise ValueError("src_slots and dst_slots must be int32 [n] tensors of one length")
+            n = t.shape[0]
+    if n < 0:
+        n = src_rows
     if (src_slots is None and n > src_rows) or (dst_slots is None and n > dst_rows):
         raise ValueError(f"{n} entries do not fit {src_rows} source / {dst_rows} destination rows")
     return n
@@ -579,32 +608,30 @@ def hs_quant_rows(src, cache, src_slots=None, dst_slots=None, status=None, strea
     """Row dst_slots[i] of the q8 cache (uint8 [rows][656]) = row src_slots[i]
     of src (bf16 / f32 [rows][576]), quantised; without a list entry i is row
     i, negative slots are skipped."""
-    sp, dt, stride = _wide_rows(src, "src")
-    dp = _q8_cache(cache, "cache")
+    cur = _device()
+    sp, dt, stride = _wide_rows(src, "src", cur)
+    dp = _q8_cache(cache, "cache", cur)
     n = _slots(src_slots, dst_slots, src.shape[0], cache.shape[0])
-    _on_current_device(src=src, cache=cache, src_slots=src_slots, dst_slots=dst_slots,
-                       status=status)
     _check(lib().hs_quant_rows(
         sp, dt, stride, src.shape[0], dp, cache.shape[0],
-        _ptr(src_slots, "src_slots", torch.int32, allow_none=True),
-        _ptr(dst_slots, "dst_slots", torch.int32, allow_none=True), n,
-        _ptr(status, "status", torch.int32, (1,), allow_none=True), _stream(stream)),
+        _on(src_slots, "src_slots", torch.int32, None, cur, True),
+        _on(dst_slots, "dst_slots", torch.int32, None, cur, True), n,
+        _on(status, "status", torch.int32, (1,), cur, True), _on_stream(stream, cur)),
         "hs_quant_rows")
 
 
 def hs_dequant_rows(cache, dst, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
     """Row dst_slots[i] of dst (bf16 / f32 [rows][576]) = the values of row
     src_slots[i] of the q8 cache."""
-    sp = _q8_cache(cache, "cache")
-    dp, dt, stride = _wide_rows(dst, "dst")
+    cur = _device()
+    sp = _q8_cache(cache, "cache", cur)
+    dp, dt, stride = _wide_rows(dst, "dst", cur)
     n = _slots(src_slots, dst_slots, cache.shape[0], dst.shape[0])
-    _on_current_device(cache=cache, dst=dst, src_slots=src_slots, dst_slots=dst_slots,
-                       status=status)
     _check(lib().hs_dequant_rows(
         sp, cache.shape[0], dp, dt, stride, dst.shape[0],
-        _ptr(src_slots, "src_slots", torch.int32, allow_none=True),
-        _ptr(dst_slots, "dst_slots", torch.int32, allow_none=True), n,
-        _ptr(status, "status", torch.int32, (1,), allow_none=True), _stream(stream)),
+        _on(src_slots, "src_slots", torch.int32, None, cur, True),
+        _on(dst_slots, "dst_slots", torch.int32, None, cur, True), n,
+        _on(status, "status", torch.int32, (1,), cur, True), _on_stream(stream, cur)),
         "hs_dequant_rows")
 
 
@@ -621,42 +648,37 @@ def hs_sparse_attn_decode_q8(q, kv, idx, scale: float, out, lse=None, workspace=
     if idx.dim() != 2:
         raise ValueError("idx must be [R][K]")
     K = idx.shape[1]
-    _on_current_device(q=q, kv=kv, idx=idx, out=out, lse=lse, workspace=workspace, status=status)
+    cur = _device()
     _check(lib().hs_sparse_attn_decode_q8(
-        _ptr(q, "q", torch.bfloat16), _ptr(kv, "kv", torch.uint8), kv.shape[0],
-        _ptr(idx, "idx", torch.int32, (R, K)), R, H, K, float(scale),
-        _ptr(out, "out", torch.bfloat16, (R, H, VALUE_DIM)),
-        _ptr(lse, "lse", torch.float32, (R, H), allow_none=True),
-        _ptr(workspace, "workspace", torch.uint8, allow_none=True),
+        _on(q, "q", torch.bfloat16, None, cur), _on(kv, "kv", torch.uint8, None, cur), kv.shape[0],
+        _on(idx, "idx", torch.int32, (R, K), cur), R, H, K, float(scale),
+        _on(out, "out", torch.bfloat16, (R, H, VALUE_DIM), cur),
+        _on(lse, "lse", torch.float32, (R, H), cur, True),
+        _on(workspace, "workspace", torch.uint8, None, cur, True),
         workspace.numel() if workspace is not None else 0,
-        _ptr(status, "status", torch.int32, (1,), allow_none=True),
-        _stream(stream)), "hs_sparse_attn_decode_q8")
+        _on(status, "status", torch.int32, (1,), cur, True), _on_stream(stream, cur)),
+        "hs_sparse_attn_decode_q8")
 
 
 # --------------------------------------------- verification by sampling --
 
-def _sample_args(logits, temperature, draft_tokens, draft_probs, uniforms, noise, accept_len,
+def _sample_args(cur, logits, temperature, draft_tokens, draft_probs, uniforms, noise, accept_len,
                  next_token, logprob):
     """The C arguments shared by the two calls, checked."""
     B, d1, V = logits.shape
     d = d1 - 1
-    if logits.dtype == torch.float32:
-        dt = HS_LOGITS_F32
-    elif logits.dtype == torch.bfloat16:
-        dt = HS_LOGITS_BF16
-    else:
+    if logits.dtype not in _WIDE:
         raise TypeError("logits must be float32 or bfloat16")
-    _on_current_device(logits=logits, temperature=temperature, draft_tokens=draft_tokens,
-                       draft_probs=draft_probs, uniforms=uniforms, noise=noise,
-                       accept_len=accept_len, next_token=next_token, logprob=logprob)
     f32, i32 = torch.float32, torch.int32
-    head = (_ptr(logits, "logits"), dt, B, d, V, _ptr(temperature, "temperature", f32, (B,)),
-            _ptr(draft_tokens, "draft_tokens", i32, (B, d), allow_none=(d == 0)),
-            _ptr(draft_probs, "draft_probs", f32, (B, d, V), allow_none=True),
-            _ptr(uniforms, "uniforms", f32, (B, d), allow_none=(d == 0)),
-            _ptr(noise, "noise", f32, (B, V)))
-    tail = (_ptr(accept_len, "accept_len", i32, (B,)), _ptr(next_token, "next_token", i32, (B,)),
-            _ptr(logprob, "logprob", f32, (B, d1), allow_none=True))
+    head = (_on(logits, "logits", logits.dtype, None, cur), _WIDE[logits.dtype], B, d, V,
+            _on(temperature, "temperature", f32, (B,), cur),
+            _on(draft_tokens, "draft_tokens", i32, (B, d), cur, d == 0),
+            _on(draft_probs, "draft_probs", f32, (B, d, V), cur, True),
+            _on(uniforms, "uniforms", f32, (B, d), cur, d == 0),
+            _on(noise, "noise", f32, (B, V), cur))
+    tail = (_on(accept_len, "accept_len", i32, (B,), cur),
+            _on(next_token, "next_token", i32, (B,), cur),
+            _on(logprob, "logprob", f32, (B, d1), cur, True))
     return head, tail
 
 
@@ -665,24 +687,24 @@ def hs_verify_sample(logits, temperature, draft_tokens, draft_probs, uniforms, n
     """Drafts accepted against the target's probabilities with given random
     numbers (temperature 0: greedily); draft_probs None: the drafts were
     chosen outright. See include/hisparse.h."""
-    head, tail = _sample_args(logits, temperature, draft_tokens, draft_probs, uniforms, noise,
+    cur = _device()
+    head, tail = _sample_args(cur, logits, temperature, draft_tokens, draft_probs, uniforms, noise,
                               accept_len, next_token, logprob)
-    _on_current_device(status=status)
     _check(lib().hs_verify_sample(
-        *head, *tail, _ptr(status, "status", torch.int32, (1,), allow_none=True),
-        _stream(stream)), "hs_verify_sample")
+        *head, *tail, _on(status, "status", torch.int32, (1,), cur, True),
+        _on_stream(stream, cur)), "hs_verify_sample")
 
 
 def hs_verify_sample_finalize(buf: HsBuffer, logits, temperature, draft_tokens, draft_probs,
                               uniforms, noise, step_kv, kv_len, accept_len, next_token,
                               logprob=None, req_ids=None, stream=None) -> None:
     """hs_verify_sample and the commit of the accepted prefix's KV."""
-    head, tail = _sample_args(logits, temperature, draft_tokens, draft_probs, uniforms, noise,
+    cur = _device()
+    head, tail = _sample_args(cur, logits, temperature, draft_tokens, draft_probs, uniforms, noise,
                               accept_len, next_token, logprob)
     B, d1, _ = logits.shape
-    _on_current_device(step_kv=step_kv, req_ids=req_ids, kv_len=kv_len)
     _check(lib().hs_verify_sample_finalize(
-        buf.handle, *head, _ptr(step_kv, "step_kv", torch.bfloat16, (B, d1, LATENT_DIM)),
-        _ptr(req_ids, "req_ids", torch.int32, (B,), allow_none=True),
-        _ptr(kv_len, "kv_len", torch.int32, (buf.max_reqs,)), *tail, _stream(stream)),
-        "hs_verify_sample_finalize")
+        buf.handle, *head, _on(step_kv, "step_kv", torch.bfloat16, (B, d1, LATENT_DIM), cur),
+        _on(req_ids, "req_ids", torch.int32, (B,), cur, True),
+        _on(kv_len, "kv_len", torch.int32, (buf.max_reqs,), cur), *tail,
+        _on_stream(stream, cur)), "hs_verify_sample_finalize")
