@@ -52,6 +52,19 @@
 // distributed shared memory about half a microsecond after the CTA's own P
 // of the same pair, and an own tile queued behind it would hold its ring
 // slots that much longer.
+// k_attn_pair<true> reads q8 rows (hs_q8.cuh). Its products, softmax and
+// exchange are the same, over the same bf16 tiles: their values are exact in
+// bf16, so the output is bit for bit that of the bf16 kernel over the rows read
+// back. Four more warps and different rings bring the rows in: they land raw,
+// 656 bytes instead of 1152, and are decoded into the slots. Measured, 128 rows
+// x 128 heads x 2048 keys: 96.5 us, a tile pair per 1.25 us against 1.0 in the
+// bf16 kernel (84 us; with rows that need no gathering or decoding the rest
+// takes 77). A slot of ring VO is held from the decoding (0.5 us) through Q K^T,
+// softmax and its P V, about 2.9 pairs, and three fit beside the raw rings.
+// Rows decoded by the gather warps of both kinds of tile in turn: 124 us;
+// rows loaded into registers one tile ahead: 112, two ahead: 137.
+// Few rows: the keys of a row are split over clusters (parts of whole tiles,
+// each a row of its own to the kernel) and k_attn_join joins the parts.
 // The kernel is a programmatic dependent launch: its prologue (barriers, TMEM,
 // Q) overlaps the previous kernel (hs_resolve_topk releases it at entry), and
 // it reads the indices and request flags after griddepcontrol.wait.
@@ -76,7 +89,9 @@ constexpr int QT_DIMS = 384;              // Q dims held in TMEM
 constexpr int QS_BLOCKS = (D - QT_DIMS) / 64;   // 3 swizzle blocks of Q in SMEM
 constexpr int NSB = 2;                    // S / P buffers (own tiles)
 constexpr int VB_BLOCKS = 4;              // swizzle blocks of one value half
-constexpr int RA_SLOTS = 3, VO_SLOTS = 4, VP_SLOTS = 2, XP_SLOTS = 1;
+constexpr int XP_SLOTS = 1;
+constexpr int RAWO_SLOTS = 1, RAWH_SLOTS = 2;
+constexpr int MAX_RA = 3, MAX_VO = 4, MAX_VP = 2;          // of both kernels, for the barriers
 constexpr int PEER_LAG = 2;               // own tiles gathered ahead of the peer tiles
 constexpr int THREADS = 480;
 // Registers per thread, at most: a swap-in gather block (256 threads, 56
@@ -86,11 +101,14 @@ constexpr int THREADS = 480;
 // attention. 4 x 96 x 32 + 2 x 56 x 32 = 15,872; at 98 (rounded to 104) it
 // no longer fits and the copies wait for whole SMs.
 #define ATTN_MAX_REGS 96
-// The q8 kernel runs beside no copies: as many as the register file gives
-// 15 warps, for the rows that its gather warps hold in registers.
-#define Q8_MAX_REGS 128
-static_assert(THREADS * ATTN_MAX_REGS <= 65536 && THREADS * Q8_MAX_REGS <= 65536, "register budget");
+// The q8 kernel's 19 warps: five of them share a quarter of the register file
+// (5 x 96 x 32 = 15,360 of 16,384; 104 would not fit).
+#define Q8_MAX_REGS 96
+static_assert(THREADS * ATTN_MAX_REGS <= 65536, "register budget");
 constexpr int NPROD = 256;
+constexpr int Q8_HALF = 128;                                // threads decoding peer tiles' halves
+constexpr int Q8_THREADS = THREADS + Q8_HALF;
+static_assert((Q8_THREADS / 32 + 3) / 4 * 32 * Q8_MAX_REGS <= 16384, "register budget");
 constexpr float REF_SLACK = 30.0f;        // P <= 2^30 on the shared reference
 
 // shared memory (offsets from a 1024-byte aligned base)
@@ -99,24 +117,58 @@ constexpr int QS_OFF = 0;
 constexpr int QS_BYTES = QS_BLOCKS * HG * 128;              // 49152
 constexpr int RA_SLOT_BYTES = (D / 64 - VB_BLOCKS) * KV_BLOCK_BYTES;   // 20480
 constexpr int V_SLOT_BYTES = VB_BLOCKS * KV_BLOCK_BYTES;              // 16384
+constexpr int RAWO_BYTES = NK * HS_Q8_ROW_BYTES;            // 20992: a q8 tile's rows
+constexpr int RAWH_BYTES = NK * (DV / 2 + 16);              // 8704: half the codes, the exponents
 constexpr int P_SLOT_BYTES = HG * NK * 2;                   // 8192: 128 rows x 64 B, 64-byte swizzle
 constexpr int RA_OFF = QS_OFF + QS_BYTES;
-constexpr int VO_OFF = RA_OFF + RA_SLOTS * RA_SLOT_BYTES;
-constexpr int XS_OFF = VO_OFF + VO_SLOTS * V_SLOT_BYTES;    // own P staged for the bulk copy
-constexpr int XP_OFF = XS_OFF + XP_SLOTS * P_SLOT_BYTES;    // the peer's P
-constexpr int VP_OFF = XP_OFF + XP_SLOTS * P_SLOT_BYTES;
-constexpr int XMAX_OFF = VP_OFF + VP_SLOTS * V_SLOT_BYTES;  // peer's first-tile maxima
-constexpr int XEND_OFF = XMAX_OFF + HG * 4;                 // peer's (l or mark, max) per pass
-constexpr int BAR_OFF = XEND_OFF + 2 * HG * 8;
-constexpr int SMEM_USED = BAR_OFF + 512;
-// 1 KB of slack to align the base to 1024 bytes (the 128-byte swizzled tiles
-// need it) at run time; declaring the alignment instead gave slower code. The
-// SM keeps 3 KB of shared memory beside one CTA for a small kernel (the
-// swap-in gather).
-constexpr int SMEM_ALLOC = SMEM_USED + 1024;
-static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
-static_assert(RA_OFF % 1024 == 0 && VO_OFF % 1024 == 0 && VP_OFF % 1024 == 0 &&
-                  XS_OFF % 1024 == 0 && XP_OFF % 1024 == 0, "slot alignment");
+// Ring slots, and where everything lies. The q8 kernel's rows land in raw
+// rings first (its slots are taken only once a row is decoded, about a
+// microsecond later), which its rings A and VO make room for.
+template <bool Q8>
+struct Lay {
+  static constexpr int RA_SLOTS = Q8 ? 2 : 3, VO_SLOTS = Q8 ? 3 : 4, VP_SLOTS = 2;
+  static constexpr int VO_OFF = RA_OFF + RA_SLOTS * RA_SLOT_BYTES;
+  static constexpr int XS_OFF = VO_OFF + VO_SLOTS * V_SLOT_BYTES;    // own P staged for the bulk copy
+  static constexpr int XP_OFF = XS_OFF + XP_SLOTS * P_SLOT_BYTES;    // the peer's P
+  static constexpr int VP_OFF = XP_OFF + XP_SLOTS * P_SLOT_BYTES;
+  static constexpr int RAWO_OFF = VP_OFF + VP_SLOTS * V_SLOT_BYTES;  // raw rows of own tiles
+  static constexpr int RAWH_OFF = RAWO_OFF + (Q8 ? RAWO_SLOTS * RAWO_BYTES : 0);   // raw halves
+  static constexpr int XMAX_OFF = RAWH_OFF + (Q8 ? RAWH_SLOTS * RAWH_BYTES : 0);   // peer's first-tile maxima
+  static constexpr int XEND_OFF = XMAX_OFF + HG * 4;                 // peer's (l or mark, max) per pass
+  static constexpr int BAR_OFF = XEND_OFF + 2 * HG * 8;
+  static constexpr int SMEM_USED = BAR_OFF + 512;
+  // 1 KB of slack to align the base to 1024 bytes (the 128-byte swizzled tiles
+  // need it) at run time; declaring the alignment instead gave slower code.
+  // Beside the bf16 kernel the SM keeps 3 KB of shared memory for a small
+  // kernel (the swap-in gather).
+  static constexpr int SMEM_ALLOC = SMEM_USED + 1024;
+  static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+  static_assert(RA_OFF % 1024 == 0 && VO_OFF % 1024 == 0 && VP_OFF % 1024 == 0 &&
+                    XS_OFF % 1024 == 0 && XP_OFF % 1024 == 0 && RAWO_OFF % 1024 == 0 &&
+                    XMAX_OFF % 16 == 0, "slot alignment");
+  // Staging place of Q block a (dims 64a..64a+63, a < 6) before it moves into
+  // TMEM, outside the slots of the first tiles, which are gathered meanwhile:
+  // ring A behind slot 0 (bf16: two blocks in its two slots, q8: one), ring VO
+  // behind slot 0, the P buffers (the sixth block of bf16), and for q8 ring VP
+  // behind slot 0 and the raw ring of own tiles.
+  __host__ __device__ static constexpr uint32_t q_stage_off(int a) {
+    constexpr int BLK = HG * 128, in_a = (RA_SLOTS - 1) * RA_SLOT_BYTES / BLK;
+    if (a < in_a) return RA_OFF + RA_SLOT_BYTES + a * BLK;
+    a -= in_a;
+    if (a < VO_SLOTS - 1) return VO_OFF + (a + 1) * BLK;
+    a -= VO_SLOTS - 1;
+    if (a < XP_SLOTS) return XS_OFF + a * BLK;
+    a -= XP_SLOTS;
+    if (a < VP_SLOTS - 1) return VP_OFF + (a + 1) * BLK;
+    a -= VP_SLOTS - 1;
+    return RAWO_OFF + a * BLK;
+  }
+  static_assert(q_stage_off(0) % 1024 == 0 && q_stage_off(1) % 1024 == 0 && q_stage_off(2) % 1024 == 0 &&
+                    q_stage_off(3) % 1024 == 0 && q_stage_off(4) % 1024 == 0 &&
+                    q_stage_off(5) % 1024 == 0 && q_stage_off(5) + HG * 128 <= XMAX_OFF &&
+                    V_SLOT_BYTES == HG * 128 && 2 * P_SLOT_BYTES == HG * 128,
+                "Q staging map");
+};
 
 // TMEM columns
 constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 448;
@@ -125,11 +177,11 @@ static_assert(COL_Q + QT_DIMS / 2 == COL_S && COL_S + NSB * NK == 512, "TMEM col
 // barriers (8-byte words at BAR_OFF)
 enum {
   B_FULLA = 0,                        // own tile landed (NPROD arrivals)
-  B_EMPTYA = B_FULLA + RA_SLOTS,      // ring A slot: Q K^T done
-  B_EMPTYVO = B_EMPTYA + RA_SLOTS,    // ring VO slot: own P V done
-  B_FULLVP = B_EMPTYVO + VO_SLOTS,    // peer tile's value half landed (NPROD arrivals)
-  B_EMPTYVP = B_FULLVP + VP_SLOTS,    // ring VP slot: P V done
-  B_SFULL = B_EMPTYVP + VP_SLOTS,     // S ready
+  B_EMPTYA = B_FULLA + MAX_RA,      // ring A slot: Q K^T done
+  B_EMPTYVO = B_EMPTYA + MAX_RA,    // ring VO slot: own P V done
+  B_FULLVP = B_EMPTYVO + MAX_VO,    // peer tile's value half landed (NPROD, or Q8_HALF, arrivals)
+  B_EMPTYVP = B_FULLVP + MAX_VP,    // ring VP slot: P V done
+  B_SFULL = B_EMPTYVP + MAX_VP,     // S ready
   B_SFREE = B_SFULL + NSB,            // own P V done with the S / P buffer
   B_PFULL = B_SFREE + NSB,            // P in TMEM (4 softmax warps)
   B_XPFULL = B_PFULL + NSB,           // the peer's P landed here (1 arrival + bytes)
@@ -147,7 +199,8 @@ static_assert(B_COUNT * 8 + 16 <= 512, "barrier area");
 // O staged for the epilogue's stores: four 16 KB blocks over ring A and the
 // start of ring VO (free once the last P V is done)
 constexpr int O_STG_OFF = RA_OFF;
-static_assert(O_STG_OFF + 4 * HG * 128 <= XS_OFF, "O staging");
+static_assert(O_STG_OFF + 8 * 32 * 272 <= Lay<true>::XS_OFF && O_STG_OFF + 4 * HG * 128 <= Lay<false>::XS_OFF &&
+                  O_STG_OFF + 4 * HG * 128 <= Lay<true>::XS_OFF, "O staging");
 
 constexpr int WAIT_LIMIT = 1 << 24;
 
@@ -159,21 +212,6 @@ __device__ __forceinline__ uint32_t kv_block(uint32_t ra, uint32_t rv, int c, in
   const int pa = (c == 0) ? a - 4 : (a == 8 ? 4 : a);
   return ra + (uint32_t)pa * KV_BLOCK_BYTES;
 }
-
-// Staging place of Q block a (dims 64a..64a+63, a < 6) before it moves into
-// TMEM: slots 1-2 of ring A (two blocks), slots 1-3 of ring VO (three
-// blocks), the two P buffers (one block). Slot 0 of rings A and VO and all of
-// ring VP are left for the first tiles, which are gathered meanwhile.
-__host__ __device__ constexpr uint32_t q_stage_off(int a) {
-  return a < 2 ? RA_OFF + RA_SLOT_BYTES + a * (HG * 128)
-               : a < 5 ? VO_OFF + V_SLOT_BYTES + (a - 2) * (HG * 128) : XS_OFF;
-}
-static_assert(q_stage_off(1) + HG * 128 <= RA_OFF + RA_SLOTS * RA_SLOT_BYTES &&
-                  q_stage_off(4) + HG * 128 == XS_OFF && XS_OFF + HG * 128 == VP_OFF &&
-                  q_stage_off(0) % 1024 == 0 && q_stage_off(1) % 1024 == 0 &&
-                  q_stage_off(2) % 1024 == 0 && q_stage_off(5) % 1024 == 0 && RA_SLOTS == 3 &&
-                  VO_SLOTS == 4 && XP_SLOTS == 1,
-              "Q staging map");
 
 __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk) {
   return row * 128 + ((chunk ^ (row & 7)) << 4);
@@ -294,6 +332,15 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, const uint4 v) {
                "r"(v.z), "r"(v.w)
                : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
@@ -441,12 +488,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
                 const int32_t *__restrict__ idx, int32_t H, int32_t K_row, float scale_log2,
                 __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, uint32_t *status,
                 const __grid_constant__ Parts parts) {
+  using L = Lay<Q8>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(sm);
-  const uint32_t bars = sbase + BAR_OFF;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + BAR_OFF + B_COUNT * 8);
+  const uint32_t bars = sbase + L::BAR_OFF;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::BAR_OFF + B_COUNT * 8);
   volatile uint32_t *s_redo = tmem_slot + 1;
   volatile uint32_t *s_last = tmem_slot + 2;   // the last pass run (0 or 1)
   volatile uint32_t *s_fail = tmem_slot + 3;   // a wait of warps 0-7 gave up
@@ -479,9 +527,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     static_assert(B_COUNT <= 32, "one lane per barrier");
     if (lane < B_COUNT) {
       const int i = lane;
-      const bool prod = (i >= B_FULLA && i < B_FULLA + RA_SLOTS) || (i >= B_FULLVP && i < B_FULLVP + VP_SLOTS);
+      const bool prod = i >= B_FULLA && i < B_FULLA + MAX_RA;
+      const bool half = i >= B_FULLVP && i < B_FULLVP + MAX_VP;
       const bool four = (i >= B_PFULL && i < B_PFULL + NSB) || i == B_VOTE;
-      bar_init(bar(i), prod ? NPROD : four ? 4 : 1);
+      bar_init(bar(i), prod ? NPROD : half ? (Q8 ? Q8_HALF : NPROD) : four ? 4 : 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (lane == 0) {
@@ -519,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     arrive_expect_tx(bar(B_QLOAD), 9 * HG * 128);
     for (int a = 0; a < D / 64; ++a) {
-      const uint32_t dst = a < 6 ? sbase + q_stage_off(a) : sbase + QS_OFF + (a - 6) * (HG * 128);
+      const uint32_t dst = a < 6 ? sbase + L::q_stage_off(a) : sbase + QS_OFF + (a - 6) * (HG * 128);
       asm volatile(
           "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
           " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
@@ -541,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
 #pragma unroll 1
       for (int kk = 0; kk < QT_DIMS / 16; ++kk)
         asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;\n" ::"r"(tmem + COL_Q + kk * 8),
-                     "l"(sdesc(sbase + q_stage_off(kk >> 2) + (kk & 3) * 32, 16, 1024))
+                     "l"(sdesc(sbase + L::q_stage_off(kk >> 2) + (kk & 3) * 32, 16, 1024))
                      : "memory");
       mma_commit(bar(B_QSTAGED));
     }
@@ -564,110 +613,163 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
   if (!req_ok && status && tid == 0 && c == 0) atomicOr(status, HS_STATUS_INDEX);
 
 
-  if (Q8 && warp >= 4 && warp < 12) {
+  if (Q8 && ((warp >= 4 && warp < 12) || warp > 12 + NSB)) {
     // ------------------------- gather producers, q8 rows made bf16 tiles ----
-    // The same steps and slots as the bf16 gather below, but a thread loads
-    // its part of a row into registers one step ahead, and then decodes it
-    // into the slot: thread `sub` of a key takes 16-code chunks sub + 8 k
-    // (scale byte sub / 2 of word k of the row's exponents), rope chunk sub,
-    // and of a peer tile the two code chunks in this CTA's value half.
-    const int p = tid - 128;
-    const int key = p >> 3;
-    const int sub = p & 7;
+    // Rows land in raw rings (cp.async), are read into registers, their places
+    // refilled at once, and decoded into a slot when it is free. (Loads
+    // straight into registers cannot run ahead: the L1 beside this kernel's
+    // shared memory holds only some 20 KB of loads in flight.) Warps 4-11 take
+    // the own tiles, eight threads per key, warps 15-18 the peer tiles' halves,
+    // four threads per key, so that neither waits behind the other's slots.
+    // A thread copies and decodes the same 16-byte chunks, in places of its
+    // own; the exponents are copied by a key's first thread and read by all,
+    // which are of one warp. Eight neighbouring threads take four chunks of
+    // two neighbouring keys: under the 128-byte swizzle their stores fall
+    // into different banks.
+    const bool own = warp < 12;
+    const int lw = own ? warp - 4 : warp - 15;
+    const int key = own ? 4 * lw + 2 * (lane >> 4) + ((lane >> 2) & 1) : 8 * lw + (lane >> 2);
+    const int sub = (lane & 3) + (own ? 4 * ((lane >> 3) & 1) : 0);
+    const int p = 32 * lw + lane;
     auto load_id = [&](int t) -> int32_t {
       const int j = t * NK + key;
       return (t < T && j < K) ? __ldg(idx_row + j) : -1;
     };
-    struct Chunks {
-      uint4 code[4], rope, scale;
-    };
-    auto load_row = [&](int t, int32_t id, Chunks &x) {
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x.code[k] = zero;
-      x.rope = x.scale = zero;
-      if (id < 0 || id >= n_kv) return;
-      const uint4 *row = reinterpret_cast<const uint4 *>(kv + (int64_t)id * HS_Q8_ROW_BYTES);
-      x.scale = __ldg(row + Q8_SCALE_OFF / 16);
-      if ((t & 1) == c) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x.code[k] = __ldg(row + sub + 8 * k);
-        x.rope = __ldg(row + Q8_ROPE_OFF / 16 + sub);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) x.code[k] = __ldg(row + 16 * c + sub + 8 * k);
-      }
-    };
-    // 16 codes into two chunks of a swizzled 64-dim block; the threads of the
-    // second half of a key write their upper chunk first, so that a quarter
-    // warp's eight stores fall into different banks
+    // 16 codes into two chunks of a swizzled 64-dim block
     auto put = [&](uint32_t block, const uint4 w, uint32_t byte) {
-      const float s = q8_scale(byte & 0xFFu);
+      const uint64_t s = q8_scale2(byte & 0xFFu);
       const uint2 a = q8_decode4_bf16(w.x, s), b = q8_decode4_bf16(w.y, s);
+      st_shared16(block + sw128(key, 2 * (sub & 3)), make_uint4(a.x, a.y, b.x, b.y));
       const uint2 d = q8_decode4_bf16(w.z, s), e = q8_decode4_bf16(w.w, s);
-      const bool up = sub >= 4;
-      const uint32_t j = 2 * (sub & 3);
-      st_shared16(block + sw128(key, j + up), up ? make_uint4(d.x, d.y, e.x, e.y)
-                                                 : make_uint4(a.x, a.y, b.x, b.y));
-      st_shared16(block + sw128(key, j + !up), up ? make_uint4(a.x, a.y, b.x, b.y)
-                                                  : make_uint4(d.x, d.y, e.x, e.y));
+      st_shared16(block + sw128(key, 2 * (sub & 3) + 1), make_uint4(d.x, d.y, e.x, e.y));
     };
-    int ig = 0, jg = 0;
-    for (int pass = 0; pass < 2 && !timed_out; ++pass) {
-      if (pass == 1) {
-        if (!bar_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
-        if (!*s_redo) break;
-      }
-      int la = 0, lb = 0;
-      auto step = [&](int &a, int &b) -> int {
-        if (a < n_own && (b >= n_peer || a < b + PEER_LAG + 1)) return 2 * (a++) + c;
-        if (b < n_peer) return 2 * (b++) + (1 - c);
-        return T;
+    const int sh = 8 * (sub >> 1);     // this thread's byte of a word of exponents
+    if (own) {
+      // chunks sub + 8 k: codes (block 2 k + sub / 4, exponent word k), rope
+      const uint32_t raw = sbase + L::RAWO_OFF;
+      auto copy = [&](int32_t id, int slot) {
+        const bool v = id >= 0 && id < n_kv;
+        const char *row = v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q;
+        const uint32_t to = raw + slot * RAWO_BYTES;
+#pragma unroll
+        for (int k = 0; k < 5; ++k) cp_async16(to + (k * NPROD + p) * 16, v ? row + (sub + 8 * k) * 16 : q, v);
+        if (sub == 0) cp_async16(to + 5 * NPROD * 16 + key * 16, v ? row + Q8_SCALE_OFF : q, v);
+        cp_async_commit();
       };
-      int t1 = step(la, lb), t2 = step(la, lb);
-      int32_t id2 = load_id(t2);
-      Chunks next;
-      load_row(t1, load_id(t1), next);
-      for (int i = 0; i < T; ++i) {
-        const int t = t1;
-        const Chunks x = next;
-        t1 = t2;
-        load_row(t1, id2, next);
-        t2 = step(la, lb);
-        id2 = load_id(t2);
-        const uint32_t sw[4] = {x.scale.x, x.scale.y, x.scale.z, x.scale.w};
-        const int sh = 8 * (sub >> 1);
-        if ((t & 1) == c) {
-          const int sa = ig % RA_SLOTS, so = ig % VO_SLOTS;
-          if ((ig == 1 && !bar_wait(bar(B_QSTAGED), 0)) ||
-              (ig >= RA_SLOTS && !bar_wait(bar(B_EMPTYA + sa), ((ig / RA_SLOTS) - 1) & 1)) ||
-              (ig >= VO_SLOTS && !bar_wait(bar(B_EMPTYVO + so), ((ig / VO_SLOTS) - 1) & 1))) {
+      int ig = 0;                      // own tiles taken, over both passes
+      for (int pass = 0; pass < 2 && !timed_out; ++pass) {
+        uint4 code[4], rope, scale;
+        int copied = 0;
+        if (pass == 0) {
+          // the first own tile comes straight into registers: the raw ring
+          // holds staged Q until it is in TMEM
+          const int32_t id = load_id(c);
+          const bool v = id >= 0 && id < n_kv;
+          const uint4 *row = reinterpret_cast<const uint4 *>(v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q);
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) code[k] = v ? __ldg(row + sub + 8 * k) : zero;
+          rope = v ? __ldg(row + Q8_ROPE_OFF / 16 + sub) : zero;
+          scale = v ? __ldg(row + Q8_SCALE_OFF / 16) : zero;
+          copied = 1;
+        } else {
+          if (!warp_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
+          if (!*s_redo) break;
+        }
+        int32_t id = load_id(2 * copied + c);
+        auto next = [&]() {            // past the last tile: a copy of zeros that nothing reads
+          copy(id, copied % RAWO_SLOTS);
+          ++copied;
+          id = load_id(2 * copied + c);
+        };
+        if (pass == 1)
+          for (int k = 0; k < RAWO_SLOTS; ++k) next();
+        for (int a = 0; a < n_own; ++a, ++ig) {
+          if (pass == 1 || a > 0) {
+            if (pass == 0 && a == 1) { // the raw ring and the other slots, once Q has left them
+              if (!warp_wait(bar(B_QSTAGED), 0)) { timed_out = true; break; }
+              for (int k = 0; k < RAWO_SLOTS; ++k) next();
+            }
+            cp_async_wait<RAWO_SLOTS - 1>();
+            __syncwarp();
+            const uint32_t from = raw + (a % RAWO_SLOTS) * RAWO_BYTES;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) code[k] = ld_shared16(from + (k * NPROD + p) * 16);
+            rope = ld_shared16(from + (4 * NPROD + p) * 16);
+            scale = ld_shared16(from + 5 * NPROD * 16 + key * 16);
+            __syncwarp();
+            next();
+          }
+          const int sa = ig % L::RA_SLOTS, so = ig % L::VO_SLOTS;
+          if ((ig >= L::RA_SLOTS && !warp_wait(bar(B_EMPTYA + sa), ((ig / L::RA_SLOTS) - 1) & 1)) ||
+              (ig >= L::VO_SLOTS && !warp_wait(bar(B_EMPTYVO + so), ((ig / L::VO_SLOTS) - 1) & 1))) {
             timed_out = true;
             break;
           }
           const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
-          const uint32_t rv = sbase + VO_OFF + so * V_SLOT_BYTES;
+          const uint32_t rv = sbase + L::VO_OFF + so * V_SLOT_BYTES;
+          const uint32_t sw[4] = {scale.x, scale.y, scale.z, scale.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            put(kv_block(ra, rv, c, 2 * k + (sub >> 2)), x.code[k], sw[k] >> sh);
-          st_shared16(kv_block(ra, rv, c, 8) + sw128(key, sub), x.rope);
+          for (int k = 0; k < 4; ++k) put(kv_block(ra, rv, c, 2 * k + (sub >> 2)), code[k], sw[k] >> sh);
+          st_shared16(kv_block(ra, rv, c, 8) + sw128(key, sub), rope);
           fence_proxy_async();
           bar_arrive(bar(B_FULLA + sa));
-          ++ig;
-        } else {
-          const int sp = jg % VP_SLOTS;
-          if (jg >= VP_SLOTS && !bar_wait(bar(B_EMPTYVP + sp), ((jg / VP_SLOTS) - 1) & 1)) {
+        }
+        cp_async_wait<0>();
+      }
+    } else {
+      // chunks sub + 4 k of the half's 16: block k of the slot, exponent word
+      // 2 c + k / 2, byte 2 (k & 1) + sub / 2
+      const uint32_t raw = sbase + L::RAWH_OFF;
+      auto copy = [&](int32_t id, int slot) {
+        const bool v = id >= 0 && id < n_kv;
+        const char *row = v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q;
+        const uint32_t to = raw + slot * RAWH_BYTES;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          cp_async16(to + (k * Q8_HALF + p) * 16, v ? row + (DV / 2) * c + (sub + 4 * k) * 16 : q, v);
+        if (sub == 0) cp_async16(to + 4 * Q8_HALF * 16 + key * 16, v ? row + Q8_SCALE_OFF : q, v);
+        cp_async_commit();
+      };
+      int jg = 0;                      // peer tiles taken, over both passes
+      if (!warp_wait(bar(B_QSTAGED), 0)) timed_out = true;
+      for (int pass = 0; pass < 2 && !timed_out; ++pass) {
+        if (pass == 1) {
+          if (!warp_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
+          if (!*s_redo) break;
+        }
+        int copied = 0;
+        int32_t id = load_id(1 - c);
+        auto next = [&]() {
+          copy(id, copied % RAWH_SLOTS);
+          ++copied;
+          id = load_id(2 * copied + 1 - c);
+        };
+        for (int k = 0; k < RAWH_SLOTS; ++k) next();
+        for (int b = 0; b < n_peer; ++b, ++jg) {
+          cp_async_wait<RAWH_SLOTS - 1>();
+          __syncwarp();
+          const uint32_t from = raw + (b % RAWH_SLOTS) * RAWH_BYTES;
+          uint4 code[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) code[k] = ld_shared16(from + (k * Q8_HALF + p) * 16);
+          const uint4 scale = ld_shared16(from + 4 * Q8_HALF * 16 + key * 16);
+          __syncwarp();
+          next();
+          const int sp = jg % L::VP_SLOTS;
+          if (jg >= L::VP_SLOTS && !warp_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
             timed_out = true;
             break;
           }
-          const uint32_t rv = sbase + VP_OFF + sp * V_SLOT_BYTES;
+          const uint32_t rv = sbase + L::VP_OFF + sp * V_SLOT_BYTES;
+          const uint32_t lo = c ? scale.z : scale.x, hi = c ? scale.w : scale.y;
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            put(rv + (2 * k + (sub >> 2)) * KV_BLOCK_BYTES, x.code[k], (c ? sw[2 + k] : sw[k]) >> sh);
+          for (int k = 0; k < 4; ++k)
+            put(rv + k * KV_BLOCK_BYTES, code[k], (k < 2 ? lo : hi) >> (16 * (k & 1) + sh));
           fence_proxy_async();
           bar_arrive(bar(B_FULLVP + sp));
-          ++jg;
         }
+        cp_async_wait<0>();
       }
     }
   } else if (warp >= 4 && warp < 12) {
@@ -706,22 +808,22 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
         const bool v = id >= 0 && id < n_kv;
         const char *src = kv + (v ? (int64_t)id * ROWB : 0);
         if ((t & 1) == c) {
-          const int sa = ig % RA_SLOTS, so = ig % VO_SLOTS;
+          const int sa = ig % L::RA_SLOTS, so = ig % L::VO_SLOTS;
           // slots 1 and 2 hold staged Q until it is in TMEM
           if (ig == 1 && !bar_wait(bar(B_QSTAGED), 0)) {
             timed_out = true;
             break;
           }
-          if (ig >= RA_SLOTS && !bar_wait(bar(B_EMPTYA + sa), ((ig / RA_SLOTS) - 1) & 1)) {
+          if (ig >= L::RA_SLOTS && !bar_wait(bar(B_EMPTYA + sa), ((ig / L::RA_SLOTS) - 1) & 1)) {
             timed_out = true;
             break;
           }
-          if (ig >= VO_SLOTS && !bar_wait(bar(B_EMPTYVO + so), ((ig / VO_SLOTS) - 1) & 1)) {
+          if (ig >= L::VO_SLOTS && !bar_wait(bar(B_EMPTYVO + so), ((ig / L::VO_SLOTS) - 1) & 1)) {
             timed_out = true;
             break;
           }
           const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
-          const uint32_t rv = sbase + VO_OFF + so * V_SLOT_BYTES;
+          const uint32_t rv = sbase + L::VO_OFF + so * V_SLOT_BYTES;
           // copy k of this thread is chunk sub + 4k: swizzle block k / 2,
           // chunk sub + 4 (k & 1) within the block's 128-byte row
 #pragma unroll
@@ -733,12 +835,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
                        : "memory");
           ++ig;
         } else {
-          const int sp = jg % VP_SLOTS;
-          if (jg >= VP_SLOTS && !bar_wait(bar(B_EMPTYVP + sp), ((jg / VP_SLOTS) - 1) & 1)) {
+          const int sp = jg % L::VP_SLOTS;
+          if (jg >= L::VP_SLOTS && !bar_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
             timed_out = true;
             break;
           }
-          const uint32_t rv = sbase + VP_OFF + sp * V_SLOT_BYTES;
+          const uint32_t rv = sbase + L::VP_OFF + sp * V_SLOT_BYTES;
           // only this CTA's value half: copies k = 8c .. 8c + 7 of the 18
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -768,14 +870,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
         for (int il = 0; il < n_own && ok; ++il) {
           const int ig = pass * n_own + il;
           if (ig % NSB != b) continue;
-          const int sa = ig % RA_SLOTS;
-          ok = warp_wait(bar(B_FULLA + sa), (ig / RA_SLOTS) & 1);
+          const int sa = ig % L::RA_SLOTS;
+          ok = warp_wait(bar(B_FULLA + sa), (ig / L::RA_SLOTS) & 1);
           if (ok && ig >= NSB) ok = warp_wait(bar(B_SFREE + b), ((ig / NSB) - 1) & 1);
           if (!ok) break;
           fence_after();
-          fence_proxy_async();   // the tile was written by cp.async (generic proxy)
+          if (!Q8) fence_proxy_async();   // the tile was written by cp.async (generic proxy)
+                                          // (the q8 producers fence their own stores)
           const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
-          const uint32_t rv = sbase + VO_OFF + (ig % VO_SLOTS) * V_SLOT_BYTES;
+          const uint32_t rv = sbase + L::VO_OFF + (ig % L::VO_SLOTS) * V_SLOT_BYTES;
           const uint32_t sd = tmem + COL_S + b * NK;
           if (elect_one()) {
 #pragma unroll
@@ -811,11 +914,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
         for (int i = 0; i < T && ok; ++i) {
           const int t = tile_at(i);
           if ((t & 1) == c) {
-            const int sb = ig % NSB, so = ig % VO_SLOTS;
+            const int sb = ig % NSB, so = ig % L::VO_SLOTS;
             ok = warp_wait(bar(B_PFULL + sb), (ig / NSB) & 1);
             if (!ok) break;
             fence_after();
-            const uint32_t vb = sbase + VO_OFF + so * V_SLOT_BYTES;
+            const uint32_t vb = sbase + L::VO_OFF + so * V_SLOT_BYTES;
             if (elect_one()) {
 #pragma unroll
               for (int ks = 0; ks < NK / 16; ++ks)
@@ -827,8 +930,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
             __syncwarp();
             ++ig;
           } else {
-            const int sp = jg % VP_SLOTS, xs = jg % XP_SLOTS;
-            ok = warp_wait(bar(B_FULLVP + sp), (jg / VP_SLOTS) & 1);
+            const int sp = jg % L::VP_SLOTS, xs = jg % XP_SLOTS;
+            ok = warp_wait(bar(B_FULLVP + sp), (jg / L::VP_SLOTS) & 1);
             if (ok) {
               if (lane == 0) arrive_expect_tx(bar(B_XPFULL + xs), HG * 64);
               __syncwarp();
@@ -836,12 +939,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
             }
             if (!ok) break;
             fence_after();
-            fence_proxy_async();   // V by cp.async, P by a bulk copy
-            const uint32_t vb = sbase + VP_OFF + sp * V_SLOT_BYTES;
+            if (!Q8) fence_proxy_async();   // V by cp.async, P by a bulk copy (V fenced by its
+                                            // producers: q8)
+            const uint32_t vb = sbase + L::VP_OFF + sp * V_SLOT_BYTES;
             if (elect_one()) {
 #pragma unroll
               for (int ks = 0; ks < NK / 16; ++ks)
-                mma_ss(tmem + COL_O, sdesc64(sbase + XP_OFF + xs * P_SLOT_BYTES + ks * 32),
+                mma_ss(tmem + COL_O, sdesc64(sbase + L::XP_OFF + xs * P_SLOT_BYTES + ks * 32),
                        sdesc(vb + ks * 2048, KV_BLOCK_BYTES, 1024), IDESC_PV, (i > 0 || ks > 0));
               mma_commit(bar(B_EMPTYVP + sp));
               mma_commit_multicast(bar(B_XPFREE + xs), (uint16_t)(1u << peer));   // the peer may refill
@@ -863,7 +967,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     cluster_wait();                                // the peer's barriers exist
     const int hrow = tid;                          // head row = TMEM lane
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t peer_xp = peer_addr(sbase + XP_OFF, peer) + (uint32_t)warp * 32 * 64;
+    const uint32_t peer_xp = peer_addr(sbase + L::XP_OFF, peer) + (uint32_t)warp * 32 * 64;
     float ref = 0.f, l = 0.f, l_peer = 0.f, m_ex = -INFINITY;
     bool flag = false, ref_unset = false, decided = false;
     int ig = 0, last_pass = 0;
@@ -872,10 +976,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     };
     // the peer's first-tile maxima, taken once
     auto agree_ref = [&](float mt) -> bool {
-      st_async_b32(peer_addr(sbase + XMAX_OFF, peer) + hrow * 4, __float_as_uint(mt),
+      st_async_b32(peer_addr(sbase + L::XMAX_OFF, peer) + hrow * 4, __float_as_uint(mt),
                    peer_addr(bar(B_XMAX), peer));
       if (!warp_wait_cluster(bar(B_XMAX), 0)) return false;
-      const float pm = reinterpret_cast<volatile float *>(sm + XMAX_OFF)[hrow];
+      const float pm = reinterpret_cast<volatile float *>(sm + L::XMAX_OFF)[hrow];
       ref = fmaxf(mt, pm);
       if (ref == -INFINITY) {   // neither first tile has a valid key
         ref = 0.f;
@@ -943,13 +1047,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4 *>(sm + XS_OFF + xs * P_SLOT_BYTES + sw64(hrow, j)) =
+          *reinterpret_cast<uint4 *>(sm + L::XS_OFF + xs * P_SLOT_BYTES + sw64(hrow, j)) =
               make_uint4(sr[4 * j], sr[4 * j + 1], sr[4 * j + 2], sr[4 * j + 3]);
         fence_proxy_async();     // the bulk copy reads through the async proxy
         __syncwarp();
         if (lane == 0)
           bulk_to_peer(peer_xp + xs * P_SLOT_BYTES,
-                       sbase + XS_OFF + xs * P_SLOT_BYTES + warp * 32 * 64, 32 * 64,
+                       sbase + L::XS_OFF + xs * P_SLOT_BYTES + warp * 32 * 64, 32 * 64,
                        peer_addr(bar(B_XPFULL + xs), peer));
       }
       if (timed_out) break;
@@ -957,12 +1061,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
 
       // end of pass: (l, running max, flag) to the peer, the peer's back
       // l < 0 carries a mark for a second pass (only the first pass marks)
-      st_async_v2(peer_addr(sbase + XEND_OFF + pass * HG * 8, peer) + hrow * 8,
+      st_async_v2(peer_addr(sbase + L::XEND_OFF + pass * HG * 8, peer) + hrow * 8,
                   __float_as_uint(pass == 0 && flag ? -1.f : l), __float_as_uint(m_ex),
                   peer_addr(bar(B_XEND + pass), peer));
       if (!warp_wait_cluster(bar(B_XEND + pass), 0)) { timed_out = true; break; }
       const volatile uint32_t *pe =
-          reinterpret_cast<const volatile uint32_t *>(sm + XEND_OFF + pass * HG * 8) + hrow * 2;
+          reinterpret_cast<const volatile uint32_t *>(sm + L::XEND_OFF + pass * HG * 8) + hrow * 2;
       l_peer = __uint_as_float(pe[0]);
       const float m_peer = __uint_as_float(pe[1]);
       const bool f_peer = pass == 0 && l_peer < 0.f;
@@ -987,7 +1091,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     // free: the reference was agreed in the first pass)
     const int h = h0 + hrow;
     const float lt = l + l_peer;
-    reinterpret_cast<volatile float *>(sm + XMAX_OFF)[hrow] = lt > 0.f ? 1.0f / lt : 0.f;
+    reinterpret_cast<volatile float *>(sm + L::XMAX_OFF)[hrow] = lt > 0.f ? 1.0f / lt : 0.f;
     float *lse_to = Q8 && parts.n > 1 ? parts.lse + (int64_t)part * parts.R * H : lse;
     if (lse_to && c == 0 && h < H)
       lse_to[(int64_t)r * H + h] = lt > 0.f ? (ref + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
@@ -1014,7 +1118,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     const int q4 = warp & 3, half = warp >> 2;
     const int row = q4 * 32 + lane;
     const bool f32_out = Q8 && parts.n > 1;
-    const float inv = ok ? reinterpret_cast<volatile float *>(sm + XMAX_OFF)[row] : 0.f;
+    const float inv = ok ? reinterpret_cast<volatile float *>(sm + L::XMAX_OFF)[row] : 0.f;
     const uint32_t lane_q = tmem + ((uint32_t)(q4 * 32) << 16);
 #pragma unroll 1
     for (int pp = 0; pp < 4; pp += 2) {
@@ -1029,17 +1133,28 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
         for (int k = 0; k < 32; ++k) o[0][k] = o[1][k] = 0u;
       }
       if (f32_out) {
-        // a part of the row: O / l in f32, a thread's 64 dims as 256 bytes
-        if (h0 + row < H) {
-          float *dst = parts.o + (((int64_t)part * parts.R + r) * H + h0 + row) * DV + 256 * c + 32 * p0;
+        // a part of the row: O / l in f32, 64 dims of the warp's 32 heads at a
+        // time through the warp's own piece of the drained rings (rows of 272
+        // bytes, which spreads them over the banks), so that a store writes
+        // whole 256-byte pieces of two rows
+        unsigned char *stg = sm + O_STG_OFF + warp * (32 * 272);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const uint32_t *v = &o[k >> 3][4 * (k & 7)];
-            *reinterpret_cast<float4 *>(dst + 4 * k) =
-                make_float4(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv,
-                            __uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
-          }
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t *v = &o[k >> 3][4 * (k & 7)];
+          *reinterpret_cast<float4 *>(stg + lane * 272 + 16 * k) =
+              make_float4(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv,
+                          __uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
         }
+        __syncwarp();
+        float *dst = parts.o + (((int64_t)part * parts.R + r) * H + h0 + q4 * 32) * DV + 256 * c + 32 * p0 +
+                     4 * (lane & 15);
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+          const int hr = 2 * k + (lane >> 4);
+          const float4 v = *reinterpret_cast<const float4 *>(stg + hr * 272 + 16 * (lane & 15));
+          if (h0 + q4 * 32 + hr < H) *reinterpret_cast<float4 *>(dst + (int64_t)hr * DV) = v;
+        }
+        __syncwarp();
         continue;
       }
 #pragma unroll
@@ -1093,7 +1208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
 
   if (timed_out && status) atomicOr(status, HS_STATUS_TIMEOUT);
   __syncwarp();
-  if (warp >= 4 && warp < 12 + NSB) cluster_wait();   // the opening barrier's wait
+  if (warp >= 4 && warp != 12 + NSB) cluster_wait();   // the opening barrier's wait
   fence_before();
   cluster_sync();          // the peer writes into this CTA's shared memory until here
   if (warp == 0) {
@@ -1132,9 +1247,9 @@ static int set_attn_attributes() {
   static bool attr_done[64] = {false};
   if (dev >= 64 || !attr_done[dev]) {
     HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     SMEM_ALLOC));
+                                     Lay<false>::SMEM_ALLOC));
     HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     SMEM_ALLOC));
+                                     Lay<true>::SMEM_ALLOC));
     if (dev < 64) attr_done[dev] = true;
   }
   return HS_OK;
@@ -1145,7 +1260,7 @@ int hs_attn_block_attrs(cudaFuncAttributes *attr, int *threads, size_t *dyn_smem
   if (rc) return rc;
   HS_CUDA_TRY(cudaFuncGetAttributes(attr, k_attn_pair<false>));
   *threads = THREADS;
-  *dyn_smem = SMEM_ALLOC;
+  *dyn_smem = Lay<false>::SMEM_ALLOC;
   return HS_OK;
 }
 
@@ -1160,7 +1275,7 @@ int hs_attn_wave_rows(int32_t H, int32_t *rows) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM_ALLOC;
+    cfg.dynamicSmemBytes = Lay<false>::SMEM_ALLOC;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -1237,8 +1352,8 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
   // run while the previous kernel in the stream finishes
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM_ALLOC;
+  cfg.blockDim = dim3(Q8 ? Q8_THREADS : THREADS);
+  cfg.dynamicSmemBytes = Lay<Q8>::SMEM_ALLOC;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1278,23 +1393,29 @@ namespace {
 
 // Joins the parts of every (row, head): with L = max_s lse_s and w_s =
 // exp(lse_s - L), out = sum_s w_s O_s / sum_s w_s and lse = L + ln(sum_s w_s).
-// A block per (row, head), four dims per thread; parts without a valid key
-// have lse_s = -inf and weigh nothing.
-__global__ void __launch_bounds__(DV / 4) k_attn_join(const float *__restrict__ o,
-                                                      const float *__restrict__ part_lse, int32_t n,
-                                                      int64_t rows, __nv_bfloat16 *__restrict__ out,
-                                                      float *__restrict__ lse) {
+// Parts without a valid key have lse_s = -inf and weigh nothing. A block per
+// (row, head); GROUPS groups of 128 threads (four dims each) take every
+// GROUPS-th part, four loads in flight, and their sums meet in shared memory in
+// a fixed order. Latency bounds a small grid: four groups read its parts in
+// as few rounds as they allow (one row of 128 heads, 16 parts: 16.4 us for the
+// whole call against 17.5 with one group, 64 parts: 20.0 against 25.7); a
+// large one fills the SMs and takes one (4 rows: 18.5 us against 19.7).
+template <int GROUPS>
+__global__ void __launch_bounds__(GROUPS * DV / 4)
+    k_attn_join(const float *__restrict__ o, const float *__restrict__ part_lse, int32_t n, int64_t rows,
+                __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
   // a programmatic dependent launch of the kernel that writes the parts
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int64_t row = blockIdx.x;
-  const float4 *src = reinterpret_cast<const float4 *>(o + row * DV) + threadIdx.x;
+  const int g = threadIdx.x / (DV / 4), t = threadIdx.x % (DV / 4);
+  const float4 *src = reinterpret_cast<const float4 *>(o + row * DV) + t;
   float top = -INFINITY;
   for (int s = 0; s < n; ++s) top = fmaxf(top, part_lse[s * rows + row]);
   const float ref = top == -INFINITY ? 0.f : top;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float w_sum = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < n; ++s) {
+  for (int s = g; s < n; s += GROUPS) {
     const float w = exp2f((part_lse[s * rows + row] - ref) * 1.4426950408889634f);
     const float4 v = src[s * rows * (DV / 4)];
     w_sum += w;
@@ -1303,13 +1424,34 @@ __global__ void __launch_bounds__(DV / 4) k_attn_join(const float *__restrict__ 
     a.z += w * v.z;
     a.w += w * v.w;
   }
+  if constexpr (GROUPS > 1) {
+    __shared__ float4 acc[GROUPS][DV / 4];
+    __shared__ float sums[GROUPS];
+    acc[g][t] = a;
+    if (t == 0) sums[g] = w_sum;
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) {
+      const float4 b = acc[k][t];
+      w_sum += sums[k];
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
+    }
+  }
   const float inv = w_sum == 0.f ? 0.f : 1.f / w_sum;
-  reinterpret_cast<uint2 *>(out + row * DV)[threadIdx.x] =
+  reinterpret_cast<uint2 *>(out + row * DV)[t] =
       make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-  if (lse && threadIdx.x == 0) lse[row] = w_sum == 0.f ? -INFINITY : ref + logf(w_sum);
+  if (lse && t == 0) lse[row] = w_sum == 0.f ? -INFINITY : ref + logf(w_sum);
 }
 
-constexpr int PART_MIN_TILES = 4;   // tiles of 32 keys, at least, in a part of a row
+constexpr int JOIN_FEW = 256;       // (row, head) pairs that leave a grid of one group each small
+
+// Tiles of 32 keys, at least, in a part of a row: a cluster costs ~9 us whatever
+// its tiles (8 and 4 tiles measured 16.2 and 15.4 us on 4 rows of 2048 keys).
+constexpr int PART_MIN_TILES = 4;
 
 }  // namespace
 
@@ -1345,17 +1487,19 @@ extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n
   int rc = attn_launch<true>(q, kv, n_kv_rows, nullptr, 0, nullptr, nullptr, 0, idx, R, H, K, scale,
                              out, lse, status, parts, true, stream);
   if (rc || parts.n == 1) return rc;
+  const bool few = (int64_t)R * H <= JOIN_FEW;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(R * H));
-  cfg.blockDim = dim3(DV / 4);
+  cfg.blockDim = dim3((few ? 4 : 1) * DV / 4);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  HS_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_attn_join, (const float *)parts.o, (const float *)parts.lse,
-                                 parts.n, (int64_t)R * H, reinterpret_cast<__nv_bfloat16 *>(out), lse));
+  HS_CUDA_TRY(cudaLaunchKernelEx(&cfg, few ? k_attn_join<4> : k_attn_join<1>, (const float *)parts.o,
+                                 (const float *)parts.lse, parts.n, (int64_t)R * H,
+                                 reinterpret_cast<__nv_bfloat16 *>(out), lse));
   HS_LAUNCH_CHECK("k_attn_join");
   return HS_OK;
 }

@@ -182,11 +182,12 @@ __global__ void __launch_bounds__(QT_THREADS) k_dequant_rows(
       uint4 *out = reinterpret_cast<uint4 *>(d[u]) + lane;
 #pragma unroll
       for (int k = 0; k < L::PASSES; ++k) {
-        const float s = q8_scale(e[u][k]);
         if constexpr (L::VEC == 8) {
+          const uint64_t s = q8_scale2(e[u][k]);
           const uint2 a = q8_decode4_bf16(c[u][k].x, s), b = q8_decode4_bf16(c[u][k].y, s);
           __stcs(out + 32 * k, make_uint4(a.x, a.y, b.x, b.y));
         } else {
+          const float s = q8_scale(e[u][k]);
           const float2 a = q8_decode2(c[u][k], 0, s), b = q8_decode2(c[u][k], 2, s);
           __stcs(out + 32 * k, make_uint4(__float_as_uint(a.x), __float_as_uint(a.y),
                                           __float_as_uint(b.x), __float_as_uint(b.y)));
