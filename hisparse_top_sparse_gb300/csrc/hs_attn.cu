@@ -57,7 +57,7 @@
 // bf16, so the output is bit for bit that of the bf16 kernel over the rows read
 // back. Four more warps and different rings bring the rows in: they land raw,
 // 656 bytes instead of 1152, and are decoded into the slots. Measured, 128 rows
-// x 128 heads x 2048 keys: 96.5 us, a tile pair per 1.25 us against 1.0 in the
+// x 128 heads x 2048 keys: 95.5 us, a tile pair per 1.2 us against 1.0 in the
 // bf16 kernel (84 us; with rows that need no gathering or decoding the rest
 // takes 77). A slot of ring VO is held from the decoding (0.5 us) through Q K^T,
 // softmax and its P V, about 2.9 pairs, and three fit beside the raw rings.
@@ -636,27 +636,34 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
       return (t < T && j < K) ? __ldg(idx_row + j) : -1;
     };
     // 16 codes into two chunks of a swizzled 64-dim block
-    auto put = [&](uint32_t block, const uint4 w, uint32_t byte) {
+    auto put = [&](uint32_t to, const uint4 w, uint32_t byte) {
       const uint64_t s = q8_scale2(byte & 0xFFu);
       const uint2 a = q8_decode4_bf16(w.x, s), b = q8_decode4_bf16(w.y, s);
-      st_shared16(block + sw128(key, 2 * (sub & 3)), make_uint4(a.x, a.y, b.x, b.y));
+      st_shared16(to, make_uint4(a.x, a.y, b.x, b.y));
       const uint2 d = q8_decode4_bf16(w.z, s), e = q8_decode4_bf16(w.w, s);
-      st_shared16(block + sw128(key, 2 * (sub & 3) + 1), make_uint4(d.x, d.y, e.x, e.y));
+      st_shared16(to ^ 16, make_uint4(d.x, d.y, e.x, e.y));      // the chunk beside it
     };
     const int sh = 8 * (sub >> 1);     // this thread's byte of a word of exponents
     if (own) {
       // chunks sub + 8 k: codes (block 2 k + sub / 4, exponent word k), rope
       const uint32_t raw = sbase + L::RAWO_OFF;
       auto copy = [&](int32_t id, int slot) {
+        // (a copy of no bytes where the index names no row: q stands for its address)
         const bool v = id >= 0 && id < n_kv;
-        const char *row = v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q;
+        const char *row = (v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q) + sub * 16;
         const uint32_t to = raw + slot * RAWO_BYTES;
 #pragma unroll
-        for (int k = 0; k < 5; ++k) cp_async16(to + (k * NPROD + p) * 16, v ? row + (sub + 8 * k) * 16 : q, v);
-        if (sub == 0) cp_async16(to + 5 * NPROD * 16 + key * 16, v ? row + Q8_SCALE_OFF : q, v);
+        for (int k = 0; k < 5; ++k) cp_async16(to + p * 16 + k * (NPROD * 16), row + k * 128, v);
+        if (sub == 0) cp_async16(to + 5 * NPROD * 16 + key * 16, row + Q8_SCALE_OFF, v);
         cp_async_commit();
       };
+      // where chunk sub + 8 k lies: block 2 k + sub / 4, of the CTA's value half
+      // (ring VO) for two of the k, of the other half (ring A) for two
+      const uint32_t at0 = (uint32_t)(sub >> 2) * KV_BLOCK_BYTES + sw128(key, 2 * (sub & 3));
+      const uint32_t rope_at = 4 * KV_BLOCK_BYTES + sw128(key, sub);
       int ig = 0;                      // own tiles taken, over both passes
+      int sa = 0, so = 0;              // their slots; parities of the releases waited for
+      uint32_t pa = 1, po = 1;         // (flipped to 0 before the first wait)
       for (int pass = 0; pass < 2 && !timed_out; ++pass) {
         uint4 code[4], rope, scale;
         int copied = 0;
@@ -700,20 +707,24 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
             __syncwarp();
             next();
           }
-          const int sa = ig % L::RA_SLOTS, so = ig % L::VO_SLOTS;
-          if ((ig >= L::RA_SLOTS && !warp_wait(bar(B_EMPTYA + sa), ((ig / L::RA_SLOTS) - 1) & 1)) ||
-              (ig >= L::VO_SLOTS && !warp_wait(bar(B_EMPTYVO + so), ((ig / L::VO_SLOTS) - 1) & 1))) {
+          if ((ig >= L::RA_SLOTS && !warp_wait(bar(B_EMPTYA + sa), pa)) ||
+              (ig >= L::VO_SLOTS && !warp_wait(bar(B_EMPTYVO + so), po))) {
             timed_out = true;
             break;
           }
           const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
           const uint32_t rv = sbase + L::VO_OFF + so * V_SLOT_BYTES;
-          const uint32_t sw[4] = {scale.x, scale.y, scale.z, scale.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) put(kv_block(ra, rv, c, 2 * k + (sub >> 2)), code[k], sw[k] >> sh);
-          st_shared16(kv_block(ra, rv, c, 8) + sw128(key, sub), rope);
+          const uint32_t lo = (c ? ra : rv) + at0, hi = (c ? rv : ra) + at0;   // dims below / from 256
+          put(lo, code[0], scale.x >> sh);
+          put(lo + 2 * KV_BLOCK_BYTES, code[1], scale.y >> sh);
+          put(hi, code[2], scale.z >> sh);
+          put(hi + 2 * KV_BLOCK_BYTES, code[3], scale.w >> sh);
+          st_shared16(ra + rope_at, rope);
           fence_proxy_async();
           bar_arrive(bar(B_FULLA + sa));
+          // the next tile's slots, and the parity of their next release
+          if (++sa == L::RA_SLOTS) { sa = 0; pa ^= 1; }
+          if (++so == L::VO_SLOTS) { so = 0; po ^= 1; }
         }
         cp_async_wait<0>();
       }
@@ -723,14 +734,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
       const uint32_t raw = sbase + L::RAWH_OFF;
       auto copy = [&](int32_t id, int slot) {
         const bool v = id >= 0 && id < n_kv;
-        const char *row = v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q;
+        const char *row = (v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q) + sub * 16;
         const uint32_t to = raw + slot * RAWH_BYTES;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          cp_async16(to + (k * Q8_HALF + p) * 16, v ? row + (DV / 2) * c + (sub + 4 * k) * 16 : q, v);
-        if (sub == 0) cp_async16(to + 4 * Q8_HALF * 16 + key * 16, v ? row + Q8_SCALE_OFF : q, v);
+          cp_async16(to + p * 16 + k * (Q8_HALF * 16), row + (DV / 2) * c + k * 64, v);
+        if (sub == 0) cp_async16(to + 4 * Q8_HALF * 16 + key * 16, row + Q8_SCALE_OFF, v);
         cp_async_commit();
       };
+      const uint32_t at0 = sw128(key, 2 * sub);
       int jg = 0;                      // peer tiles taken, over both passes
       if (!warp_wait(bar(B_QSTAGED), 0)) timed_out = true;
       for (int pass = 0; pass < 2 && !timed_out; ++pass) {
@@ -761,11 +773,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
             timed_out = true;
             break;
           }
-          const uint32_t rv = sbase + L::VP_OFF + sp * V_SLOT_BYTES;
+          const uint32_t to = sbase + L::VP_OFF + sp * V_SLOT_BYTES + at0;
           const uint32_t lo = c ? scale.z : scale.x, hi = c ? scale.w : scale.y;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            put(rv + k * KV_BLOCK_BYTES, code[k], (k < 2 ? lo : hi) >> (16 * (k & 1) + sh));
+            put(to + k * KV_BLOCK_BYTES, code[k], (k < 2 ? lo : hi) >> (16 * (k & 1) + sh));
           fence_proxy_async();
           bar_arrive(bar(B_FULLVP + sp));
         }
