@@ -11,9 +11,11 @@
 //   refusal and w = p_d past the last draft. With E_v exponentially
 //   distributed, that is v with probability w(v) / sum w: a race whose winner
 //   needs one pass and no running sum over the vocabulary, so that the order
-//   of additions cannot move the answer.
+//   of additions cannot move the answer. (The ratio is taken with an
+//   approximate reciprocal, off by 2^-23 like p itself: two tokens that near
+//   each other may change places.)
 //
-// One cluster of 1 to 8 blocks per request takes the request's rows in order,
+// One cluster of 1 to 16 blocks per request takes the request's rows in order,
 // one or a few at a time, and stops at the first refusal: the logits behind it,
 // and the draft probabilities of every row but the last, are never read. HBM
 // bounds it: each logits row is streamed once for (M, S), and the row that
@@ -32,9 +34,10 @@
 // overwrites the inputs during the call.
 //
 // Measured (bf16 logits, draft probabilities given): 256 requests x 3 drafts,
-// V = 129280: 92 us, 62 % of what the 385 MB it has to move take at the
-// measured copy rate (requests of unlike lengths leave SMs idle at the end);
-// 64 x 3: 34 us; 2 x 3, V = 1024 f32: 6.4 us, latency.
+// V = 129280: 94 us, 61 % of what the 385 MB it has to move take at the
+// measured copy rate (requests of unlike lengths: SMs are busy 79 % of the
+// time, at 5.6 TB/s); 64 x 3: 34 us; 1 x 3: 10 us and 2 x 3, V = 1024 f32: 6.4
+// us, latency.
 
 #include <float.h>
 
@@ -49,7 +52,7 @@ constexpr int RING = 12;            // 16-byte places of a thread's ring of copi
 constexpr int BATCH = 4;            // vectors of a row taken together
 constexpr int NB = 8;               // values of a thread in flight where rows are not aligned
 constexpr size_t RING_BYTES = (size_t)RING * NT * 16;
-constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_CLUSTER = 16;
 constexpr int MAX_DRAFTS = 255;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -448,45 +451,65 @@ struct BestOp {
   }
 };
 
-// The race over the row that yields the token: the largest w(v) / E(v) of this
-// thread's values and its v (INT32_MAX: none). `barred`: a token without weight.
-//
-// A value is divided only when it may win: p / E > best, rounded, needs
-// p > h E for h a little below best (2^-21, past the two roundings). t = p - h E
-// is one fused operation with the sign of the exact difference, and a group
-// of values whose largest t is negative is passed over. `best` is first that of
-// the thread's warp so far, so few groups are looked into.
+// What the race needs of its row.
+struct RaceRow {
+  float top, c, inv;       // p(v) = exp2((l(v) - top) c) inv
+  int32_t barred;          // a token without weight, or -1
+};
+
+// w(v) / E(v) of the pair of values l2 (their draft probabilities minus, their
+// E): one multiplication by an approximate reciprocal, as exact as p itself. A
+// NaN never wins; neither does a weight of 0 or less.
+__device__ __forceinline__ void ratio2(uint64_t l2, uint64_t minus_q, float e0, float e1, uint64_t nm,
+                                       uint64_t cc, uint64_t ii, float &r0, float &r1) {
+  float a, b, f, g;
+  unpack2(mul2(add2(l2, nm), cc), a, b);
+  const uint64_t p = fma2(pack2(ex2(a), ex2(b)), ii, minus_q);
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(f) : "f"(e0));
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(g) : "f"(e1));
+  unpack2(mul2(p, pack2(f, g)), r0, r1);
+}
+
+// The race over the row that yields the token: this thread's largest ratio and
+// its index (INT32_MAX: none above 0). A thread looks for the place of a
+// group's largest ratio only when it reaches the best of its warp so far.
 struct Race {
   float best;
   uint32_t at;
-  float h;
-  // (a logit of +inf, which counts as the row's maximum, has come out infinite)
-  __device__ __forceinline__ void look(float p, float e, float w, float inv, int32_t v, int32_t barred) {
-    if (p == INFINITY) p = inv - w;
-    if (p > 0.f && v != barred) {
-      const float r = p / e;
-      if (r > best) {                  // a thread's indices ascend: the lowest stays
-        best = r;
-        at = (uint32_t)v;
-      }
+  float bar;               // the warp's best so far
+
+  // (the whole warp; `big` is the largest of r, or 0 to take none)
+  template <int N>
+  __device__ __forceinline__ void group(const float (&r)[N], float big, int32_t v0, int32_t step) {
+    if (big >= bar && big > best) {
+      best = big;
+#pragma unroll
+      for (int j = N - 1; j >= 0; --j)
+        if (r[j] == big) at = (uint32_t)(v0 + j * step);      // the lowest of equals stays
     }
-  }
-  __device__ __forceinline__ void share() {        // by the whole warp
-    h = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(best))) * 0.9999995f;
+    bar = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(best)));
   }
 };
 
 template <int DTYPE, bool VEC>
 __device__ __forceinline__ Race race(const char *row, const float *q, const float *E, int32_t V,
-                                     uint32_t rank, uint32_t log_n, float top, float c, float inv,
-                                     int32_t barred, uint4 *ring) {
+                                     uint32_t rank, uint32_t log_n, const RaceRow &rr, uint4 *ring) {
   Race ra = {0.f, INT32_MAX, 0.f};
+  const uint64_t nm = pack2(-rr.top, -rr.top), cc = pack2(rr.c, rr.c), ii = pack2(rr.inv, rr.inv);
+  // a logit of +inf, which counts as the row's maximum, has come out infinite:
+  // its weight is that of the maximum
+  auto mend = [&](float &r, float w, float e) {
+    float f;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(f) : "f"(e));
+    if (r == INFINITY) r = (rr.inv - w) * f;
+  };
   if (VEC) {
     // units of 16 bytes of logits and as many values of q and E, through the
     // thread's ring places as in row_stat
     constexpr int PER = Slice<DTYPE>::PER, QV = PER / 4, SLOTS = 1 + 2 * QV, DEPTH = RING / SLOTS;
     const int32_t units = V / PER;
     const int32_t lo = part_of(units, rank, log_n), hi = part_of(units, rank + 1, log_n);
+    const int32_t barred_unit = rr.barred >= 0 ? rr.barred / PER : -1;
     auto issue = [&](int32_t k, int place) {
       uint4 *to = ring + place * SLOTS * NT;
       if (k < hi) {
@@ -501,79 +524,81 @@ __device__ __forceinline__ Race race(const char *row, const float *q, const floa
     };
 #pragma unroll
     for (int p = 0; p < DEPTH; ++p) issue(lo + p * NT + (int)threadIdx.x, p);
-    const uint64_t nm = pack2(-top, -top), cc = pack2(c, c), ii = pack2(inv, inv);
     int place = 0;
     for (int32_t k0 = lo; k0 < hi; k0 += NT) {
       const int32_t k = k0 + (int)threadIdx.x;
       copy_wait<DEPTH - 1>();
-      if (k < hi) {
-        const uint4 *from = ring + place * SLOTS * NT;
-        const uint4 x = from[0];
-        float p[PER], e[PER], t[PER];
-        const uint64_t nh = pack2(-ra.h, -ra.h);
+      const uint4 *from = ring + place * SLOTS * NT;
+      const uint4 x = from[0];
+      uint4 e4[QV], w4[QV];
 #pragma unroll
-        for (int j = 0; j < QV; ++j) {
-          const uint4 e4 = from[(1 + j) * NT];
-          const uint4 w4 = q ? from[(1 + QV + j) * NT] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            const int o = 4 * j + i;
-            e[o] = value<HS_LOGITS_F32>(e4, i);
-            e[o + 1] = value<HS_LOGITS_F32>(e4, i + 1);
-            float a, b;
-            // (a NaN among the logits makes its p NaN, which never wins)
-            unpack2(mul2(add2(pack2(value<DTYPE>(x, o), value<DTYPE>(x, o + 1)), nm), cc), a, b);
-            const uint64_t pp = fma2(pack2(ex2(a), ex2(b)), ii,
-                                     pack2(-value<HS_LOGITS_F32>(w4, i), -value<HS_LOGITS_F32>(w4, i + 1)));
-            unpack2(pp, p[o], p[o + 1]);
-            unpack2(fma2(nh, pack2(e[o], e[o + 1]), pp), t[o], t[o + 1]);
-          }
-        }
-        float big = t[0];
-#pragma unroll
-        for (int j = 1; j < PER; ++j) big = fmaxf(big, t[j]);
-        if (big >= 0.f) {
-#pragma unroll
-          for (int j = 0; j < PER; ++j)
-            if (t[j] >= 0.f)
-              ra.look(p[j], e[j], q ? value<HS_LOGITS_F32>(from[(1 + QV + j / 4) * NT], j) : 0.f, inv,
-                      k * PER + j, barred);
-        }
+      for (int j = 0; j < QV; ++j) {
+        e4[j] = from[(1 + j) * NT];
+        w4[j] = q ? from[(1 + QV + j) * NT] : make_uint4(0, 0, 0, 0);
       }
       issue(k + DEPTH * NT, place);
       place = place + 1 == DEPTH ? 0 : place + 1;
-      ra.share();
+      float r[PER], big = 0.f;
+#pragma unroll
+      for (int j = 0; j < QV; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const int o = 4 * j + i;
+          ratio2(pack2(value<DTYPE>(x, o), value<DTYPE>(x, o + 1)),
+                 pack2(-value<HS_LOGITS_F32>(w4[j], i), -value<HS_LOGITS_F32>(w4[j], i + 1)),
+                 value<HS_LOGITS_F32>(e4[j], i), value<HS_LOGITS_F32>(e4[j], i + 1), nm, cc, ii, r[o],
+                 r[o + 1]);
+          big = fmaxf(big, fmaxf(r[o], r[o + 1]));
+        }
+      }
+      if (k == barred_unit || big == INFINITY) {
+#pragma unroll
+        for (int o = 0; o < PER; ++o) {
+          mend(r[o], value<HS_LOGITS_F32>(w4[o / 4], o), value<HS_LOGITS_F32>(e4[o / 4], o));
+          if (k * PER + o == rr.barred) r[o] = 0.f;
+        }
+        big = 0.f;
+#pragma unroll
+        for (int o = 0; o < PER; ++o) big = fmaxf(big, r[o]);
+      }
+      ra.group(r, k < hi ? big : 0.f, k * PER, 1);      // (past the end: what the places held)
     }
     copy_wait<0>();
   } else {
     const int32_t lo = part_of(V, rank, log_n), hi = part_of(V, rank + 1, log_n);
     for (int32_t k0 = lo; k0 < hi; k0 += NB * NT) {
-      float p[NB], e[NB], w[NB];
+      float r[NB], e[NB], w[NB], big = 0.f;
 #pragma unroll
       for (int u = 0; u < NB; ++u) {
         const int32_t v = k0 + u * NT + (int)threadIdx.x;
-        p[u] = -INFINITY;
+        r[u] = -INFINITY;
         e[u] = 1.f;
         w[u] = 0.f;
         if (v < hi) {
-          p[u] = DTYPE == HS_LOGITS_F32
+          r[u] = DTYPE == HS_LOGITS_F32
                      ? __ldg(reinterpret_cast<const float *>(row) + v)
                      : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(row) + v) << 16);
           e[u] = __ldcs(E + v);
           if (q) w[u] = __ldcs(q + v);
         }
       }
-      float big = -1.f;
 #pragma unroll
-      for (int u = 0; u < NB; ++u) {
-        p[u] = fmaf(ex2((p[u] - top) * c), inv, -w[u]);
-        big = fmaxf(big, fmaf(-ra.h, e[u], p[u]));
+      for (int u = 0; u < NB; u += 2) {
+        ratio2(pack2(r[u], r[u + 1]), pack2(-w[u], -w[u + 1]), e[u], e[u + 1], nm, cc, ii, r[u], r[u + 1]);
+        big = fmaxf(big, fmaxf(r[u], r[u + 1]));
       }
-      if (big >= 0.f) {
+      const int32_t v0 = k0 + (int)threadIdx.x;
+      if (big == INFINITY || rr.barred >= 0) {
 #pragma unroll
-        for (int u = 0; u < NB; ++u) ra.look(p[u], e[u], w[u], inv, k0 + u * NT + (int)threadIdx.x, barred);
+        for (int u = 0; u < NB; ++u) {
+          mend(r[u], w[u], e[u]);
+          if (v0 + u * NT == rr.barred) r[u] = 0.f;
+        }
+        big = 0.f;
+#pragma unroll
+        for (int u = 0; u < NB; ++u) big = fmaxf(big, r[u]);
       }
-      ra.share();
+      ra.group(r, big, v0, NT);
     }
   }
   return ra;
@@ -681,8 +706,9 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
     const float *q = sa.probs && m < d ? sa.probs + ((int64_t)b * d + m) * V : nullptr;
     int32_t barred = !sa.probs && m < d ? sh.draft[m] : -1;   // a sure draft's own token
     for (;;) {
-      Race ra = sa.aligned ? race<DTYPE, true>(row, q, E, V, rank, log_n, top, c, inv, barred, ring)
-                           : race<DTYPE, false>(row, q, E, V, rank, log_n, top, c, inv, barred, ring);
+      const RaceRow rr = {top, c, inv, barred};
+      Race ra = sa.aligned ? race<DTYPE, true>(row, q, E, V, rank, log_n, rr, ring)
+                           : race<DTYPE, false>(row, q, E, V, rank, log_n, rr, ring);
       cluster_join(sh, ra.best, ra.at, rank, n, 0, turn, BestOp{});
       if (ra.at != INT32_MAX) {
         token = (int32_t)ra.at;
@@ -733,13 +759,14 @@ int check_sample(const void *logits, int32_t dtype, int32_t B, int32_t d, int32_
 // A cluster that takes its rows one after the other reads no row behind the
 // refusal, but each row costs a few microseconds of latency (the first loads,
 // the joins). So while few blocks run, up to four rows are taken side by side
-// (2 x 3 drafts, V = 1024: 7.1 us against 10.5; 33 x 5, V = 50257: 16.0 against
-// 22.8); at half of the resident blocks two (64 x 3, V = 129280: 33.6 against
-// 36.9 for one and 35.2 for four); with the device full, one. The blocks
-// of a request grow while all of them fit at once and a part keeps 2048
-// values, and past that (a second wave of blocks evens out requests of
-// different lengths) while a part keeps 16384 (256 x 3, V = 129280: 91 us with
-// four blocks, 97 with two; V = 32000: 45 with four, 33 with two).
+// (2 x 3 drafts, V = 1024: 6.3 us against 9.8; 33 x 5, V = 50257: 16 against
+// 23); at half of the resident blocks two (64 x 3, V = 129280: 34 us against 36
+// for one or four); with the device full, one. The blocks of a request
+// grow to eight while all of them fit at once and a part keeps 2048 values,
+// to sixteen while each has an SM of its own (1 x 3, V = 129280: 10.3 us
+// against 12.3), and to eight past one wave (a second wave evens out requests
+// of different lengths) while a part keeps 16384 (256 x 3, V = 129280: 94 us
+// with four blocks, 99 with two; V = 32000: 44 with four, 33 with two).
 int cluster_shape(int32_t B, int32_t d, int32_t V, int *n, int *g) {
   int sms = 0;
   int rc = hs_sm_count(&sms);
@@ -747,9 +774,10 @@ int cluster_shape(int32_t B, int32_t d, int32_t V, int *n, int *g) {
   const int64_t at_once = (int64_t)sms * MIN_BLOCKS;
   const int most = d >= 2 ? 4 : d + 1;           // rows side by side
   int k = 1;
-  while (k < MAX_CLUSTER && (int64_t)B * 2 * k <= at_once && (k < most || (int64_t)V * most / (2 * k) >= 2048))
+  while (k < MAX_CLUSTER && (int64_t)B * 2 * k <= (k < 8 ? at_once : (int64_t)sms) &&
+         (k < most || (int64_t)V * most / (2 * k) >= 2048))
     k *= 2;
-  while (k < MAX_CLUSTER && (int64_t)B * 2 * k <= 2 * at_once && V / (2 * k) >= 16384) k *= 2;
+  while (k < 8 && (int64_t)B * 2 * k <= 2 * at_once && V / (2 * k) >= 16384) k *= 2;
   int r = (int64_t)B * k <= at_once / 2 ? most : (int64_t)B * k <= at_once ? 2 : 1;
   if (r > most) r = most;
   if (r > k) r = k;
@@ -787,6 +815,11 @@ int launch(SampleArgs &sa, int32_t dtype, int32_t B, const CommitArgs &ca, cudaS
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES));
     HS_CUDA_TRY(cudaFuncSetAttribute(k_verify_sample<HS_LOGITS_BF16, COMMIT>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES));
+    // clusters of 16 blocks
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_verify_sample<HS_LOGITS_F32, COMMIT>,
+                                     cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_verify_sample<HS_LOGITS_BF16, COMMIT>,
+                                     cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     if (dev < 64) attr_done[dev] = true;
   }
   if (dtype == HS_LOGITS_F32)
