@@ -73,6 +73,7 @@
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <float.h>
 #include <math.h>
 
 #include "hs_q8.cuh"
@@ -1474,6 +1475,10 @@ extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n
                                         hs_stream_t stream) {
   if ((uintptr_t)workspace & 15)
     return hs_set_error(HS_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  // the softmax reference is the scaled maximum, which a negative scale would not give
+  if (!(scale >= 0.f) || scale > FLT_MAX)
+    return hs_set_error(HS_ERR_INVALID_ARG, "scale must be finite and not negative");
+  if (scale < FLT_MIN) scale = FLT_MIN;      // equal weights all the same; 0 times a masked -inf is NaN
   Parts parts = {1, K, R, nullptr, nullptr};
   if (R > 0 && H >= 1 && H <= 1024 && K > 0 && workspace) {
     // Few rows leave most of the SMs idle and walk their keys one after the

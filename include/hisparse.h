@@ -316,6 +316,7 @@ int hs_dequant_rows(const void *src, int64_t src_rows, void *dst, int32_t dst_dt
  * hs_sparse_attn_decode over a q8 cache: the same arguments, formulas, skipped
  * entries and launch, with kv [n_kv_rows][656]. The values enter the products
  * as bf16 (exactly), the softmax numerators are rounded to bf16 as there.
+ * scale is finite and not negative.
  *   workspace   device memory, 16-byte aligned, or NULL: with few rows the
  *               keys of a row are split over the idle SMs and the parts'
  *               outputs joined by a second kernel; the parts (f32) go here.

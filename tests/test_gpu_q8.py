@@ -412,3 +412,106 @@ def test_a_step_over_a_q8_follower_layer():
         assert np.array_equal(ts[b].numpy(), ref.token_slot_array(b))
     assert hs.hs_get_status(buf) == 0
     buf.close()
+
+
+def test_row_calls_from_and_to_host_memory_in_a_graph():
+    """Pinned source rows into a device cache and its rows into pinned memory,
+    captured once, replayed over new rows."""
+    hs = lib()
+    g = np.random.default_rng(13)
+    n = 90
+    src = _rows(g, n, torch.float32).pin_memory()
+    cache = torch.zeros((n, 656), dtype=torch.uint8, device=DEV)
+    back = torch.zeros((n, 576), dtype=torch.bfloat16).pin_memory()
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        hs.hs_quant_rows(src, cache, status=st)
+        hs.hs_dequant_rows(cache, back, status=st)
+    for _ in range(2):
+        src.copy_(_rows(g, n, torch.float32))
+        gr.replay()
+        torch.cuda.synchronize()
+        want = O.q8_quantise(_f64(src))
+        _check_bytes(np_(cache), want)
+        assert np.array_equal(_f64(back), O.q8_values(want))
+    assert int(st.item()) == 0
+
+
+def test_row_calls_on_a_side_stream():
+    hs = lib()
+    g = np.random.default_rng(14)
+    src = _rows(g, 3000, torch.bfloat16).to(DEV)
+    cache = torch.zeros((3000, 656), dtype=torch.uint8, device=DEV)
+    back = torch.zeros((3000, 576), dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    hs.hs_quant_rows(src, cache, stream=s)
+    hs.hs_dequant_rows(cache, back, stream=s.cuda_stream)
+    s.synchronize()
+    assert np.array_equal(_f64(back), O.q8_values(O.q8_quantise(_f64(src))))
+
+
+def test_attention_degenerate_calls_and_refusals():
+    hs = lib()
+    g = np.random.default_rng(15)
+    rows, values = _cache(g, 300)
+    cache = _t(rows)
+    q = torch.as_tensor(g.standard_normal((2, 24, 576)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    idx = _t(_indices(g, 2, 700, 300, 0.1))
+    ref, ref_lse = _attend(hs, q, cache, idx, 1 / 24)
+    _check(ref, ref_lse, _f64(q), values, np_(idx), 1 / 24)
+    # a workspace too small for two parts: one part, the same bits
+    out, lse = _attend(hs, q, cache, idx, 1 / 24, torch.empty(160, dtype=torch.uint8, device=DEV))
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    # no lse wanted, whole and in parts
+    big = torch.empty(32 << 20, dtype=torch.uint8, device=DEV)
+    whole, _ = _attend(hs, q, cache, idx, 1 / 24, big)
+    for ws, want in ((None, ref), (big, whole)):
+        out = torch.empty_like(ref)
+        hs.hs_sparse_attn_decode_q8(q, cache, idx, 1 / 24, out, workspace=ws)
+        assert torch.equal(out, want)
+    # scale 0: the mean of the values, lse = ln of their number
+    out, lse = _attend(hs, q, cache, idx, 0.0, big)
+    _check(out, lse, _f64(q), values, np_(idx), 0.0)
+    # no keys, an empty cache, no rows
+    for c, i in ((cache, idx[:, :0].contiguous()), (cache[:0], idx)):
+        out, lse = _attend(hs, q, c, i, 1 / 24, big)
+        assert not out.any() and torch.isneginf(lse).all()
+    hs.hs_sparse_attn_decode_q8(q[:0], cache, idx[:0], 1 / 24, ref[:0])
+    for bad in (-0.1, float("inf"), float("nan")):
+        with pytest.raises(hs.HisparseError):
+            hs.hs_sparse_attn_decode_q8(q, cache, idx, bad, ref)
+    with pytest.raises(hs.HisparseError):
+        hs.hs_sparse_attn_decode_q8(q, cache, idx, 1 / 24, ref, workspace=big[8:])
+    with pytest.raises(ValueError):
+        hs.hs_sparse_attn_decode_q8(q, cache, idx[:1], 1 / 24, ref)
+    with pytest.raises(ValueError):
+        hs.hs_sparse_attn_decode_q8(q, cache[:, :655], idx, 1 / 24, ref)
+    with pytest.raises(ValueError):
+        hs.hs_sparse_attn_decode_q8(q, cache.cpu(), idx, 1 / 24, ref)
+    with pytest.raises(TypeError):
+        hs.hs_sparse_attn_decode_q8(q.float(), cache, idx, 1 / 24, ref)
+
+
+def test_attention_leaves_its_neighbours_alone():
+    """Outputs and workspace in the middle of larger buffers: nothing around
+    them is written."""
+    hs = lib()
+    g = np.random.default_rng(16)
+    rows, _ = _cache(g, 500)
+    R, H, K = 3, 50, 640
+    q = torch.as_tensor(g.standard_normal((R, H, 576)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    idx = _t(_indices(g, R, K, 500, 0.0))
+    pad_o = torch.full((R * H * 512 + 256,), 3.0, dtype=torch.bfloat16, device=DEV)
+    pad_l = torch.full((R * H + 32,), 3.0, device=DEV)
+    parts = 5                                              # 20 tiles of 32 keys, four to a part
+    size = parts * R * H * 513 * 4
+    pad_w = torch.full((size + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+    out, lse = pad_o[128:128 + R * H * 512].view(R, H, 512), pad_l[16:16 + R * H].view(R, H)
+    hs.hs_sparse_attn_decode_q8(q, _t(rows), idx, 1 / 24, out, lse=lse, workspace=pad_w[256:256 + size])
+    want, want_lse = _attend(hs, q, _t(rows), idx, 1 / 24, torch.empty(32 << 20, dtype=torch.uint8, device=DEV))
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert (pad_o[:128] == 3).all() and (pad_o[-128:] == 3).all()
+    assert (pad_l[:16] == 3).all() and (pad_l[-16:] == 3).all()
+    assert (pad_w[:256] == 0x5A).all() and (pad_w[-256:] == 0x5A).all()

@@ -70,7 +70,8 @@ def _check(got, want):
 @pytest.mark.parametrize("B,d,V,masked", [(1, 0, 1, 0.0), (3, 1, 2, 0.0), (2, 3, 1024, 0.0), (5, 4, 1001, 0.5),
                                            (40, 2, 333, 0.95), (1, 7, 50257, 0.0), (3, 15, 9999, 0.2),
                                            (2, 3, 129280, 0.0), (160, 2, 4097, 0.1), (330, 1, 700, 0.0),
-                                           (2, 40, 100, 0.0)])
+                                           (2, 40, 100, 0.0), (1, 255, 64, 0.0), (2000, 1, 40, 0.2),
+                                           (1, 3, 40000, 0.0), (9, 3, 32768, 0.0), (70, 5, 20000, 0.9)])
 def test_against_the_oracle(dtype, probs, B, d, V, masked):
     hs = lib()
     c = _case(B * 131 + d * 17 + V, B, d, V, dtype, probs, masked)
@@ -304,3 +305,56 @@ def test_finalize_refusals():
         acc.add_(0)
     assert err.value.code == hs.HS_ERR_UNSUPPORTED
     buf.close()
+
+
+@pytest.mark.parametrize("shift", ["logits", "probs", "noise"])
+def test_one_array_off_its_sixteen_bytes(shift):
+    """A vocabulary of whole 16-byte vectors whose arrays do not all start on
+    one: the same answers as aligned ones."""
+    hs = lib()
+    B, d, V = 4, 2, 4096
+    logits, T, x, q, u, E = _case(41, B, d, V, torch.bfloat16, True)
+    dev = {"logits": logits.to(DEV), "probs": _t(q), "noise": _t(E)}
+    flat = torch.empty(dev[shift].numel() + 1, dtype=dev[shift].dtype, device=DEV)
+    off = flat[1:].view(dev[shift].shape)
+    off.copy_(dev[shift])
+    dev[shift] = off
+    acc = torch.empty(B, dtype=torch.int32, device=DEV)
+    nxt, lp = torch.empty_like(acc), torch.empty((B, d + 1), device=DEV)
+    hs.hs_verify_sample(dev["logits"], _t(T), _t(x), dev["probs"], _t(u), dev["noise"], acc, nxt, logprob=lp)
+    _check((np_(acc), np_(nxt), np_(lp)), O.verify_sample(logits, T, x, q, u, E))
+
+
+def test_equal_ratios_go_to_the_lowest_index():
+    """Uniform logits and noise: every token is drawn alike."""
+    hs = lib()
+    for V in (5, 1000, 4096, 131072):
+        for dtype in (torch.float32, torch.bfloat16):
+            B, d = 3, 1
+            logits = torch.zeros((B, d + 1, V), dtype=dtype)
+            u = np.array([[0.0], [1.0], [1.0]], np.float32)
+            x = np.array([[V - 1], [0], [V // 2]], np.int32)
+            got = _run(hs, logits, np.ones(B, np.float32), x, None, u, np.ones((B, V), np.float32))
+            # accepted: the lowest of all; refused: the lowest but the draft's own
+            assert got[0].tolist() == [1, 0, 0] and got[1].tolist() == [0, 1, 0]
+
+
+def test_refusals_of_the_binding():
+    hs = lib()
+    B, d, V = 2, 1, 64
+    logits, T, x, q, u, E = _case(1, B, d, V, torch.float32, True)
+    good = dict(logits=logits.to(DEV), temperature=_t(T), draft_tokens=_t(x), draft_probs=_t(q), uniforms=_t(u),
+                noise=_t(E), accept_len=torch.empty(B, dtype=torch.int32, device=DEV),
+                next_token=torch.empty(B, dtype=torch.int32, device=DEV))
+    hs.hs_verify_sample(**good)
+    for k, v in (("logits", good["logits"].half()), ("temperature", good["temperature"].double()),
+                 ("draft_tokens", good["draft_tokens"].long()), ("noise", good["noise"].bfloat16())):
+        with pytest.raises(TypeError):
+            hs.hs_verify_sample(**dict(good, **{k: v}))
+    for k, v in (("temperature", good["temperature"][:1]), ("draft_probs", good["draft_probs"][:, :, :32]),
+                 ("uniforms", good["uniforms"].cpu()), ("noise", good["noise"].t().contiguous().t()),
+                 ("uniforms", None), ("noise", None), ("logits", good["logits"].transpose(1, 2).contiguous().transpose(1, 2))):
+        with pytest.raises(ValueError):
+            hs.hs_verify_sample(**dict(good, **{k: v}))
+    with pytest.raises(hs.HisparseError):
+        hs.hs_verify_sample(**{k: (v[:0] if v is not None else None) for k, v in good.items()})

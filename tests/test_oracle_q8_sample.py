@@ -134,7 +134,7 @@ def test_refusals_without_a_gpu():
     assert attn(rows=-1) == bad and attn(q=None) == bad and attn(out=None) == bad
     assert attn(K=1, idx=None) == bad and attn(K=1, kv=None) == bad
     assert attn(q=P(8)) == bad and attn(kv=P(8)) == bad and attn(out=P(8)) == bad and attn(ws=P(8)) == bad
-    assert attn(scale=float("nan")) == bad
+    assert attn(scale=float("nan")) == bad and attn(scale=-0.5) == bad and attn(scale=float("inf")) == bad
     assert attn(R=0) == hs.HS_OK
 
     def sample(l=P(16), dt=0, B=1, d=1, V=8, t=P(16), x=P(16), u=P(16), e=P(16), a=P(16), n=P(16), q=None):
