@@ -525,14 +525,12 @@ def hs_backup_indexer(src_caches, dst_caches, src_slots, host_slots, positions,
 # that is wanted of a tensor, and the reasons only once it has failed. Every
 # CUDA tensor must be on the current device, where the call launches.
 
-def _on(t, name, dtype, shape, cur, none=False):
+def _on(t, name, dtype, shape, cur):
     """Pointer of a contiguous CUDA tensor of the current device."""
-    if t is None and none:
-        return None
     try:
         if t.dtype is dtype and t.get_device() == cur and t.is_contiguous() and \
                 (shape is None or t.shape == shape):
-            return t.data_ptr() if t.numel() > 0 else None
+            return t.data_ptr() or None
     except AttributeError:
         pass
     p = _ptr(t, name, dtype, shape)
@@ -545,8 +543,6 @@ def _on_stream(stream, cur):
     return torch._C._cuda_getCurrentRawStream(cur) if stream is None else _stream(stream)
 
 
-# ------------------------------------------------- quantised latent rows --
-
 def _device() -> int:
     """The current CUDA device; -2 where there is none (no tensor's device)."""
     try:
@@ -555,53 +551,73 @@ def _device() -> int:
         return -2
 
 
-def _host_or_device(t, name, cur) -> None:
+# ------------------------------------------------- quantised latent rows --
+
+def _elsewhere(t, name, cur) -> None:
+    """Raises unless t, which is not on the current device, is pinned memory."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != cur:
-        if t.is_cuda:
-            raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{cur}")
-        if cur < 0 or not t.is_pinned():
-            raise ValueError(f"{name} must be a CUDA tensor or pinned host memory")
+    if t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{cur}")
+    if cur < 0 or not t.is_pinned():
+        raise ValueError(f"{name} must be a CUDA tensor or pinned host memory")
 
 
-def _q8_cache(t, name, cur) -> int:
-    _host_or_device(t, name, cur)
-    if t.dtype is not torch.uint8 or t.dim() != 2 or t.shape[1] != Q8_ROW_BYTES or \
-            not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous uint8 [rows][{Q8_ROW_BYTES}] tensor")
-    return t.data_ptr()
+def _q8_cache(t, name, cur):
+    """(pointer, rows) of a q8 cache."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != cur:
+        _elsewhere(t, name, cur)
+    if t.dtype is torch.uint8 and t.is_contiguous():
+        s = t.shape
+        if len(s) == 2 and s[1] == Q8_ROW_BYTES:
+            return t.data_ptr(), s[0]
+    raise ValueError(f"{name} must be a contiguous uint8 [rows][{Q8_ROW_BYTES}] tensor")
 
 
 _WIDE = {torch.float32: HS_LOGITS_F32, torch.bfloat16: HS_LOGITS_BF16}
 
 
 def _wide_rows(t, name, cur):
-    """(pointer, dtype code, row stride) of bf16 / f32 rows of 576 values, the
-    rows any distance apart."""
-    _host_or_device(t, name, cur)
-    n = t.shape[0] if t.dim() == 2 else 0
-    if t.dim() != 2 or t.shape[1] != LATENT_DIM or (n > 0 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows][{LATENT_DIM}] with contiguous rows")
-    if t.dtype not in _WIDE:
+    """(pointer, dtype code, row stride, rows) of bf16 / f32 rows of 576 values,
+    the rows any distance apart."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != cur:
+        _elsewhere(t, name, cur)
+    dt = _WIDE.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be float32 or bfloat16")
-    return t.data_ptr(), _WIDE[t.dtype], t.stride(0) if n > 1 else LATENT_DIM
+    s, st = t.shape, t.stride()
+    if len(s) != 2 or s[1] != LATENT_DIM or (s[0] > 0 and st[1] != 1):
+        raise ValueError(f"{name} must be [rows][{LATENT_DIM}] with contiguous rows")
+    return t.data_ptr(), dt, st[0] if s[0] > 1 else LATENT_DIM, s[0]
 
 
-def _slots(src_slots, dst_slots, src_rows, dst_rows) -> int:
-    """Entries of a row call: the slot lists' length, else every source row
-    (which the destination must hold)."""
-    n = -1
-    for t in (src_slots, dst_slots):
-        if t is not None:
-            if not isinstance(t, torch.Tensor) or t.dim() != 1 or n not in (-1, t.shape[0]):
-                raise ValueError("src_slots and dst_slots must be int32 [n] tensors of one length")
-            n = t.shape[0]
-    if n < 0:
+def _slot_list(t, name, cur):
+    """(pointer, length) of a slot list."""
+    p = _on(t, name, torch.int32, None, cur)
+    s = t.shape
+    if len(s) != 1:
+        raise ValueError(f"{name} must be int32 [n]")
+    return p, s[0]
+
+
+def _entries(src_slots, dst_slots, src_rows, dst_rows, cur):
+    """(source list, destination list, entries) of a row call: the lists'
+    length, else every source row (which the destination must hold)."""
+    sp = dp = None
+    if src_slots is not None:
+        sp, n = _slot_list(src_slots, "src_slots", cur)
+        if dst_slots is not None:
+            dp, m = _slot_list(dst_slots, "dst_slots", cur)
+            if m != n:
+                raise ValueError("src_slots and dst_slots must be of one length")
+            return sp, dp, n
+    elif dst_slots is not None:
+        dp, n = _slot_list(dst_slots, "dst_slots", cur)
+    else:
         n = src_rows
     if (src_slots is None and n > src_rows) or (dst_slots is None and n > dst_rows):
         raise ValueError(f"{n} entries do not fit {src_rows} source / {dst_rows} destination rows")
-    return n
+    return sp, dp, n
 
 
 def hs_quant_rows(src, cache, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
@@ -609,30 +625,26 @@ def hs_quant_rows(src, cache, src_slots=None, dst_slots=None, status=None, strea
     of src (bf16 / f32 [rows][576]), quantised; without a list entry i is row
     i, negative slots are skipped."""
     cur = _device()
-    sp, dt, stride = _wide_rows(src, "src", cur)
-    dp = _q8_cache(cache, "cache", cur)
-    n = _slots(src_slots, dst_slots, src.shape[0], cache.shape[0])
+    sp, dt, stride, src_rows = _wide_rows(src, "src", cur)
+    dp, rows = _q8_cache(cache, "cache", cur)
+    ss, ds, n = _entries(src_slots, dst_slots, src_rows, rows, cur)
     _check(lib().hs_quant_rows(
-        sp, dt, stride, src.shape[0], dp, cache.shape[0],
-        _on(src_slots, "src_slots", torch.int32, None, cur, True),
-        _on(dst_slots, "dst_slots", torch.int32, None, cur, True), n,
-        _on(status, "status", torch.int32, (1,), cur, True), _on_stream(stream, cur)),
-        "hs_quant_rows")
+        sp, dt, stride, src_rows, dp, rows, ss, ds, n,
+        None if status is None else _on(status, "status", torch.int32, (1,), cur),
+        _on_stream(stream, cur)), "hs_quant_rows")
 
 
 def hs_dequant_rows(cache, dst, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
     """Row dst_slots[i] of dst (bf16 / f32 [rows][576]) = the values of row
     src_slots[i] of the q8 cache."""
     cur = _device()
-    sp = _q8_cache(cache, "cache", cur)
-    dp, dt, stride = _wide_rows(dst, "dst", cur)
-    n = _slots(src_slots, dst_slots, cache.shape[0], dst.shape[0])
+    sp, rows = _q8_cache(cache, "cache", cur)
+    dp, dt, stride, dst_rows = _wide_rows(dst, "dst", cur)
+    ss, ds, n = _entries(src_slots, dst_slots, rows, dst_rows, cur)
     _check(lib().hs_dequant_rows(
-        sp, cache.shape[0], dp, dt, stride, dst.shape[0],
-        _on(src_slots, "src_slots", torch.int32, None, cur, True),
-        _on(dst_slots, "dst_slots", torch.int32, None, cur, True), n,
-        _on(status, "status", torch.int32, (1,), cur, True), _on_stream(stream, cur)),
-        "hs_dequant_rows")
+        sp, rows, dp, dt, stride, dst_rows, ss, ds, n,
+        None if status is None else _on(status, "status", torch.int32, (1,), cur),
+        _on_stream(stream, cur)), "hs_dequant_rows")
 
 
 def hs_sparse_attn_decode_q8(q, kv, idx, scale: float, out, lse=None, workspace=None, status=None,
@@ -653,11 +665,11 @@ def hs_sparse_attn_decode_q8(q, kv, idx, scale: float, out, lse=None, workspace=
         _on(q, "q", torch.bfloat16, None, cur), _on(kv, "kv", torch.uint8, None, cur), kv.shape[0],
         _on(idx, "idx", torch.int32, (R, K), cur), R, H, K, float(scale),
         _on(out, "out", torch.bfloat16, (R, H, VALUE_DIM), cur),
-        _on(lse, "lse", torch.float32, (R, H), cur, True),
-        _on(workspace, "workspace", torch.uint8, None, cur, True),
-        workspace.numel() if workspace is not None else 0,
-        _on(status, "status", torch.int32, (1,), cur, True), _on_stream(stream, cur)),
-        "hs_sparse_attn_decode_q8")
+        None if lse is None else _on(lse, "lse", torch.float32, (R, H), cur),
+        None if workspace is None else _on(workspace, "workspace", torch.uint8, None, cur),
+        0 if workspace is None else workspace.numel(),
+        None if status is None else _on(status, "status", torch.int32, (1,), cur),
+        _on_stream(stream, cur)), "hs_sparse_attn_decode_q8")
 
 
 # --------------------------------------------- verification by sampling --
@@ -672,13 +684,14 @@ def _sample_args(cur, logits, temperature, draft_tokens, draft_probs, uniforms, 
     f32, i32 = torch.float32, torch.int32
     head = (_on(logits, "logits", logits.dtype, None, cur), _WIDE[logits.dtype], B, d, V,
             _on(temperature, "temperature", f32, (B,), cur),
-            _on(draft_tokens, "draft_tokens", i32, (B, d), cur, d == 0),
-            _on(draft_probs, "draft_probs", f32, (B, d, V), cur, True),
-            _on(uniforms, "uniforms", f32, (B, d), cur, d == 0),
+            None if d == 0 else _on(draft_tokens, "draft_tokens", i32, (B, d), cur),
+            None if draft_probs is None or d == 0 else _on(draft_probs, "draft_probs", f32,
+                                                           (B, d, V), cur),
+            None if d == 0 else _on(uniforms, "uniforms", f32, (B, d), cur),
             _on(noise, "noise", f32, (B, V), cur))
     tail = (_on(accept_len, "accept_len", i32, (B,), cur),
             _on(next_token, "next_token", i32, (B,), cur),
-            _on(logprob, "logprob", f32, (B, d1), cur, True))
+            None if logprob is None else _on(logprob, "logprob", f32, (B, d1), cur))
     return head, tail
 
 
@@ -691,7 +704,7 @@ def hs_verify_sample(logits, temperature, draft_tokens, draft_probs, uniforms, n
     head, tail = _sample_args(cur, logits, temperature, draft_tokens, draft_probs, uniforms, noise,
                               accept_len, next_token, logprob)
     _check(lib().hs_verify_sample(
-        *head, *tail, _on(status, "status", torch.int32, (1,), cur, True),
+        *head, *tail, None if status is None else _on(status, "status", torch.int32, (1,), cur),
         _on_stream(stream, cur)), "hs_verify_sample")
 
 
@@ -705,6 +718,6 @@ def hs_verify_sample_finalize(buf: HsBuffer, logits, temperature, draft_tokens, 
     B, d1, _ = logits.shape
     _check(lib().hs_verify_sample_finalize(
         buf.handle, *head, _on(step_kv, "step_kv", torch.bfloat16, (B, d1, LATENT_DIM), cur),
-        _on(req_ids, "req_ids", torch.int32, (B,), cur, True),
+        None if req_ids is None else _on(req_ids, "req_ids", torch.int32, (B,), cur),
         _on(kv_len, "kv_len", torch.int32, (buf.max_reqs,), cur), *tail,
         _on_stream(stream, cur)), "hs_verify_sample_finalize")
