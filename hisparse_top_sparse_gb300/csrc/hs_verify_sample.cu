@@ -34,10 +34,9 @@
 // overwrites the inputs during the call.
 //
 // Measured (bf16 logits, draft probabilities given): 256 requests x 3 drafts,
-// V = 129280: 94 us, 61 % of what the 385 MB it has to move take at the
-// measured copy rate (requests of unlike lengths: SMs are busy 79 % of the
-// time, at 5.6 TB/s); 64 x 3: 34 us; 1 x 3: 10 us and 2 x 3, V = 1024 f32: 6.4
-// us, latency.
+// V = 129280: 72 us, 80 % of what the 385 MB it has to move take at the
+// measured copy rate; 128 x 3: 45 us; 64 x 3: 26 us; 1 x 3: 9 us and 2 x 3, V =
+// 1024 f32: 6.4 us, latency.
 
 #include <float.h>
 
@@ -46,9 +45,9 @@
 namespace {
 
 constexpr int NT = 256;             // threads per block
-constexpr int MIN_BLOCKS = 4;       // blocks per SM, at least
+constexpr int MIN_BLOCKS = 3;       // blocks per SM, at least (80 registers, nothing spilled)
 constexpr int WARPS = NT / 32;
-constexpr int RING = 12;            // 16-byte places of a thread's ring of copies in flight
+constexpr int RING = 15;            // 16-byte places of a thread's ring of copies in flight
 constexpr int BATCH = 4;            // vectors of a row taken together
 constexpr int NB = 8;               // values of a thread in flight where rows are not aligned
 constexpr size_t RING_BYTES = (size_t)RING * NT * 16;
@@ -479,19 +478,19 @@ struct Race {
   float bar;               // the warp's best so far
 
   // (the whole warp; `big` is the largest of r, or 0 to take none)
-  template <int N>
-  __device__ __forceinline__ void group(const float (&r)[N], float big, int32_t v0, int32_t step) {
+  template <int N, typename At>
+  __device__ __forceinline__ void group(const float (&r)[N], float big, const At &index) {
     if (big >= bar && big > best) {
       best = big;
 #pragma unroll
       for (int j = N - 1; j >= 0; --j)
-        if (r[j] == big) at = (uint32_t)(v0 + j * step);      // the lowest of equals stays
+        if (r[j] == big) at = (uint32_t)index(j);      // indices ascend: the lowest of equals stays
     }
     bar = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(best)));
   }
 };
 
-template <int DTYPE, bool VEC>
+template <int DTYPE, bool VEC, bool HAS_Q>
 __device__ __forceinline__ Race race(const char *row, const float *q, const float *E, int32_t V,
                                      uint32_t rank, uint32_t log_n, const RaceRow &rr, uint4 *ring) {
   Race ra = {0.f, INT32_MAX, 0.f};
@@ -504,64 +503,77 @@ __device__ __forceinline__ Race race(const char *row, const float *q, const floa
     if (r == INFINITY) r = (rr.inv - w) * f;
   };
   if (VEC) {
-    // units of 16 bytes of logits and as many values of q and E, through the
-    // thread's ring places as in row_stat
-    constexpr int PER = Slice<DTYPE>::PER, QV = PER / 4, SLOTS = 1 + 2 * QV, DEPTH = RING / SLOTS;
+    // Units of 16 bytes of logits and as many values of q and E through the
+    // thread's ring places. A warp takes 32 neighbouring units at a time, each
+    // lane the groups of four values of which it copies E and q (group lane, and
+    // of bf16 logits group 32 + lane too), so that every copy of a warp is one
+    // contiguous piece: with a lane's eight values side by side its copies of E
+    // and q touched each 32-byte sector twice (94 us against 82 on 256 x 3
+    // drafts). A bf16 lane's logits are then the halves of two others' copies.
+    constexpr int PER = Slice<DTYPE>::PER, QV = PER / 4, SLOTS = 1 + (HAS_Q ? 2 : 1) * QV, DEPTH = RING / SLOTS;
     const int32_t units = V / PER;
     const int32_t lo = part_of(units, rank, log_n), hi = part_of(units, rank + 1, log_n);
-    const int32_t barred_unit = rr.barred >= 0 ? rr.barred / PER : -1;
-    auto issue = [&](int32_t k, int place) {
+    const int32_t lane = threadIdx.x & 31, warp0 = threadIdx.x & ~31;
+    // the first value of group j of the warp's units from u0 on, and whether its unit exists
+    auto value_at = [&](int32_t u0, int j) { return u0 * PER + 128 * j + 4 * lane; };
+    auto exists = [&](int32_t u0, int j) { return u0 + (32 * j + lane) / QV < hi; };
+    auto issue = [&](int32_t u0, int place) {
       uint4 *to = ring + place * SLOTS * NT;
-      if (k < hi) {
-        copy16(to, reinterpret_cast<const uint4 *>(row) + k);
+      if (u0 + lane < hi) copy16(to, reinterpret_cast<const uint4 *>(row) + u0 + lane);
 #pragma unroll
-        for (int j = 0; j < QV; ++j) {
-          copy16(to + (1 + j) * NT, reinterpret_cast<const uint4 *>(E) + QV * k + j);
-          if (q) copy16(to + (1 + QV + j) * NT, reinterpret_cast<const uint4 *>(q) + QV * k + j);
+      for (int j = 0; j < QV; ++j) {
+        if (exists(u0, j)) {
+          copy16(to + (1 + j) * NT, E + value_at(u0, j));
+          if (HAS_Q) copy16(to + (1 + QV + j) * NT, q + value_at(u0, j));
         }
       }
       copy_commit();
     };
 #pragma unroll
-    for (int p = 0; p < DEPTH; ++p) issue(lo + p * NT + (int)threadIdx.x, p);
+    for (int p = 0; p < DEPTH; ++p) issue(lo + p * NT + warp0, p);
     int place = 0;
-    for (int32_t k0 = lo; k0 < hi; k0 += NT) {
-      const int32_t k = k0 + (int)threadIdx.x;
+    for (int32_t u0 = lo + warp0; u0 < hi; u0 += NT) {       // the whole warp
       copy_wait<DEPTH - 1>();
+      __syncwarp();
       const uint4 *from = ring + place * SLOTS * NT;
-      const uint4 x = from[0];
+      float r[PER], big = 0.f;
       uint4 e4[QV], w4[QV];
 #pragma unroll
       for (int j = 0; j < QV; ++j) {
+        uint4 x = from[0];
+        if (DTYPE == HS_LOGITS_BF16) {
+          const uint2 half = reinterpret_cast<const uint2 *>(from - lane)[32 * j + lane];
+          x = make_uint4(half.x, half.y, 0, 0);
+        }
         e4[j] = from[(1 + j) * NT];
-        w4[j] = q ? from[(1 + QV + j) * NT] : make_uint4(0, 0, 0, 0);
-      }
-      issue(k + DEPTH * NT, place);
-      place = place + 1 == DEPTH ? 0 : place + 1;
-      float r[PER], big = 0.f;
-#pragma unroll
-      for (int j = 0; j < QV; ++j) {
+        w4[j] = HAS_Q ? from[(1 + QV + j) * NT] : make_uint4(0, 0, 0, 0);
+        const bool here = exists(u0, j);       // (else: what the places held)
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           const int o = 4 * j + i;
-          ratio2(pack2(value<DTYPE>(x, o), value<DTYPE>(x, o + 1)),
+          ratio2(pack2(value<DTYPE>(x, i), value<DTYPE>(x, i + 1)),
                  pack2(-value<HS_LOGITS_F32>(w4[j], i), -value<HS_LOGITS_F32>(w4[j], i + 1)),
                  value<HS_LOGITS_F32>(e4[j], i), value<HS_LOGITS_F32>(e4[j], i + 1), nm, cc, ii, r[o],
                  r[o + 1]);
+          r[o] = here ? r[o] : 0.f;
+          r[o + 1] = here ? r[o + 1] : 0.f;
           big = fmaxf(big, fmaxf(r[o], r[o + 1]));
         }
       }
-      if (k == barred_unit || big == INFINITY) {
-#pragma unroll
-        for (int o = 0; o < PER; ++o) {
-          mend(r[o], value<HS_LOGITS_F32>(w4[o / 4], o), value<HS_LOGITS_F32>(e4[o / 4], o));
-          if (k * PER + o == rr.barred) r[o] = 0.f;
-        }
+      __syncwarp();
+      issue(u0 + DEPTH * NT, place);
+      place = place + 1 == DEPTH ? 0 : place + 1;
+      const bool barred_here = rr.barred >= u0 * PER && rr.barred < (u0 + 32) * PER;
+      if (barred_here || big == INFINITY) {
         big = 0.f;
 #pragma unroll
-        for (int o = 0; o < PER; ++o) big = fmaxf(big, r[o]);
+        for (int o = 0; o < PER; ++o) {
+          mend(r[o], value<HS_LOGITS_F32>(w4[o / 4], o & 3), value<HS_LOGITS_F32>(e4[o / 4], o & 3));
+          if (value_at(u0, o / 4) + (o & 3) == rr.barred) r[o] = 0.f;
+          big = fmaxf(big, r[o]);
+        }
       }
-      ra.group(r, k < hi ? big : 0.f, k * PER, 1);      // (past the end: what the places held)
+      ra.template group<PER>(r, big, [&](int o) { return value_at(u0, o / 4) + (o & 3); });
     }
     copy_wait<0>();
   } else {
@@ -579,7 +591,7 @@ __device__ __forceinline__ Race race(const char *row, const float *q, const floa
                      ? __ldg(reinterpret_cast<const float *>(row) + v)
                      : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(row) + v) << 16);
           e[u] = __ldcs(E + v);
-          if (q) w[u] = __ldcs(q + v);
+          if (HAS_Q) w[u] = __ldcs(q + v);
         }
       }
 #pragma unroll
@@ -598,7 +610,7 @@ __device__ __forceinline__ Race race(const char *row, const float *q, const floa
 #pragma unroll
         for (int u = 0; u < NB; ++u) big = fmaxf(big, r[u]);
       }
-      ra.group(r, big, v0, NT);
+      ra.template group<NB>(r, big, [&](int u) { return v0 + u * NT; });
     }
   }
   return ra;
@@ -707,8 +719,13 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
     int32_t barred = !sa.probs && m < d ? sh.draft[m] : -1;   // a sure draft's own token
     for (;;) {
       const RaceRow rr = {top, c, inv, barred};
-      Race ra = sa.aligned ? race<DTYPE, true>(row, q, E, V, rank, log_n, rr, ring)
-                           : race<DTYPE, false>(row, q, E, V, rank, log_n, rr, ring);
+      Race ra;
+      if (sa.aligned)
+        ra = q ? race<DTYPE, true, true>(row, q, E, V, rank, log_n, rr, ring)
+               : race<DTYPE, true, false>(row, q, E, V, rank, log_n, rr, ring);
+      else
+        ra = q ? race<DTYPE, false, true>(row, q, E, V, rank, log_n, rr, ring)
+               : race<DTYPE, false, false>(row, q, E, V, rank, log_n, rr, ring);
       cluster_join(sh, ra.best, ra.at, rank, n, 0, turn, BestOp{});
       if (ra.at != INT32_MAX) {
         token = (int32_t)ra.at;
@@ -758,15 +775,14 @@ int check_sample(const void *logits, int32_t dtype, int32_t B, int32_t d, int32_
 //
 // A cluster that takes its rows one after the other reads no row behind the
 // refusal, but each row costs a few microseconds of latency (the first loads,
-// the joins). So while few blocks run, up to four rows are taken side by side
-// (2 x 3 drafts, V = 1024: 6.3 us against 9.8; 33 x 5, V = 50257: 16 against
-// 23); at half of the resident blocks two (64 x 3, V = 129280: 34 us against 36
-// for one or four); with the device full, one. The blocks of a request
-// grow to eight while all of them fit at once and a part keeps 2048 values,
-// to sixteen while each has an SM of its own (1 x 3, V = 129280: 10.3 us
-// against 12.3), and to eight past one wave (a second wave evens out requests
-// of different lengths) while a part keeps 16384 (256 x 3, V = 129280: 94 us
-// with four blocks, 99 with two; V = 32000: 44 with four, 33 with two).
+// the joins). So while the blocks leave a third of the device free, up to four
+// rows are taken side by side (2 x 3 drafts, V = 1024: 6.4 us against 9.8; 33 x
+// 5, V = 50257: 13.8 against 23; 64 x 3, V = 129280: 26.2 against 28.7), while
+// all blocks run at once two (96 x 3, V = 50257: 24.7 us against 26.2), else
+// one. The blocks of a request double, to eight, while all blocks run at once
+// and a part of a row keeps 2048 values, and to sixteen while each has an SM
+// of its own (1 x 3, V = 129280: 9.1 us against 10.9). Not past that: 256 x 3,
+// V = 129280 takes 72 us with one block, 82 with two, 77 with four.
 int cluster_shape(int32_t B, int32_t d, int32_t V, int *n, int *g) {
   int sms = 0;
   int rc = hs_sm_count(&sms);
@@ -777,8 +793,7 @@ int cluster_shape(int32_t B, int32_t d, int32_t V, int *n, int *g) {
   while (k < MAX_CLUSTER && (int64_t)B * 2 * k <= (k < 8 ? at_once : (int64_t)sms) &&
          (k < most || (int64_t)V * most / (2 * k) >= 2048))
     k *= 2;
-  while (k < 8 && (int64_t)B * 2 * k <= 2 * at_once && V / (2 * k) >= 16384) k *= 2;
-  int r = (int64_t)B * k <= at_once / 2 ? most : (int64_t)B * k <= at_once ? 2 : 1;
+  int r = (int64_t)B * k <= 2 * (int64_t)sms ? most : (int64_t)B * k <= at_once ? 2 : 1;
   if (r > most) r = most;
   if (r > k) r = k;
   *n = k;
