@@ -10,10 +10,11 @@
 // codes is contiguous over the warp; a group of 32 dims is 32 / VEC
 // neighbouring lanes, whose largest magnitude and scale byte take shuffles
 // only. A warp has two rows in flight in bf16, one in f32 (its registers hold
-// no more), 32 warps on an SM. Measured, scattered slots: 262144 bf16 rows
-// quantised and read back 176 us (81 % of the measured copy rate for the bytes
-// both move; one row in flight 183, four 211), 131072 rows read back to bf16
-// 41 us (87 %), 131072 f32 rows there and back 126 us (137 with two rows in flight).
+// no more), 32 warps on an SM, and loads its next slots meanwhile. Measured,
+// scattered slots: 262144 bf16 rows quantised and read back 165 us, 86 % of the
+// measured copy rate for the bytes both move (slots not loaded ahead 178, one
+// row in flight 180, 40 warps 193); 131072 rows read back to bf16 40 us (89 %),
+// 131072 f32 rows there and back 128 us.
 
 #include <type_traits>
 
@@ -22,7 +23,7 @@
 namespace {
 
 constexpr int QT_THREADS = 256;
-constexpr int QT_BLOCKS = 4;    // blocks per SM, at most
+constexpr int QT_BLOCKS = 4;    // blocks per SM, at most and at least
 
 template <typename T>
 struct Lay {
@@ -48,11 +49,25 @@ __device__ __forceinline__ void unpack(const uint4 w, float (&f)[Lay<T>::VEC]) {
   }
 }
 
-// Row of entry i on one side: slots[i], or i itself without a list. -1: no
-// entry; a slot at or past `rows` gives -1 and sets bad.
-__device__ __forceinline__ int64_t row_of(const int32_t *slots, int64_t i, int64_t rows, bool &bad) {
-  const int64_t s = slots ? (int64_t)__ldg(slots + i) : i;
-  if (s < 0) return -1;
+// The slots of a warp's next rows, loaded while the rows before them are on
+// their way: entries base, base + step, ...; without a list entry i is row i;
+// -1 past the last.
+template <int ROWS>
+struct Slots {
+  int32_t s[ROWS], d[ROWS];
+  __device__ __forceinline__ Slots(const int32_t *src_slots, const int32_t *dst_slots, int64_t base,
+                                   int64_t step, int32_t n) {
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+      const int64_t i = base + u * step;
+      s[u] = i >= n ? -1 : src_slots ? __ldg(src_slots + i) : (int32_t)i;
+      d[u] = i >= n ? -1 : dst_slots ? __ldg(dst_slots + i) : (int32_t)i;
+    }
+  }
+};
+
+// -1: no entry; a slot at or past `rows` gives -1 and sets bad.
+__device__ __forceinline__ int64_t row_of(int32_t s, int64_t rows, bool &bad) {
   if (s >= rows) {
     bad = true;
     return -1;
@@ -61,7 +76,7 @@ __device__ __forceinline__ int64_t row_of(const int32_t *slots, int64_t i, int64
 }
 
 template <typename T>
-__global__ void __launch_bounds__(QT_THREADS) k_quant_rows(
+__global__ void __launch_bounds__(QT_THREADS, QT_BLOCKS) k_quant_rows(
     const char *__restrict__ src, int64_t src_stride, int64_t src_rows, char *__restrict__ dst,
     int64_t dst_rows, const int32_t *__restrict__ src_slots, const int32_t *__restrict__ dst_slots,
     int32_t n, uint32_t *status) {
@@ -70,22 +85,22 @@ __global__ void __launch_bounds__(QT_THREADS) k_quant_rows(
   const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
   bool bad = false;
+  Slots<L::ROWS> next(src_slots, dst_slots, warp, n_warps, n);
   for (int64_t base = warp; base < n; base += n_warps * L::ROWS) {
     char *d[L::ROWS];
     uint4 w[L::ROWS][L::PASSES], rope[L::ROWS];
+    const Slots<L::ROWS> here = next;
+    next = Slots<L::ROWS>(src_slots, dst_slots, base + n_warps * L::ROWS, n_warps, n);
 #pragma unroll
     for (int u = 0; u < L::ROWS; ++u) {
-      const int64_t i = base + u * n_warps;
       d[u] = nullptr;
-      if (i < n) {
-        const int64_t s = row_of(src_slots, i, src_rows, bad), t = row_of(dst_slots, i, dst_rows, bad);
-        if (s >= 0 && t >= 0) {
-          d[u] = dst + t * HS_Q8_ROW_BYTES;
-          const uint4 *p = reinterpret_cast<const uint4 *>(src + s * src_stride) + lane;
+      const int64_t s = row_of(here.s[u], src_rows, bad), t = row_of(here.d[u], dst_rows, bad);
+      if (s >= 0 && t >= 0) {
+        d[u] = dst + t * HS_Q8_ROW_BYTES;
+        const uint4 *p = reinterpret_cast<const uint4 *>(src + s * src_stride) + lane;
 #pragma unroll
-          for (int k = 0; k < L::PASSES; ++k) w[u][k] = __ldcs(p + 32 * k);
-          if (lane < L::ROPE_LANES) rope[u] = __ldcs(p + 32 * L::PASSES);
-        }
+        for (int k = 0; k < L::PASSES; ++k) w[u][k] = __ldcs(p + 32 * k);
+        if (lane < L::ROPE_LANES) rope[u] = __ldcs(p + 32 * L::PASSES);
       }
     }
 #pragma unroll
@@ -143,7 +158,7 @@ __global__ void __launch_bounds__(QT_THREADS) k_quant_rows(
 }
 
 template <typename T>
-__global__ void __launch_bounds__(QT_THREADS) k_dequant_rows(
+__global__ void __launch_bounds__(QT_THREADS, QT_BLOCKS) k_dequant_rows(
     const char *__restrict__ src, int64_t src_rows, char *__restrict__ dst, int64_t dst_stride,
     int64_t dst_rows, const int32_t *__restrict__ src_slots, const int32_t *__restrict__ dst_slots,
     int32_t n, uint32_t *status) {
@@ -153,31 +168,31 @@ __global__ void __launch_bounds__(QT_THREADS) k_dequant_rows(
   const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
   bool bad = false;
+  Slots<L::ROWS> next(src_slots, dst_slots, warp, n_warps, n);
   for (int64_t base = warp; base < n; base += n_warps * L::ROWS) {
     char *d[L::ROWS];
     Code c[L::ROWS][L::PASSES], rope_lo[L::ROWS], rope_hi[L::ROWS];
     uint32_t e[L::ROWS][L::PASSES];
+    const Slots<L::ROWS> here = next;
+    next = Slots<L::ROWS>(src_slots, dst_slots, base + n_warps * L::ROWS, n_warps, n);
 #pragma unroll
     for (int u = 0; u < L::ROWS; ++u) {
-      const int64_t i = base + u * n_warps;
       d[u] = nullptr;
-      if (i < n) {
-        const int64_t s = row_of(src_slots, i, src_rows, bad), t = row_of(dst_slots, i, dst_rows, bad);
-        if (s >= 0 && t >= 0) {
-          d[u] = dst + t * dst_stride;
-          const char *row = src + s * HS_Q8_ROW_BYTES;
-          const Code *p = reinterpret_cast<const Code *>(row) + lane;
+      const int64_t s = row_of(here.s[u], src_rows, bad), t = row_of(here.d[u], dst_rows, bad);
+      if (s >= 0 && t >= 0) {
+        d[u] = dst + t * dst_stride;
+        const char *row = src + s * HS_Q8_ROW_BYTES;
+        const Code *p = reinterpret_cast<const Code *>(row) + lane;
 #pragma unroll
-          for (int k = 0; k < L::PASSES; ++k) {
-            c[u][k] = __ldg(p + 32 * k);
-            e[u][k] = __ldg(reinterpret_cast<const unsigned char *>(row) + Q8_SCALE_OFF +
-                            (32 * k + lane) / L::GL);
-          }
-          if (lane < L::ROPE_LANES) {             // VEC bf16 dims per lane: two Code words
-            const Code *rp = reinterpret_cast<const Code *>(row + Q8_ROPE_OFF) + 2 * lane;
-            rope_lo[u] = __ldg(rp);
-            rope_hi[u] = __ldg(rp + 1);
-          }
+        for (int k = 0; k < L::PASSES; ++k) {
+          c[u][k] = __ldg(p + 32 * k);
+          e[u][k] = __ldg(reinterpret_cast<const unsigned char *>(row) + Q8_SCALE_OFF +
+                          (32 * k + lane) / L::GL);
+        }
+        if (lane < L::ROPE_LANES) {             // VEC bf16 dims per lane: two Code words
+          const Code *rp = reinterpret_cast<const Code *>(row + Q8_ROPE_OFF) + 2 * lane;
+          rope_lo[u] = __ldg(rp);
+          rope_hi[u] = __ldg(rp + 1);
         }
       }
     }
