@@ -76,6 +76,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "hs_q8.cuh"
 
 namespace {
@@ -1257,7 +1259,7 @@ extern "C" int hs_wait_probe(uint32_t *status, int64_t max_cycles, hs_stream_t s
 static int set_attn_attributes() {
   int dev = 0;
   HS_CUDA_TRY(cudaGetDevice(&dev));
-  static bool attr_done[64] = {false};
+  static std::atomic<bool> attr_done[64];
   if (dev >= 64 || !attr_done[dev]) {
     HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Lay<false>::SMEM_ALLOC));
@@ -1475,6 +1477,8 @@ extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n
                                         hs_stream_t stream) {
   if ((uintptr_t)workspace & 15)
     return hs_set_error(HS_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  if (((uintptr_t)idx | (uintptr_t)lse | (uintptr_t)status) & 3)
+    return hs_set_error(HS_ERR_INVALID_ARG, "idx, lse and status must be 4-byte aligned");
   // the softmax reference is the scaled maximum, which a negative scale would not give
   if (!(scale >= 0.f) || scale > FLT_MAX)
     return hs_set_error(HS_ERR_INVALID_ARG, "scale must be finite and not negative");

@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(QT_THREADS, QT_BLOCKS) k_dequant_rows(
 
 // Checks shared by both directions; wide: the bf16 / f32 side, q8: the other.
 int check_rows(const void *wide, int32_t dtype, int64_t wide_stride, int64_t wide_rows, const void *q8,
-               int64_t q8_rows, int32_t n, const void **wide_dev, const void **q8_dev) {
+               int64_t q8_rows, const int32_t *src_slots, const int32_t *dst_slots,
+               const uint32_t *status, int32_t n, const void **wide_dev, const void **q8_dev) {
   if (dtype != HS_LOGITS_F32 && dtype != HS_LOGITS_BF16)
     return hs_set_error(HS_ERR_INVALID_ARG, "row dtype %d", dtype);
   const int64_t elem = dtype == HS_LOGITS_F32 ? 4 : 2;
@@ -241,6 +242,8 @@ int check_rows(const void *wide, int32_t dtype, int64_t wide_stride, int64_t wid
   if (n == 0) return HS_OK;
   if (!wide || !q8 || (((uintptr_t)wide | (uintptr_t)q8) & 15))
     return hs_set_error(HS_ERR_INVALID_ARG, "src and dst must be 16-byte aligned and not NULL");
+  if (((uintptr_t)src_slots | (uintptr_t)dst_slots | (uintptr_t)status) & 3)
+    return hs_set_error(HS_ERR_INVALID_ARG, "slot lists and status must be 4-byte aligned");
   int rc = hs_device_alias(wide, wide_dev, "the bf16 / f32 rows");
   if (rc) return rc;
   return hs_device_alias(q8, q8_dev, "the q8 rows");
@@ -263,7 +266,8 @@ extern "C" int hs_quant_rows(const void *src, int32_t src_dtype, int64_t src_str
                              const int32_t *dst_slots, int32_t n, uint32_t *status,
                              hs_stream_t stream) {
   const void *s = nullptr, *d = nullptr;
-  int rc = check_rows(src, src_dtype, src_stride, src_rows, dst, dst_rows, n, &s, &d);
+  int rc = check_rows(src, src_dtype, src_stride, src_rows, dst, dst_rows, src_slots, dst_slots,
+                      status, n, &s, &d);
   if (rc || n == 0) return rc;
   int blocks = 0;
   if ((rc = row_blocks(n, &blocks))) return rc;
@@ -284,7 +288,8 @@ extern "C" int hs_dequant_rows(const void *src, int64_t src_rows, void *dst, int
                                const int32_t *dst_slots, int32_t n, uint32_t *status,
                                hs_stream_t stream) {
   const void *s = nullptr, *d = nullptr;
-  int rc = check_rows(dst, dst_dtype, dst_stride, dst_rows, src, src_rows, n, &d, &s);
+  int rc = check_rows(dst, dst_dtype, dst_stride, dst_rows, src, src_rows, src_slots, dst_slots,
+                      status, n, &d, &s);
   if (rc || n == 0) return rc;
   int blocks = 0;
   if ((rc = row_blocks(n, &blocks))) return rc;

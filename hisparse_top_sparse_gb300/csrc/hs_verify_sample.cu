@@ -40,6 +40,8 @@
 
 #include <float.h>
 
+#include <atomic>
+
 #include "hs_commit.cuh"
 
 namespace {
@@ -756,7 +758,7 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
 int check_sample(const void *logits, int32_t dtype, int32_t B, int32_t d, int32_t V,
                  const float *temperature, const int32_t *drafts, const float *probs,
                  const float *uniforms, const float *noise, const int32_t *accept_len,
-                 const int32_t *next_token) {
+                 const int32_t *next_token, const float *logprob, const uint32_t *status) {
   if (B < 1 || d < 0 || d > MAX_DRAFTS || V < 1 || V > 1 << 30)
     return hs_set_error(HS_ERR_INVALID_ARG, "bad sizes B=%d d=%d (0..%d) V=%d (1..2^30)", B, d,
                         MAX_DRAFTS, V);
@@ -765,8 +767,10 @@ int check_sample(const void *logits, int32_t dtype, int32_t B, int32_t d, int32_
   if (!logits || !temperature || (d > 0 && (!drafts || !uniforms)) || !noise || !accept_len || !next_token)
     return hs_set_error(HS_ERR_INVALID_ARG, "NULL argument");
   const uintptr_t elem = dtype == HS_LOGITS_F32 ? 4 : 2;
-  if ((uintptr_t)logits % elem || (((uintptr_t)temperature | (uintptr_t)probs | (uintptr_t)uniforms |
-                                    (uintptr_t)noise) & 3))
+  if ((uintptr_t)logits % elem ||
+      (((uintptr_t)temperature | (uintptr_t)drafts | (uintptr_t)probs | (uintptr_t)uniforms |
+        (uintptr_t)noise | (uintptr_t)accept_len | (uintptr_t)next_token | (uintptr_t)logprob |
+        (uintptr_t)status) & 3))
     return hs_set_error(HS_ERR_INVALID_ARG, "an array is not aligned to its elements");
   return HS_OK;
 }
@@ -824,7 +828,7 @@ int launch(SampleArgs &sa, int32_t dtype, int32_t B, const CommitArgs &ca, cudaS
   cfg.numAttrs = 1;
   int dev = 0;
   HS_CUDA_TRY(cudaGetDevice(&dev));
-  static bool attr_done[64] = {false};
+  static std::atomic<bool> attr_done[64];
   if (dev >= 64 || !attr_done[dev]) {
     HS_CUDA_TRY(cudaFuncSetAttribute(k_verify_sample<HS_LOGITS_F32, COMMIT>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES));
@@ -853,7 +857,7 @@ extern "C" int hs_verify_sample(const void *logits, int32_t logits_dtype, int32_
                                 int32_t *accept_len, int32_t *next_token, float *logprob,
                                 uint32_t *status, hs_stream_t stream) {
   int rc = check_sample(logits, logits_dtype, B, d, V, temperature, draft_tokens, draft_probs,
-                        uniforms, noise, accept_len, next_token);
+                        uniforms, noise, accept_len, next_token, logprob, status);
   if (rc) return rc;
   SampleArgs sa = {logits,   d,     V,          temperature, draft_tokens, draft_probs,
                          uniforms, noise, accept_len, next_token,  logprob,      status, 0, false};
@@ -870,14 +874,14 @@ extern "C" int hs_verify_sample_finalize(hs_buffer *buf, const void *logits, int
   int rc = hs_check_buffer(buf);
   if (rc) return rc;
   rc = check_sample(logits, logits_dtype, B, d, V, temperature, draft_tokens, draft_probs, uniforms,
-                    noise, accept_len, next_token);
+                    noise, accept_len, next_token, logprob, nullptr);
   if (rc) return rc;
   if (B > buf->max_reqs || d + 1 > buf->n_step)
     return hs_set_error(HS_ERR_INVALID_ARG, "bad sizes B=%d (1..%d) d=%d (d+1<=%d)", B, buf->max_reqs,
                         d, buf->n_step);
   if (!step_kv || !kv_len) return hs_set_error(HS_ERR_INVALID_ARG, "NULL argument");
-  if ((uintptr_t)step_kv & 15)
-    return hs_set_error(HS_ERR_INVALID_ARG, "step_kv must be 16-byte aligned");
+  if (((uintptr_t)step_kv & 15) || (((uintptr_t)req_ids | (uintptr_t)kv_len) & 3))
+    return hs_set_error(HS_ERR_INVALID_ARG, "step_kv must be 16-byte aligned, req_ids and kv_len to 4");
   // A commit is told from a repeated one by the host's clock, which a
   // replayed graph does not advance: its second run would commit nothing.
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;

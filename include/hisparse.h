@@ -300,7 +300,7 @@ int hs_sparse_attn_decode(const void *q, const void *kv, int64_t n_kv_rows,
  *   src_slots, dst_slots  device int32 [n] or NULL (entry i is row i)
  *   status      device uint32 or NULL
  * Requirements: n >= 0, src_stride >= 576, src, dst and src_stride in bytes
- * multiples of 16.
+ * multiples of 16; src and dst do not overlap.
  */
 int hs_quant_rows(const void *src, int32_t src_dtype, int64_t src_stride, int64_t src_rows,
                   void *dst, int64_t dst_rows, const int32_t *src_slots,
@@ -653,7 +653,8 @@ int hs_verify_accept_noalloc(const void *logits, int32_t logits_dtype, int32_t B
  *     m < d (p_m itself if that is 0 everywhere) and w = p_d when m = d.
  * With uniforms uniform in [0, 1) and noise exponentially distributed (mean
  * 1), all independent of the drafts, the tokens are distributed as if sampled
- * from p one by one. draft_probs NULL: the drafts were chosen outright, q_i is
+ * from p one by one. p, w and the quotients are f32 (quotients within a few
+ * 2^-23 of each other may change places). draft_probs NULL: the drafts were chosen outright, q_i is
  * 1 at the draft and 0 elsewhere.
  * T <= 0 (or NaN) verifies the entry greedily, as hs_verify_finalize does; its
  * numbers are not used.

@@ -145,6 +145,16 @@ def test_refusals_without_a_gpu():
     for k in "ltxuean":
         assert sample(**{k: None}) == bad
     assert sample(l=P(18)) == bad and sample(dt=1, l=P(17)) == bad and sample(q=P(18)) == bad
+    for k in "txueanq":
+        assert sample(**{k: P(18)}) == bad
+    for lp, st in ((P(18), None), (None, P(18))):
+        assert L.hs_verify_sample(P(16), 0, 1, 1, 8, P(16), P(16), None, P(16), P(16), P(16), P(16), lp, st,
+                                  None) == bad
+        assert L.hs_sparse_attn_decode_q8(P(16), P(16), 4, P(16), 1, 1, 1, ctypes.c_float(1.0), P(16), lp,
+                                          None, 0, st, None) == bad
+    for ss, ds, st in ((P(18), None, None), (None, P(18), None), (None, None, P(18))):
+        assert L.hs_quant_rows(P(16), 1, 576, 4, P(16), 4, ss, ds, 1, st, None) == bad
+        assert L.hs_dequant_rows(P(16), 4, P(16), 1, 576, 4, ss, ds, 1, st, None) == bad
     assert L.hs_verify_sample_finalize(None, P(16), 0, 1, 0, 8, P(16), None, None, None, P(16), P(16),
                                        None, P(16), P(16), P(16), None, None) == bad
 
