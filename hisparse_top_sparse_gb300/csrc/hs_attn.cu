@@ -57,9 +57,8 @@
 // bf16, so the output is bit for bit that of the bf16 kernel over the rows read
 // back. Four more warps and different rings bring the rows in: they land raw,
 // 656 bytes instead of 1152, and are decoded into the slots. Measured, 128 rows
-// x 128 heads x 2048 keys: 95.5 us, a tile pair per 1.2 us against 1.0 in the
-// bf16 kernel (84 us; with rows that need no gathering or decoding the rest
-// takes 77). A slot of ring VO is held from the decoding (0.5 us) through Q K^T,
+// x 128 heads x 2048 keys: 94 us, a tile pair per 1.2 us against 1.0 in the
+// bf16 kernel (80 us). A slot of ring VO is held from the decoding (0.5 us) through Q K^T,
 // softmax and its P V, about 2.9 pairs, and three fit beside the raw rings.
 // Rows decoded by the gather warps of both kinds of tile in turn: 124 us;
 // rows loaded into registers one tile ahead: 112, two ahead: 137.
@@ -194,16 +193,17 @@ enum {
   B_VOTE = B_XEND + 2,                // the four softmax warps have voted for a second pass
   B_DECIDE = B_VOTE + 1,              // softmax -> other roles: second pass or not
   B_OFULL = B_DECIDE + 1,             // all P V of a pass done (one per pass)
-  B_QLOAD = B_OFULL + 2,              // Q landed (9 x 16 KB by tensor copies)
-  B_QSTAGED = B_QLOAD + 1,            // Q dims 0..383 are in TMEM (4 softmax warps)
+  B_QLOAD = B_OFULL + 2,              // Q landed, two 64-dim blocks each, then the last three
+  B_QSTAGED = B_QLOAD + 4,            // Q dims 0..383 are in TMEM
   B_COUNT = B_QSTAGED + 1
 };
 static_assert(B_COUNT * 8 + 16 <= 512, "barrier area");
-// O staged for the epilogue's stores: four 16 KB blocks over ring A and the
-// start of ring VO (free once the last P V is done)
-constexpr int O_STG_OFF = RA_OFF;
-static_assert(O_STG_OFF + 8 * 32 * 272 <= Lay<true>::XS_OFF && O_STG_OFF + 4 * HG * 128 <= Lay<false>::XS_OFF &&
-                  O_STG_OFF + 4 * HG * 128 <= Lay<true>::XS_OFF, "O staging");
+// O staged for the epilogue's tensor copies, blocks of 32 rows x 128 bytes (two
+// a warp in bf16, four in f32) over Q and rings A and VO (free once the last
+// P V is done)
+constexpr int O_STG_OFF = QS_OFF, O_BLOCK = 32 * 128;
+static_assert(O_STG_OFF % 1024 == 0 && O_STG_OFF + 8 * 4 * O_BLOCK <= Lay<true>::XS_OFF &&
+                  O_STG_OFF + 8 * 2 * O_BLOCK <= Lay<false>::XS_OFF, "O staging");
 
 constexpr int WAIT_LIMIT = 1 << 24;
 
@@ -420,9 +420,9 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
-                   : "memory");
+// both halves, without the release and the acquire: nobody's writes are waited for
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
 }
 // 8 / 4 bytes into the peer's shared memory; the peer's mbarrier `rbar`
 // counts the bytes when they land
@@ -446,6 +446,19 @@ __device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_
           dst),
       "r"(src), "r"(bytes), "r"(rbar)
       : "memory");
+}
+// a block of shared memory to coordinates (x, y, z) of a tensor; a thread's
+// copies so far form a group, which bulk_wait_read waits for: their sources
+// have been read
+__device__ __forceinline__ void tensor_store(const CUtensorMap *map, const void *src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"((uint32_t)__cvta_generic_to_shared(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
 }
 // this thread's arrival plus the bytes still to come in the current phase
 __device__ __forceinline__ void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
@@ -483,7 +496,7 @@ struct Parts {
 
 template <bool Q8>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MAX_REGS)
-    k_attn_pair(const __grid_constant__ CUtensorMap tmap_q,
+    k_attn_pair(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_o,
                 const char *__restrict__ q,
                 const char *__restrict__ kv_res, int64_t n_res, const char *__restrict__ kv_hot,
                 int64_t n_hot, const int32_t *__restrict__ row_req,
@@ -526,10 +539,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
   };
 
   if (warp == 1) {
-    // one barrier per lane: its arrival count
-    static_assert(B_COUNT <= 32, "one lane per barrier");
-    if (lane < B_COUNT) {
-      const int i = lane;
+    // every barrier's arrival count
+    for (int i = lane; i < B_COUNT; i += 32) {
       const bool prod = i >= B_FULLA && i < B_FULLA + MAX_RA;
       const bool half = i >= B_FULLVP && i < B_FULLVP + MAX_VP;
       const bool four = (i >= B_PFULL && i < B_PFULL + NSB) || i == B_VOTE;
@@ -566,16 +577,22 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
   // own and the first peer tiles are gathered while Q comes in.
   // The copies are issued by the P V issuer warp, whose first MMA waits for
   // the first P anyway: issuing them can stall the issuing thread for
-  // microseconds while the other CTAs of the wave load their Q.
+  // microseconds while the other CTAs of the wave load their Q. They land on
+  // four barriers, so that the first dims move into TMEM while the others come.
+  // (Tried: each CTA copying half of Q to both by multicast, and copies issued
+  // before the CTA's first barrier: no faster.)
   if (warp == 12 + NSB && lane == 0) {
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-    arrive_expect_tx(bar(B_QLOAD), 9 * HG * 128);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) arrive_expect_tx(bar(B_QLOAD + g), (g < 3 ? 2 : 3) * HG * 128);
+#pragma unroll
     for (int a = 0; a < D / 64; ++a) {
       const uint32_t dst = a < 6 ? sbase + L::q_stage_off(a) : sbase + QS_OFF + (a - 6) * (HG * 128);
+      const uint32_t b = bar(B_QLOAD + (a < 6 ? a >> 1 : 3));
       asm volatile(
           "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
           " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
-          "l"(reinterpret_cast<uint64_t>(&tmap_q)), "r"(64 * a), "r"(h0), "r"(r), "r"(bar(B_QLOAD))
+          "l"(reinterpret_cast<uint64_t>(&tmap_q)), "r"(64 * a), "r"(h0), "r"(r), "r"(b)
           : "memory");
     }
   }
@@ -587,16 +604,21 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     // per 16-dim slice (the slice the MMA would read from shared memory),
     // issued by one lane; their completion (B_QSTAGED) frees the staging
     // slots for KV tiles and lets the Q K^T issuers start
-    if (!warp_wait(bar(B_QLOAD), 0)) timed_out = true;
-    fence_after();
-    if (elect_one()) {
-#pragma unroll 1
-      for (int kk = 0; kk < QT_DIMS / 16; ++kk)
-        asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;\n" ::"r"(tmem + COL_Q + kk * 8),
-                     "l"(sdesc(sbase + L::q_stage_off(kk >> 2) + (kk & 3) * 32, 16, 1024))
-                     : "memory");
-      mma_commit(bar(B_QSTAGED));
+    const bool one = elect_one();
+#pragma unroll
+    for (int g = 0; g < QT_DIMS / 128; ++g) {
+      if (!warp_wait(bar(B_QLOAD + g), 0)) timed_out = true;
+      fence_after();
+      if (one) {
+#pragma unroll
+        for (int kk = 8 * g; kk < 8 * g + 8; ++kk)
+          asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;\n" ::"r"(tmem + COL_Q + kk * 8),
+                       "l"(sdesc(sbase + L::q_stage_off(kk >> 2) + (kk & 3) * 32, 16, 1024))
+                       : "memory");
+      }
+      __syncwarp();
     }
+    if (one) mma_commit(bar(B_QSTAGED));
     __syncwarp();
   }
 
@@ -875,7 +897,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     {
       const uint32_t qs0 = sbase + QS_OFF;
       const int b = warp - 12;
-      bool ok = warp_wait(bar(B_QSTAGED), 0);   // Q dims 0..383 in TMEM
+      // Q dims 0..383 in TMEM, the others in shared memory
+      bool ok = warp_wait(bar(B_QSTAGED), 0) && warp_wait(bar(B_QLOAD + 3), 0);
       fence_after();
       for (int pass = 0; pass < 2 && ok; ++pass) {
         if (pass == 1) {
@@ -1006,6 +1029,13 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     for (int pass = 0; pass < 2 && !timed_out; ++pass) {
       if (tid == 0) arrive_expect_tx(bar(B_XEND + pass), HG * 8);
       int32_t my_id = load_id(c);
+      // (l, running max, flag) of the whole pass to the peer, as soon as l is
+      // known: l < 0 carries a mark for a second pass (only the first marks)
+      auto send_end = [&]() {
+        st_async_v2(peer_addr(sbase + L::XEND_OFF + pass * HG * 8, peer) + hrow * 8,
+                    __float_as_uint(pass == 0 && flag ? -1.f : l), __float_as_uint(m_ex),
+                    peer_addr(bar(B_XEND + pass), peer));
+      };
       for (int il = 0; il < n_own; ++il, ++ig) {
         const int t = 2 * il + c;
         const int sb = ig % NSB;
@@ -1049,6 +1079,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(bar(B_PFULL + sb));
+        if (il + 1 == n_own) send_end();
 
         // the same P to the peer, into slot ig % XP_SLOTS of its P buffer
         // (64-byte swizzled K-major rows, the A operand layout of its P V):
@@ -1072,13 +1103,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
                        peer_addr(bar(B_XPFULL + xs), peer));
       }
       if (timed_out) break;
-      if (pass == 0 && n_own == 0 && !agree_ref(-INFINITY)) { timed_out = true; break; }
+      if (n_own == 0) {
+        if (pass == 0 && !agree_ref(-INFINITY)) { timed_out = true; break; }
+        send_end();
+      }
 
-      // end of pass: (l, running max, flag) to the peer, the peer's back
-      // l < 0 carries a mark for a second pass (only the first pass marks)
-      st_async_v2(peer_addr(sbase + L::XEND_OFF + pass * HG * 8, peer) + hrow * 8,
-                  __float_as_uint(pass == 0 && flag ? -1.f : l), __float_as_uint(m_ex),
-                  peer_addr(bar(B_XEND + pass), peer));
+      // end of pass: the peer's figures
       if (!warp_wait_cluster(bar(B_XEND + pass), 0)) { timed_out = true; break; }
       const volatile uint32_t *pe =
           reinterpret_cast<const volatile uint32_t *>(sm + L::XEND_OFF + pass * HG * 8) + hrow * 2;
@@ -1116,12 +1146,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
 
   // ------------------------------------------------------------ epilogue ----
   // Warps 0-7 (two per TMEM lane quarter, 128 columns each) read O once the
-  // last P V is done, scale it by 1 / l, write it as bf16 into four 128-byte
-  // swizzled 16 KB blocks over the free ring A, and each half (four warps)
-  // copies its two blocks to the output with coalesced 16-byte stores (rows
-  // past H skipped). A tensor store instead kept the CTA ~1 us waiting for
-  // the copy to read shared memory; these stores drain after the CTA.
+  // last P V is done, scale it by 1 / l, write it (bf16, a part of a row f32)
+  // into swizzled blocks of shared memory and send each block out by a tensor
+  // copy; the CTA ends when the blocks have been read. Plain 16-byte stores from
+  // the same blocks leave an SM at some 20 bytes a clock, and the closing
+  // barrier waited behind them: 7.9 us against 7.5 on 8 rows of 64 keys, 94.9
+  // against 93.8 on 128 of 2048; one bulk copy per head and 128 dims, with no
+  // tensor map, is as slow (a copy issues every ten clocks).
   if (warp < 8) {
+    if (warp == 0 && !warp_wait(bar(B_QLOAD + 3), 0)) timed_out = true;   // Q, where O is staged
     if (timed_out) atomicOr((uint32_t *)s_fail, 1u);
     named_bar_sync(1, 256);             // 1 / l, the pass count and failures are in place
     bool ok = *s_fail == 0u && T > 0;
@@ -1135,80 +1168,52 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     const bool f32_out = Q8 && parts.n > 1;
     const float inv = ok ? reinterpret_cast<volatile float *>(sm + L::XMAX_OFF)[row] : 0.f;
     const uint32_t lane_q = tmem + ((uint32_t)(q4 * 32) << 16);
+    // the warp's 32 rows in blocks of 128 bytes of each, 128-byte swizzled
+    unsigned char *stg = sm + O_STG_OFF + warp * (f32_out ? 4 : 2) * O_BLOCK + lane * 128;
+    auto chunk = [&](int j) { return stg + (j >> 3) * O_BLOCK + (((j & 7) ^ (lane & 7)) << 4); };
+    auto store = [&](int block, int dims) {     // (rows past H are left out)
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0 && h0 + q4 * 32 < H)
+        tensor_store(&tmap_o, stg + block * O_BLOCK, 256 * c + 128 * half + block * dims, h0 + q4 * 32,
+                     f32_out ? part * parts.R + r : r);
+    };
 #pragma unroll 1
-    for (int pp = 0; pp < 4; pp += 2) {
-      const int p0 = half * 4 + pp;
+    for (int pp = 0; pp < 2; ++pp) {
       uint32_t o[2][32];
       if (ok) {
-        TMEM_LD32(lane_q + COL_O + p0 * 32, o[0]);
-        TMEM_LD32(lane_q + COL_O + (p0 + 1) * 32, o[1]);
+        TMEM_LD32(lane_q + COL_O + half * 128 + pp * 64, o[0]);
+        TMEM_LD32(lane_q + COL_O + half * 128 + pp * 64 + 32, o[1]);
         tmem_wait_ld();
       } else {
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[0][k] = o[1][k] = 0u;
       }
       if (f32_out) {
-        // a part of the row: O / l in f32, 64 dims of the warp's 32 heads at a
-        // time through the warp's own piece of the drained rings (rows of 272
-        // bytes, which spreads them over the banks), so that a store writes
-        // whole 256-byte pieces of two rows
-        unsigned char *stg = sm + O_STG_OFF + warp * (32 * 272);
+        // a part of the row: O / l in f32
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const uint32_t *v = &o[k >> 3][4 * (k & 7)];
-          *reinterpret_cast<float4 *>(stg + lane * 272 + 16 * k) =
+          *reinterpret_cast<float4 *>(chunk(16 * pp + k)) =
               make_float4(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv,
                           __uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
         }
-        __syncwarp();
-        float *dst = parts.o + (((int64_t)part * parts.R + r) * H + h0 + q4 * 32) * DV + 256 * c + 32 * p0 +
-                     4 * (lane & 15);
-#pragma unroll 4
-        for (int k = 0; k < 16; ++k) {
-          const int hr = 2 * k + (lane >> 4);
-          const float4 v = *reinterpret_cast<const float4 *>(stg + hr * 272 + 16 * (lane & 15));
-          if (h0 + q4 * 32 + hr < H) *reinterpret_cast<float4 *>(dst + (int64_t)hr * DV) = v;
-        }
-        __syncwarp();
-        continue;
-      }
+        store(2 * pp, 32);
+        store(2 * pp + 1, 32);
+      } else {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int part = p0 + u;
-        unsigned char *blk = sm + O_STG_OFF + (part >> 1) * (HG * 128) + row * 128;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int j = (part & 1) * 4 + k;
-          *reinterpret_cast<uint4 *>(blk + ((j ^ (row & 7)) << 4)) =
-              make_uint4(pack_bf16(__uint_as_float(o[u][8 * k]) * inv, __uint_as_float(o[u][8 * k + 1]) * inv),
-                         pack_bf16(__uint_as_float(o[u][8 * k + 2]) * inv, __uint_as_float(o[u][8 * k + 3]) * inv),
-                         pack_bf16(__uint_as_float(o[u][8 * k + 4]) * inv, __uint_as_float(o[u][8 * k + 5]) * inv),
-                         pack_bf16(__uint_as_float(o[u][8 * k + 6]) * inv, __uint_as_float(o[u][8 * k + 7]) * inv));
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t *v = &o[k >> 2][8 * (k & 3)];
+          *reinterpret_cast<uint4 *>(chunk(8 * pp + k)) =
+              make_uint4(pack_bf16(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv),
+                         pack_bf16(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv),
+                         pack_bf16(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv),
+                         pack_bf16(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv));
         }
+        store(pp, 64);
       }
     }
-    // each half (four warps) copies its two blocks out as soon as it has
-    // written them: lane l of a warp takes 16-byte chunk l & 7 of block
-    // 2 half + ((l >> 3) & 1) of row 8 it + 2 w + (l >> 4), so one warp
-    // store writes two whole 256-byte row segments; nothing waits for the
-    // stores, and the shared memory is free once it has been read
-    if (f32_out)
-      ;
-    else if (half == 0)
-      named_bar_sync(2, 128);
-    else
-      named_bar_sync(3, 128);
-    if (!f32_out) {
-      const int wq = warp & 3, b = 2 * half + ((lane >> 3) & 1), j = lane & 7;
-      const unsigned char *src = sm + O_STG_OFF + b * (HG * 128);
-      __nv_bfloat16 *dst_row = out + ((int64_t)r * H + h0) * DV + 256 * c + 64 * b + 8 * j;
-#pragma unroll 4
-      for (int it = 0; it < HG / 8; ++it) {
-        const int row = 8 * it + 2 * wq + (lane >> 4);
-        const uint4 v = *reinterpret_cast<const uint4 *>(src + row * 128 + ((j ^ (row & 7)) << 4));
-        if (h0 + row < H) *reinterpret_cast<uint4 *>(dst_row + (int64_t)row * DV) = v;
-      }
-    }
+    bulk_commit();
     if (tid == 0) {
       // every P sent must have been consumed by the peer (its multicast
       // commit arrives here) before this CTA's shared memory goes away
@@ -1219,13 +1224,17 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
         }
       }
     }
+    bulk_wait_read();        // the copies out of this CTA's shared memory
   }
 
   if (timed_out && status) atomicOr(status, HS_STATUS_TIMEOUT);
   __syncwarp();
   if (warp >= 4 && warp != 12 + NSB) cluster_wait();   // the opening barrier's wait
   fence_before();
-  cluster_sync();          // the peer writes into this CTA's shared memory until here
+  // The peer writes into this CTA's shared memory until here. Each of those
+  // writes has been waited for on its mbarrier, so nothing need be released: a
+  // release would wait for the output's stores to reach L2 (0.6 us a row).
+  cluster_sync_relaxed();
   if (warp == 0) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
@@ -1363,6 +1372,18 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (er != CUDA_SUCCESS) return hs_set_error(HS_ERR_CUDA, "tensor map of q failed (%d)", (int)er);
+  // what the epilogue writes: out [R][H][512] bf16, or the parts [n R][H][512] f32
+  alignas(64) CUtensorMap tmap_o;
+  const bool f32_out = parts.n > 1;
+  const cuuint64_t elem = f32_out ? 4 : 2;
+  const cuuint64_t odim[3] = {(cuuint64_t)DV, (cuuint64_t)H, (cuuint64_t)R * parts.n};
+  const cuuint64_t ostride[2] = {DV * elem, H * DV * elem};
+  const cuuint32_t obox[3] = {f32_out ? 32u : 64u, 32, 1};
+  const CUresult eo = encode(&tmap_o, f32_out ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                             3, f32_out ? (void *)parts.o : out, odim, ostride, obox, estride,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (eo != CUDA_SUCCESS) return hs_set_error(HS_ERR_CUDA, "tensor map of the output failed (%d)", (int)eo);
   // a programmatic dependent launch: the prologue (barriers, TMEM, Q) may
   // run while the previous kernel in the stream finishes
   cudaLaunchConfig_t cfg = {};
@@ -1376,7 +1397,7 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   HS_CUDA_TRY(cudaLaunchKernelEx(
-      &cfg, k_attn_pair<Q8>, tmap, reinterpret_cast<const char *>(q),
+      &cfg, k_attn_pair<Q8>, tmap, tmap_o, reinterpret_cast<const char *>(q),
       reinterpret_cast<const char *>(kv_resident), n_resident,
       reinterpret_cast<const char *>(kv_hot), n_hot, row_req, fully_resident, n_reqs, idx, H, K,
       scale * 1.4426950408889634f, reinterpret_cast<__nv_bfloat16 *>(out), lse, status, parts));
@@ -1412,9 +1433,9 @@ namespace {
 // (row, head); GROUPS groups of 128 threads (four dims each) take every
 // GROUPS-th part, four loads in flight, and their sums meet in shared memory in
 // a fixed order. Latency bounds a small grid: four groups read its parts in
-// as few rounds as they allow (one row of 128 heads, 16 parts: 16.4 us for the
-// whole call against 17.5 with one group, 64 parts: 20.0 against 25.7); a
-// large one fills the SMs and takes one (4 rows: 18.5 us against 19.7).
+// as few rounds as they allow (one row of 128 heads, 16 parts: 12.8 us for the
+// whole call against 13.7 with one group, 64 parts: 17.1 against 21.2); a
+// large one fills the SMs and takes one (16 rows: 23.2 us against 26.6).
 template <int GROUPS>
 __global__ void __launch_bounds__(GROUPS * DV / 4)
     k_attn_join(const float *__restrict__ o, const float *__restrict__ part_lse, int32_t n, int64_t rows,
@@ -1464,8 +1485,9 @@ __global__ void __launch_bounds__(GROUPS * DV / 4)
 
 constexpr int JOIN_FEW = 256;       // (row, head) pairs that leave a grid of one group each small
 
-// Tiles of 32 keys, at least, in a part of a row: a cluster costs ~9 us whatever
-// its tiles (8 and 4 tiles measured 16.2 and 15.4 us on 4 rows of 2048 keys).
+// Tiles of 32 keys, at least, in a part of a row: a cluster costs ~8 us whatever
+// its tiles (8, 4 and 2 tiles measured 15.3, 14.6 and 14.5 us on 4 rows of 2048
+// keys).
 constexpr int PART_MIN_TILES = 4;
 
 }  // namespace
