@@ -34,13 +34,14 @@
 // overwrites the inputs during the call.
 //
 // Measured (bf16 logits, draft probabilities given): 256 requests x 3 drafts,
-// V = 129280: 72 us, 80 % of what the 385 MB it has to move take at the
-// measured copy rate; 128 x 3: 45 us; 64 x 3: 26 us; 1 x 3: 9 us and 2 x 3, V =
-// 1024 f32: 6.4 us, latency.
+// V = 129280: 70 us, 82 % of what the 385 MB it has to move take at the
+// measured copy rate (V = 129281: 80 us); 128 x 3: 43 us; 64 x 3: 26 us; 1 x 3:
+// 9.6 us and 2 x 3, V = 1024 f32: 6.4 us, latency.
 
 #include <float.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "hs_commit.cuh"
 
@@ -49,13 +50,19 @@ namespace {
 constexpr int NT = 256;             // threads per block
 constexpr int MIN_BLOCKS = 3;       // blocks per SM, at least (80 registers, nothing spilled)
 constexpr int WARPS = NT / 32;
-constexpr int RING = 15;            // 16-byte places of a thread's ring of copies in flight
+constexpr int RING = 12;            // 16-byte places of a thread's ring of copies in flight
+constexpr int WARP_RING = 489;      // 16-byte places of a warp's ring in the race: 3 to 7 windows
 constexpr int BATCH = 4;            // vectors of a row taken together
 constexpr int NB = 8;               // values of a thread in flight where rows are not aligned
-constexpr size_t RING_BYTES = (size_t)RING * NT * 16;
+static_assert(WARP_RING * WARPS >= RING * NT, "row_stat's places");
+constexpr size_t RING_BYTES = (size_t)WARP_RING * WARPS * 16;
 constexpr int MAX_CLUSTER = 16;
 constexpr int MAX_DRAFTS = 255;
 constexpr float LOG2E = 1.4426950408889634f;
+
+// How the rows of logits, draft probabilities and noise lie: each on 16 bytes;
+// anywhere in arrays on 16 bytes; anywhere.
+enum Rows { ROWS_ON_16, ARRAYS_ON_16, ROWS_ANYWHERE };
 
 struct SampleArgs {
   const void *logits;
@@ -67,7 +74,7 @@ struct SampleArgs {
   float *logprob;
   uint32_t *status;
   uint32_t log_rows;       // 2^log_rows rows side by side in a cluster, at most its blocks
-  bool aligned;            // rows of logits, probs and noise all start on 16 bytes
+  Rows rows;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -106,6 +113,12 @@ __device__ __forceinline__ void push2(const void *p, uint32_t rank, uint32_t a, 
 __device__ __forceinline__ void copy16(uint4 *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
                "l"(src)
+               : "memory");
+}
+// its first `bytes`, zeros behind them
+__device__ __forceinline__ void copy16(uint4 *dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
@@ -301,6 +314,8 @@ __device__ __forceinline__ Stat row_stat(const Slice<DTYPE> &sl, const void *row
   };
 #pragma unroll
   for (int p = 0; p < DEPTH; ++p) issue(k0 + p * STEP, p);
+  static_assert(2 * Slice<DTYPE>::PER <= NT, "a value outside the body per thread");
+  const float rest = (int)threadIdx.x < sl.rest ? logit_at<DTYPE>(row, sl.rest_index(threadIdx.x)) : -INFINITY;
   meanwhile();
   int place = 0;
   for (int32_t k = k0; k < sl.hi; k += STEP) {
@@ -330,10 +345,7 @@ __device__ __forceinline__ Stat row_stat(const Slice<DTYPE> &sl, const void *row
       take_batch<DTYPE>(st, w, k, c);
     }
   }
-  for (int32_t j = threadIdx.x; j < sl.rest; j += NT) {
-    const float x = logit_at<DTYPE>(row, sl.rest_index(j));
-    join(st.m, st.s, x, x == -INFINITY ? 0.f : 1.f, c);
-  }
+  join(st.m, st.s, rest, rest == -INFINITY ? 0.f : 1.f, c);
   return st;
 }
 
@@ -355,8 +367,8 @@ __device__ __forceinline__ int32_t row_first(const Slice<DTYPE> &sl, const void 
         if (value<DTYPE>(w, j) == top) best = min(best, sl.head + k * Slice<DTYPE>::PER + j);
     }
   }
-  for (int32_t j = threadIdx.x; j < sl.rest; j += NT)
-    if (logit_at<DTYPE>(row, sl.rest_index(j)) == top) best = min(best, sl.rest_index(j));
+  const int32_t j = threadIdx.x;
+  if (j < sl.rest && logit_at<DTYPE>(row, sl.rest_index(j)) == top) best = min(best, sl.rest_index(j));
   return best;
 }
 
@@ -492,7 +504,7 @@ struct Race {
   }
 };
 
-template <int DTYPE, bool VEC, bool HAS_Q>
+template <int DTYPE, Rows ROWS, bool HAS_Q>
 __device__ __forceinline__ Race race(const char *row, const float *q, const float *E, int32_t V,
                                      uint32_t rank, uint32_t log_n, const RaceRow &rr, uint4 *ring) {
   Race ra = {0.f, INT32_MAX, 0.f};
@@ -504,82 +516,127 @@ __device__ __forceinline__ Race race(const char *row, const float *q, const floa
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(f) : "f"(e));
     if (r == INFINITY) r = (rr.inv - w) * f;
   };
-  if (VEC) {
-    // Units of 16 bytes of logits and as many values of q and E through the
-    // thread's ring places. A warp takes 32 neighbouring units at a time, each
-    // lane the groups of four values of which it copies E and q (group lane, and
-    // of bf16 logits group 32 + lane too), so that every copy of a warp is one
-    // contiguous piece: with a lane's eight values side by side its copies of E
-    // and q touched each 32-byte sector twice (94 us against 82 on 256 x 3
-    // drafts). A bf16 lane's logits are then the halves of two others' copies.
-    constexpr int PER = Slice<DTYPE>::PER, QV = PER / 4, SLOTS = 1 + (HAS_Q ? 2 : 1) * QV, DEPTH = RING / SLOTS;
-    const int32_t units = V / PER;
-    const int32_t lo = part_of(units, rank, log_n), hi = part_of(units, rank + 1, log_n);
-    const int32_t lane = threadIdx.x & 31, warp0 = threadIdx.x & ~31;
-    // the first value of group j of the warp's units from u0 on, and whether its unit exists
-    auto value_at = [&](int32_t u0, int j) { return u0 * PER + 128 * j + 4 * lane; };
-    auto exists = [&](int32_t u0, int j) { return u0 + (32 * j + lane) / QV < hi; };
-    auto issue = [&](int32_t u0, int place) {
-      uint4 *to = ring + place * SLOTS * NT;
-      if (u0 + lane < hi) copy16(to, reinterpret_cast<const uint4 *>(row) + u0 + lane);
+  // the block's values: whole vectors of logits
+  constexpr int PER = Slice<DTYPE>::PER;
+  const int32_t vecs = (V + PER - 1) / PER, lo = part_of(vecs, rank, log_n) * PER,
+                hi = min(part_of(vecs, rank + 1, log_n) * PER, V);
+  if (ROWS != ROWS_ANYWHERE) {
+    // A warp takes UNIT values at a time and copies for each array the 16-byte
+    // vectors that hold them, so that every copy of a warp is one contiguous
+    // piece (where each lane copied eight values' worth of E and q side by side,
+    // the copies touched each 32-byte sector twice: 94 us against 82 on 256 x 3
+    // drafts). Where the rows start on 16 bytes a lane takes groups of four
+    // values, a vector of E and q each; else the values lie somewhere in the
+    // copied windows, each array's its own way on, and a lane takes every 32nd (256
+    // x 3 drafts, V = 129281: 80 us, by loads without copies 122; V = 129280 the
+    // same way 72.9 against 70).
+    constexpr int ELEM = 16 / PER, UNIT = 32 * PER;
+    constexpr int LV = 32 + 1, EV = UNIT / 4 + 1, STAGE = LV + (HAS_Q ? 2 : 1) * EV, DEPTH = WARP_RING / STAGE;
+    const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint4 *mine = ring + warp * WARP_RING;
+    // lane l's vector of each array's first window (its other vectors of a window
+    // are 32 further on; the last one is lane 0's, 1's and 2's), and how far the
+    // lane's first value lies in the window
+    const int32_t first = lo + warp * UNIT;
+    const char *ls = row + (int64_t)first * ELEM, *ew = reinterpret_cast<const char *>(E + first),
+               *qw = HAS_Q ? reinterpret_cast<const char *>(q + first) : ew;
+    const int l_at = (int)(reinterpret_cast<uintptr_t>(ls) & 15) / ELEM + lane,
+              e_at = (int)(reinterpret_cast<uintptr_t>(ew) & 15) / 4 + lane,
+              q_at = (int)(reinterpret_cast<uintptr_t>(qw) & 15) / 4 + lane;
+    ls += 16 * lane - ELEM * (l_at - lane);
+    ew += 16 * lane - 4 * (e_at - lane);
+    qw += 16 * lane - 4 * (q_at - lane);
+    const char *last = lane == 0 ? ls + 512 : (lane == 1 ? ew : qw) + 4 * UNIT - 16 * lane;
+    const int last_at = lane == 0 ? 32 : LV + lane * EV - 1, last_step = WARPS * UNIT * (lane == 0 ? ELEM : 4);
+    auto issue = [&](int32_t v0, int place) {
+      uint4 *to = mine + place * STAGE;
+      if (v0 + UNIT + PER <= V && v0 < hi) {
+        copy16(to + lane, ls);
 #pragma unroll
-      for (int j = 0; j < QV; ++j) {
-        if (exists(u0, j)) {
-          copy16(to + (1 + j) * NT, E + value_at(u0, j));
-          if (HAS_Q) copy16(to + (1 + QV + j) * NT, q + value_at(u0, j));
+        for (int k = 0; k < UNIT / 128; ++k) {
+          copy16(to + LV + 32 * k + lane, ew + 512 * k);
+          if (HAS_Q) copy16(to + LV + EV + 32 * k + lane, qw + 512 * k);
         }
+        if (ROWS != ROWS_ON_16 && lane < (HAS_Q ? 3 : 2)) copy16(to + last_at, last);
+      } else if (v0 < hi) {                     // no byte past the row's end
+        auto part = [&](uint4 *at, const char *from, const void *end) {
+          const int64_t left = reinterpret_cast<const char *>(end) - from;
+          if (left > 0) copy16(at, from, left < 16 ? (int)left : 16);
+        };
+        part(to + lane, ls, row + (int64_t)V * ELEM);
+#pragma unroll
+        for (int k = 0; k < UNIT / 128; ++k) {
+          part(to + LV + 32 * k + lane, ew + 512 * k, E + V);
+          if (HAS_Q) part(to + LV + EV + 32 * k + lane, qw + 512 * k, q + V);
+        }
+        if (ROWS != ROWS_ON_16 && lane < (HAS_Q ? 3 : 2))
+          part(to + last_at, last, lane == 0 ? row + (int64_t)V * ELEM : reinterpret_cast<const char *>((lane == 1 ? E : q) + V));
       }
       copy_commit();
+      ls += WARPS * UNIT * ELEM;
+      ew += WARPS * UNIT * 4;
+      qw += WARPS * UNIT * 4;
+      last += last_step;
     };
-#pragma unroll
-    for (int p = 0; p < DEPTH; ++p) issue(lo + p * NT + warp0, p);
+#pragma unroll 1
+    for (int p = 0; p < DEPTH; ++p) issue(first + p * WARPS * UNIT, p);
     int place = 0;
-    for (int32_t u0 = lo + warp0; u0 < hi; u0 += NT) {       // the whole warp
+    for (int32_t v0 = first; v0 < hi; v0 += WARPS * UNIT) {       // the whole warp
       copy_wait<DEPTH - 1>();
       __syncwarp();
-      const uint4 *from = ring + place * SLOTS * NT;
-      float r[PER], big = 0.f;
-      uint4 e4[QV], w4[QV];
+      const uint4 *from = mine + place * STAGE;
+      const float *es = reinterpret_cast<const float *>(from + LV) + e_at;
+      const float *qs = reinterpret_cast<const float *>(from + LV + EV) + q_at;
+      float r[PER], e[PER], w[PER], big = 0.f;
+      auto value_at = [&](int o) {
+        return ROWS == ROWS_ON_16 ? v0 + 128 * (o / 4) + 4 * lane + (o & 3) : v0 + 32 * o + lane;
+      };
 #pragma unroll
-      for (int j = 0; j < QV; ++j) {
-        uint4 x = from[0];
-        if (DTYPE == HS_LOGITS_BF16) {
-          const uint2 half = reinterpret_cast<const uint2 *>(from - lane)[32 * j + lane];
-          x = make_uint4(half.x, half.y, 0, 0);
-        }
-        e4[j] = from[(1 + j) * NT];
-        w4[j] = HAS_Q ? from[(1 + QV + j) * NT] : make_uint4(0, 0, 0, 0);
-        const bool here = exists(u0, j);       // (else: what the places held)
+      for (int o = 0; o < PER; ++o) {
+        if (ROWS == ROWS_ON_16) {
+          if (o & 3) continue;
+          // (a bf16 lane's logits are the halves of two others' copies)
+          const uint2 half = reinterpret_cast<const uint2 *>(from)[32 * (o / 4) + lane];
+          const uint4 x = DTYPE == HS_LOGITS_F32 ? from[lane] : make_uint4(half.x, half.y, 0, 0);
+          const uint4 e4 = from[LV + 32 * (o / 4) + lane];
+          const uint4 w4 = HAS_Q ? from[LV + EV + 32 * (o / 4) + lane] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const int o = 4 * j + i;
-          ratio2(pack2(value<DTYPE>(x, i), value<DTYPE>(x, i + 1)),
-                 pack2(-value<HS_LOGITS_F32>(w4[j], i), -value<HS_LOGITS_F32>(w4[j], i + 1)),
-                 value<HS_LOGITS_F32>(e4[j], i), value<HS_LOGITS_F32>(e4[j], i + 1), nm, cc, ii, r[o],
-                 r[o + 1]);
-          r[o] = here ? r[o] : 0.f;
-          r[o + 1] = here ? r[o + 1] : 0.f;
-          big = fmaxf(big, fmaxf(r[o], r[o + 1]));
+          for (int i = 0; i < 4; ++i) {
+            r[o + i] = value<DTYPE>(x, i);
+            e[o + i] = value<HS_LOGITS_F32>(e4, i);
+            w[o + i] = value<HS_LOGITS_F32>(w4, i);
+          }
+          continue;
         }
+        r[o] = DTYPE == HS_LOGITS_F32
+                   ? reinterpret_cast<const float *>(from)[l_at + 32 * o]
+                   : __uint_as_float((uint32_t)reinterpret_cast<const unsigned short *>(from)[l_at + 32 * o] << 16);
+        e[o] = es[32 * o];
+        w[o] = HAS_Q ? qs[32 * o] : 0.f;
       }
-      __syncwarp();
-      issue(u0 + DEPTH * NT, place);
-      place = place + 1 == DEPTH ? 0 : place + 1;
-      const bool barred_here = rr.barred >= u0 * PER && rr.barred < (u0 + 32) * PER;
-      if (barred_here || big == INFINITY) {
+#pragma unroll
+      for (int o = 0; o < PER; o += 2) {
+        ratio2(pack2(r[o], r[o + 1]), pack2(-w[o], -w[o + 1]), e[o], e[o + 1], nm, cc, ii, r[o], r[o + 1]);
+        big = fmaxf(big, fmaxf(r[o], r[o + 1]));
+      }
+      const bool cut = v0 + UNIT > hi;             // (the places past hi: what they held)
+      if (cut || (rr.barred >= v0 && rr.barred < v0 + UNIT) || big == INFINITY) {
         big = 0.f;
 #pragma unroll
         for (int o = 0; o < PER; ++o) {
-          mend(r[o], value<HS_LOGITS_F32>(w4[o / 4], o & 3), value<HS_LOGITS_F32>(e4[o / 4], o & 3));
-          if (value_at(u0, o / 4) + (o & 3) == rr.barred) r[o] = 0.f;
+          const int32_t v = value_at(o);
+          mend(r[o], w[o], e[o]);
+          if (v >= hi || v == rr.barred) r[o] = 0.f;
           big = fmaxf(big, r[o]);
         }
       }
-      ra.template group<PER>(r, big, [&](int o) { return value_at(u0, o / 4) + (o & 3); });
+      __syncwarp();
+      issue(v0 + DEPTH * WARPS * UNIT, place);
+      place = place + 1 == DEPTH ? 0 : place + 1;
+      ra.template group<PER>(r, big, value_at);
     }
     copy_wait<0>();
   } else {
-    const int32_t lo = part_of(V, rank, log_n), hi = part_of(V, rank + 1, log_n);
     for (int32_t k0 = lo; k0 < hi; k0 += NB * NT) {
       float r[NB], e[NB], w[NB], big = 0.f;
 #pragma unroll
@@ -623,7 +680,6 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
                                                                   const __grid_constant__ CommitArgs ca) {
   extern __shared__ uint4 ring_base[];
   __shared__ Shared sh;
-  uint4 *ring = ring_base + threadIdx.x;
   const uint32_t rank = cluster_rank(), n = cluster_size();
   if (n > 1) cluster_arrive();       // waited for before the first push: every block runs by then
   const int b = (int)(blockIdx.x / n);
@@ -652,7 +708,7 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
     const int mine = m0 + (int)(rank >> (log_n - log_g));
     const char *row = rows + (mine <= d ? mine : d) * row_bytes;
     const Slice<DTYPE> sl(row, mine <= d ? V : 0, rank & (per_row - 1), log_n - log_g);
-    const Stat st = row_stat<DTYPE>(sl, row, c, ring, [&]() {
+    const Stat st = row_stat<DTYPE>(sl, row, c, ring_base + tid, [&]() {
       if (m0 != 0 || rank != 0 || tid >= d) return;
       const int64_t k = (int64_t)b * d + tid;
       x = __ldg(sa.drafts + k);
@@ -722,12 +778,19 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
     for (;;) {
       const RaceRow rr = {top, c, inv, barred};
       Race ra;
-      if (sa.aligned)
-        ra = q ? race<DTYPE, true, true>(row, q, E, V, rank, log_n, rr, ring)
-               : race<DTYPE, true, false>(row, q, E, V, rank, log_n, rr, ring);
-      else
-        ra = q ? race<DTYPE, false, true>(row, q, E, V, rank, log_n, rr, ring)
-               : race<DTYPE, false, false>(row, q, E, V, rank, log_n, rr, ring);
+      switch (sa.rows) {
+        case ROWS_ON_16:
+          ra = q ? race<DTYPE, ROWS_ON_16, true>(row, q, E, V, rank, log_n, rr, ring_base)
+                 : race<DTYPE, ROWS_ON_16, false>(row, q, E, V, rank, log_n, rr, ring_base);
+          break;
+        case ARRAYS_ON_16:
+          ra = q ? race<DTYPE, ARRAYS_ON_16, true>(row, q, E, V, rank, log_n, rr, ring_base)
+                 : race<DTYPE, ARRAYS_ON_16, false>(row, q, E, V, rank, log_n, rr, ring_base);
+          break;
+        default:
+          ra = q ? race<DTYPE, ROWS_ANYWHERE, true>(row, q, E, V, rank, log_n, rr, ring_base)
+                 : race<DTYPE, ROWS_ANYWHERE, false>(row, q, E, V, rank, log_n, rr, ring_base);
+      }
       cluster_join(sh, ra.best, ra.at, rank, n, 0, turn, BestOp{});
       if (ra.at != INT32_MAX) {
         token = (int32_t)ra.at;
@@ -779,15 +842,17 @@ int check_sample(const void *logits, int32_t dtype, int32_t B, int32_t d, int32_
 //
 // A cluster that takes its rows one after the other reads no row behind the
 // refusal, but each row costs a few microseconds of latency (the first loads,
-// the joins). So while the blocks leave a third of the device free, up to four
-// rows are taken side by side (2 x 3 drafts, V = 1024: 6.4 us against 9.8; 33 x
-// 5, V = 50257: 13.8 against 23; 64 x 3, V = 129280: 26.2 against 28.7), while
-// all blocks run at once two (96 x 3, V = 50257: 24.7 us against 26.2), else
-// one. The blocks of a request double, to eight, while all blocks run at once
-// and a part of a row keeps 2048 values, and to sixteen while each has an SM
-// of its own (1 x 3, V = 129280: 9.1 us against 10.9). Not past that: 256 x 3,
-// V = 129280 takes 72 us with one block, 82 with two, 77 with four.
-int cluster_shape(int32_t B, int32_t d, int32_t V, int *n, int *g) {
+// the joins). So while all blocks run at once, up to four rows are taken side
+// by side as long as one row of every request is less than 18 MB, some three
+// microseconds of HBM (2 x 3 drafts, V = 1024: 6.5 us against 11 one by one; 33 x
+// 5, V = 50257: 13.3 against 21; 96 x 3, V = 50257: 20.3 against 21.7 two by two;
+// 64 x 7, V = 65000 f32, 16.6 MB: 30.9 against 33.1), else two (110 x 3, V =
+// 129280: 36.7 us against 41.7 by fours). The blocks of a request double, to
+// eight, while all blocks run at once and a part of a row keeps 2048 values, and
+// to sixteen while each has an SM of its own (1 x 3, V = 129280: 9.5 us against
+// 11.2). Not past that: 256 x 3, V = 129280 takes 70 us with one block, 84 with
+// two, 77 with four.
+int cluster_shape(int32_t B, int32_t d, int32_t V, int32_t elem, int *n, int *g) {
   int sms = 0;
   int rc = hs_sm_count(&sms);
   if (rc) return rc;
@@ -797,7 +862,7 @@ int cluster_shape(int32_t B, int32_t d, int32_t V, int *n, int *g) {
   while (k < MAX_CLUSTER && (int64_t)B * 2 * k <= (k < 8 ? at_once : (int64_t)sms) &&
          (k < most || (int64_t)V * most / (2 * k) >= 2048))
     k *= 2;
-  int r = (int64_t)B * k <= 2 * (int64_t)sms ? most : (int64_t)B * k <= at_once ? 2 : 1;
+  int r = (int64_t)B * k > at_once ? 1 : (int64_t)B * V * elem < 18000000 ? most : 2;
   if (r > most) r = most;
   if (r > k) r = k;
   *n = k;
@@ -808,12 +873,12 @@ int cluster_shape(int32_t B, int32_t d, int32_t V, int *n, int *g) {
 template <bool COMMIT>
 int launch(SampleArgs &sa, int32_t dtype, int32_t B, const CommitArgs &ca, cudaStream_t stream) {
   int n = 1, g = 1;
-  int rc = cluster_shape(B, sa.d, sa.V, &n, &g);
+  int rc = cluster_shape(B, sa.d, sa.V, dtype == HS_LOGITS_F32 ? 4 : 2, &n, &g);
   if (rc) return rc;
   if ((int64_t)B * n > INT32_MAX) return hs_set_error(HS_ERR_UNSUPPORTED, "B too large");
   sa.log_rows = 31 - __builtin_clz((unsigned)g);
-  sa.aligned = sa.V % (dtype == HS_LOGITS_F32 ? 4 : 8) == 0 &&
-               (((uintptr_t)sa.logits | (uintptr_t)sa.probs | (uintptr_t)sa.noise) & 15) == 0;
+  const bool arrays = (((uintptr_t)sa.logits | (uintptr_t)sa.probs | (uintptr_t)sa.noise) & 15) == 0;
+  sa.rows = !arrays ? ROWS_ANYWHERE : sa.V % (dtype == HS_LOGITS_F32 ? 4 : 8) == 0 ? ROWS_ON_16 : ARRAYS_ON_16;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * n));
   cfg.blockDim = dim3(NT);
@@ -860,7 +925,7 @@ extern "C" int hs_verify_sample(const void *logits, int32_t logits_dtype, int32_
                         uniforms, noise, accept_len, next_token, logprob, status);
   if (rc) return rc;
   SampleArgs sa = {logits,   d,     V,          temperature, draft_tokens, draft_probs,
-                         uniforms, noise, accept_len, next_token,  logprob,      status, 0, false};
+                         uniforms, noise, accept_len, next_token,  logprob,      status, 0, ROWS_ANYWHERE};
   return launch<false>(sa, logits_dtype, B, CommitArgs{}, stream);
 }
 
@@ -890,6 +955,6 @@ extern "C" int hs_verify_sample_finalize(hs_buffer *buf, const void *logits, int
     return hs_set_error(HS_ERR_UNSUPPORTED, "hs_verify_sample_finalize cannot be captured in a graph");
   buf->clock += 1;
   SampleArgs sa = {logits,   d,     V,          temperature, draft_tokens, draft_probs,
-                         uniforms, noise, accept_len, next_token,  logprob,      buf->status, 0, false};
+                         uniforms, noise, accept_len, next_token,  logprob,      buf->status, 0, ROWS_ANYWHERE};
   return launch<true>(sa, logits_dtype, B, commit_args(buf, d, step_kv, req_ids, kv_len), stream);
 }

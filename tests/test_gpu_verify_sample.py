@@ -71,7 +71,9 @@ def _check(got, want):
                                            (40, 2, 333, 0.95), (1, 7, 50257, 0.0), (3, 15, 9999, 0.2),
                                            (2, 3, 129280, 0.0), (160, 2, 4097, 0.1), (330, 1, 700, 0.0),
                                            (2, 40, 100, 0.0), (1, 255, 64, 0.0), (2000, 1, 40, 0.2),
-                                           (1, 3, 40000, 0.0), (9, 3, 32768, 0.0), (70, 5, 20000, 0.9)])
+                                           (1, 3, 40000, 0.0), (9, 3, 32768, 0.0), (70, 5, 20000, 0.9),
+                                           (3, 2, 50259, 0.0), (20, 3, 12346, 0.3), (300, 1, 2570, 0.0),
+                                           (110, 3, 30004, 0.0), (4, 3, 515, 0.6)])
 def test_against_the_oracle(dtype, probs, B, d, V, masked):
     hs = lib()
     c = _case(B * 131 + d * 17 + V, B, d, V, dtype, probs, masked)
