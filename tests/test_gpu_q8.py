@@ -2,6 +2,10 @@
 of the attention over them (hs_sparse_attn_decode_q8): bytes and values
 bit-exact against the oracle, attention within bounds derived from its
 roundings, and bit-identical to hs_sparse_attn_decode over the same values."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -515,3 +519,46 @@ def test_attention_leaves_its_neighbours_alone():
     assert (pad_o[:128] == 3).all() and (pad_o[-128:] == 3).all()
     assert (pad_l[:16] == 3).all() and (pad_l[-16:] == 3).all()
     assert (pad_w[:256] == 0x5A).all() and (pad_w[-256:] == 0x5A).all()
+
+
+FIRST_CALLS = """
+import torch
+import hisparse_top_sparse_gb300 as hs
+d = "cuda"
+src = torch.randn((64, 576), device=d).bfloat16()
+cache = torch.zeros((64, 656), dtype=torch.uint8, device=d)
+back = torch.zeros((64, 576), dtype=torch.bfloat16, device=d)
+q = torch.randn((2, 128, 576), device=d).bfloat16()
+idx = torch.randint(0, 64, (2, 600), dtype=torch.int32, device=d)
+ws = torch.empty(hs.ATTN_Q8_WORKSPACE_BYTES, dtype=torch.uint8, device=d)
+outs = [torch.zeros((2, 128, 512), dtype=torch.bfloat16, device=d) for _ in range(2)]
+v = (torch.randn((2, 3, 1000), device=d), torch.ones(2, device=d), torch.zeros((2, 2), dtype=torch.int32, device=d),
+     None, torch.zeros((2, 2), device=d), torch.rand((2, 1000), device=d) + 0.1)
+toks = [torch.full((2, 2), -7, dtype=torch.int32, device=d) for _ in range(2)]
+
+
+def run(out, tok):
+    hs.hs_quant_rows(src, cache)
+    hs.hs_dequant_rows(cache, back)
+    hs.hs_sparse_attn_decode_q8(q, cache, idx, 0.04, out, workspace=ws)
+    hs.hs_verify_sample(*v, tok[0], tok[1])
+
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run(outs[0], toks[0])
+g.replay()
+run(outs[1], toks[1])
+torch.cuda.synchronize()
+assert torch.equal(outs[0], outs[1]) and outs[0].abs().sum() > 0
+assert torch.equal(toks[0], toks[1]) and (toks[0] >= 0).all()
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    lib()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
