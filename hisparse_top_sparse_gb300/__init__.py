@@ -546,8 +546,8 @@ def _on_stream(stream, cur):
 def _device() -> int:
     """The current CUDA device; -2 where there is none (no tensor's device)."""
     try:
-        return torch.cuda.current_device()
-    except (RuntimeError, AssertionError):
+        return torch._C._cuda_getDevice()
+    except (RuntimeError, AttributeError):
         return -2
 
 
