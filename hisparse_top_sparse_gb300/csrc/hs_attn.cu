@@ -1327,14 +1327,9 @@ extern "C" int hs_sparse_attn_decode_mixed(const void *q, const void *kv_residen
                         n_reqs, idx, R, H, K, scale, out, lse, status, true, stream);
 }
 
-// Checks the arguments and launches k_attn_pair<Q8> (parts: the q8 kernel's
-// split of the rows' keys, chosen by the caller after the same size checks).
-template <bool Q8>
-static int attn_launch(const void *q, const void *kv_resident, int64_t n_resident,
-                       const void *kv_hot, int64_t n_hot, const int32_t *row_req,
-                       const int32_t *fully_resident, int32_t n_reqs, const int32_t *idx, int32_t R,
-                       int32_t H, int32_t K, float scale, void *out, float *lse, uint32_t *status,
-                       const Parts &parts, bool pdl, cudaStream_t stream) {
+static int check_attn(const void *q, const void *kv_resident, int64_t n_resident, const void *kv_hot,
+                      int64_t n_hot, const int32_t *fully_resident, int32_t n_reqs, const int32_t *idx,
+                      int32_t R, int32_t H, int32_t K, float scale, const void *out) {
   if (R < 0 || H < 1 || H > 1024 || K < 0 || n_resident < 0 || n_hot < 0 ||
       (fully_resident && n_reqs < 0))
     return hs_set_error(HS_ERR_INVALID_ARG, "bad sizes R=%d H=%d (1..1024) K=%d n_kv=%lld/%lld",
@@ -1347,6 +1342,17 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
       ((uintptr_t)out & 15))
     return hs_set_error(HS_ERR_INVALID_ARG, "q, kv and out must be 16-byte aligned");
   if (!(scale == scale)) return hs_set_error(HS_ERR_INVALID_ARG, "scale is NaN");
+  return HS_OK;
+}
+
+// Launches k_attn_pair<Q8>, its arguments checked (parts: the q8 kernel's split
+// of the rows' keys).
+template <bool Q8>
+static int attn_launch(const void *q, const void *kv_resident, int64_t n_resident,
+                       const void *kv_hot, int64_t n_hot, const int32_t *row_req,
+                       const int32_t *fully_resident, int32_t n_reqs, const int32_t *idx, int32_t R,
+                       int32_t H, int32_t K, float scale, void *out, float *lse, uint32_t *status,
+                       const Parts &parts, bool pdl, cudaStream_t stream) {
   int rc = set_attn_attributes();
   if (rc) return rc;
   const int64_t blocks = (int64_t)R * ((H + HG - 1) / HG) * 2 * parts.n;
@@ -1410,6 +1416,9 @@ int hs_attn_launch(const void *q, const void *kv_resident, int64_t n_resident, c
                    int32_t n_reqs, const int32_t *idx, int32_t R, int32_t H, int32_t K,
                    float scale, void *out, float *lse, uint32_t *status, bool pdl,
                    cudaStream_t stream) {
+  const int rc = check_attn(q, kv_resident, n_resident, kv_hot, n_hot, fully_resident, n_reqs, idx, R, H, K,
+                            scale, out);
+  if (rc || R == 0) return rc;
   const Parts whole = {1, K, R, nullptr, nullptr};
   return attn_launch<false>(q, kv_resident, n_resident, kv_hot, n_hot, row_req, fully_resident,
                             n_reqs, idx, R, H, K, scale, out, lse, status, whole, pdl, stream);
@@ -1505,16 +1514,19 @@ extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n
   if (!(scale >= 0.f) || scale > FLT_MAX)
     return hs_set_error(HS_ERR_INVALID_ARG, "scale must be finite and not negative");
   if (scale < FLT_MIN) scale = FLT_MIN;      // equal weights all the same; 0 times a masked -inf is NaN
+  int rc = check_attn(q, kv, n_kv_rows, nullptr, 0, nullptr, 0, idx, R, H, K, scale, out);
+  if (rc || R == 0) return rc;
+  const bool few_heads = H <= HS_ATTN_FEW_HEADS;
   Parts parts = {1, K, R, nullptr, nullptr};
-  if (R > 0 && H >= 1 && H <= 1024 && K > 0 && workspace) {
+  if (K > 0 && workspace) {
     // Few rows leave most of the SMs idle and walk their keys one after the
-    // other: the keys of a row are split while the wave has clusters left.
-    int clusters = 0;
-    int rc = hs_attn_wave_rows(1, &clusters);
-    if (rc) return rc;
+    // other: the keys of a row are split while a wave has clusters (blocks, for
+    // few heads) left.
+    int places = 0;
+    if ((rc = few_heads ? hs_attn_few_places(&places) : hs_attn_wave_rows(1, &places))) return rc;
     const int64_t base = (int64_t)R * ((H + HG - 1) / HG), rows = (int64_t)R * H;
     const int tiles = (K + NK - 1) / NK;
-    int64_t n = clusters / base;
+    int64_t n = places / base;
     if (n > tiles / PART_MIN_TILES) n = tiles / PART_MIN_TILES;
     const int64_t room = (int64_t)(workspace_bytes / (rows * (DV + 1) * sizeof(float)));
     if (n > room) n = room;
@@ -1527,8 +1539,10 @@ extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n
     }
     if (parts.n == 1) parts.keys = K;
   }
-  int rc = attn_launch<true>(q, kv, n_kv_rows, nullptr, 0, nullptr, nullptr, 0, idx, R, H, K, scale,
-                             out, lse, status, parts, true, stream);
+  rc = few_heads ? hs_attn_few_launch(q, kv, n_kv_rows, idx, R, H, K, scale, out, lse, parts.n, parts.keys,
+                                      parts.o, parts.lse, stream)
+                 : attn_launch<true>(q, kv, n_kv_rows, nullptr, 0, nullptr, nullptr, 0, idx, R, H, K, scale,
+                                     out, lse, status, parts, true, stream);
   if (rc || parts.n == 1) return rc;
   const bool few = (int64_t)R * H <= JOIN_FEW;
   cudaLaunchConfig_t cfg = {};

@@ -218,7 +218,8 @@ def _attend(hs, q, cache, idx, scale, ws=None, **kw):
 
 CASES = [(1, 1, 1, 0.0), (3, 16, 5, 0.0), (2, 128, 2048, 0.0), (5, 40, 33, 0.3), (2, 136, 130, 0.1),
          (1, 128, 8192, 0.05), (80, 128, 96, 0.5), (9, 64, 1000, 0.9), (1, 1024, 300, 0.0),
-         (4, 128, 127, 0.0), (4, 128, 129, 0.0)]
+         (4, 128, 127, 0.0), (4, 128, 129, 0.0), (7, 16, 2048, 0.1), (320, 8, 100, 0.3), (1, 16, 8192, 0.0),
+         (2, 1, 1528, 0.5), (40, 15, 700, 0.97), (3, 17, 300, 0.0), (400, 16, 1, 0.1), (6, 4, 257, 0.0)]
 
 
 @pytest.mark.parametrize("R,H,K,pad", CASES)
@@ -258,7 +259,8 @@ def test_attention_equals_the_bf16_call_over_the_same_values(R, H, K):
     assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
 
 
-def test_attention_second_pass_and_sharp_logits():
+@pytest.mark.parametrize("H", [128, 16])
+def test_attention_second_pass_and_sharp_logits(H):
     """Scores whose later tiles pass the first ones by more than 2^30."""
     hs = lib()
     g = np.random.default_rng(9)
@@ -267,13 +269,14 @@ def test_attention_second_pass_and_sharp_logits():
     rows = O.q8_quantise(x)
     values = O.q8_values(rows)
     idx = np.arange(600, dtype=np.int32)[None].repeat(3, 0)
-    q = torch.as_tensor(g.standard_normal((3, 128, 576)).astype(np.float32)).to(torch.bfloat16)
+    q = torch.as_tensor(g.standard_normal((3, H, 576)).astype(np.float32)).to(torch.bfloat16)
     for ws in (None, torch.empty(32 << 20, dtype=torch.uint8, device=DEV)):
         out, lse = _attend(hs, q.to(DEV), _t(rows), _t(idx), 0.25, ws)
         _check(out, lse, _f64(q), values, idx, 0.25)
 
 
-def test_attention_ignores_what_it_does_not_select():
+@pytest.mark.parametrize("H", [8, 40])
+def test_attention_ignores_what_it_does_not_select(H):
     """NaN and infinity in rows that no index names, exact single keys, and
     duplicates counted each time."""
     hs = lib()
@@ -281,11 +284,11 @@ def test_attention_ignores_what_it_does_not_select():
     rows, values = _cache(g, 64)
     rows[40:, :512] = 0x7F
     rows[40:, 512:640] = 0xFF
-    q = torch.as_tensor(g.standard_normal((2, 8, 576)).astype(np.float32)).to(torch.bfloat16)
+    q = torch.as_tensor(g.standard_normal((2, H, 576)).astype(np.float32)).to(torch.bfloat16)
     idx = np.array([[-1, 7, -1, 64], [3, 3, 5, -7]], np.int32)
     out, lse = _attend(hs, q.to(DEV), _t(rows), _t(idx), 1 / 24)
     _check(out, lse, _f64(q), values, idx, 1 / 24)
-    assert torch.equal(out[0].cpu(), torch.as_tensor(values[7, :512]).to(torch.bfloat16).expand(8, 512))
+    assert torch.equal(out[0].cpu(), torch.as_tensor(values[7, :512]).to(torch.bfloat16).expand(H, 512))
     # a selected NaN row reaches the output in every split
     idx = np.zeros((1, 2048), np.int32)
     idx[0, 2000] = 50
@@ -314,14 +317,15 @@ def test_attention_in_a_cache_past_4_gib():
     assert np.array_equal(_f64(back), values[-3:])
 
 
-def test_attention_on_a_side_stream_and_in_graphs():
+@pytest.mark.parametrize("H", [128, 10])
+def test_attention_on_a_side_stream_and_in_graphs(H):
     """Two captured calls, a workspace each, replayed on two streams at once
     over new inputs; the eager call on a side stream."""
     hs = lib()
     g = np.random.default_rng(12)
     rows, _ = _cache(g, 900)
     cache = _t(rows)
-    mk = lambda: (torch.as_tensor(g.standard_normal((3, 128, 576)).astype(np.float32)).to(torch.bfloat16).to(DEV),
+    mk = lambda: (torch.as_tensor(g.standard_normal((3, H, 576)).astype(np.float32)).to(torch.bfloat16).to(DEV),
                   _t(_indices(g, 3, 1500, 900, 0.1)))
     ins = [mk(), mk()]
     ws = [torch.empty(32 << 20, dtype=torch.uint8, device=DEV) for _ in range(2)]
@@ -456,12 +460,13 @@ def test_row_calls_on_a_side_stream():
     assert np.array_equal(_f64(back), O.q8_values(O.q8_quantise(_f64(src))))
 
 
-def test_attention_degenerate_calls_and_refusals():
+@pytest.mark.parametrize("H", [24, 9])
+def test_attention_degenerate_calls_and_refusals(H):
     hs = lib()
     g = np.random.default_rng(15)
     rows, values = _cache(g, 300)
     cache = _t(rows)
-    q = torch.as_tensor(g.standard_normal((2, 24, 576)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    q = torch.as_tensor(g.standard_normal((2, H, 576)).astype(np.float32)).to(torch.bfloat16).to(DEV)
     idx = _t(_indices(g, 2, 700, 300, 0.1))
     ref, ref_lse = _attend(hs, q, cache, idx, 1 / 24)
     _check(ref, ref_lse, _f64(q), values, np_(idx), 1 / 24)
@@ -498,13 +503,14 @@ def test_attention_degenerate_calls_and_refusals():
         hs.hs_sparse_attn_decode_q8(q.float(), cache, idx, 1 / 24, ref)
 
 
-def test_attention_leaves_its_neighbours_alone():
+@pytest.mark.parametrize("H", [50, 12])
+def test_attention_leaves_its_neighbours_alone(H):
     """Outputs and workspace in the middle of larger buffers: nothing around
     them is written."""
     hs = lib()
     g = np.random.default_rng(16)
     rows, _ = _cache(g, 500)
-    R, H, K = 3, 50, 640
+    R, K = 3, 640
     q = torch.as_tensor(g.standard_normal((R, H, 576)).astype(np.float32)).to(torch.bfloat16).to(DEV)
     idx = _t(_indices(g, R, K, 500, 0.0))
     pad_o = torch.full((R * H * 512 + 256,), 3.0, dtype=torch.bfloat16, device=DEV)
