@@ -1496,8 +1496,9 @@ constexpr int JOIN_FEW = 256;       // (row, head) pairs that leave a grid of on
 
 // Tiles of 32 keys, at least, in a part of a row: a cluster costs ~8 us whatever
 // its tiles (8, 4 and 2 tiles measured 15.3, 14.6 and 14.5 us on 4 rows of 2048
-// keys).
-constexpr int PART_MIN_TILES = 4;
+// keys). A block of the kernel for few heads costs less (4 and 2 tiles: 10.8 and
+// 9.7 us on one row of 16 heads and 2048 keys).
+constexpr int PART_MIN_TILES = 4, PART_MIN_TILES_FEW = 2;
 
 }  // namespace
 
@@ -1527,7 +1528,8 @@ extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n
     const int64_t base = (int64_t)R * ((H + HG - 1) / HG), rows = (int64_t)R * H;
     const int tiles = (K + NK - 1) / NK;
     int64_t n = places / base;
-    if (n > tiles / PART_MIN_TILES) n = tiles / PART_MIN_TILES;
+    const int least = few_heads ? PART_MIN_TILES_FEW : PART_MIN_TILES;
+    if (n > tiles / least) n = tiles / least;
     const int64_t room = (int64_t)(workspace_bytes / (rows * (DV + 1) * sizeof(float)));
     if (n > room) n = room;
     if (n > 1) {

@@ -13,16 +13,27 @@
 //     decoded goes through shared memory;
 //   * the eight partial S (16 heads x 32 keys), and two of the rope dims, meet
 //     in shared memory; warp w adds those of heads 2 w and 2 w + 1, takes their
-//     running maximum and sum (f32; 16 lanes a head) and writes P (bf16, as in
-//     k_attn_pair);
-//   * each warp scales its 64 dims of O (f32 registers) when a maximum moved and
-//     adds P V.
+//     maximum and sum (f32; 16 lanes a head) and writes P (bf16, as in
+//     k_attn_pair). A head's reference moves only when a score passes it by more
+//     than 30 (of the exponent of two), so P stays below 2^30;
+//   * each warp scales its 64 dims of O (f32 registers) when a reference moved
+//     and adds P V.
 // Raw rows come by cp.async, three tiles in flight, in places of 704 bytes (of
 // 656 used), which spreads a warp's reads over the banks.
 //
-// tcgen05 would want 128 rows of something: heads padded eightfold (k_attn_pair,
-// 94 us on 128 rows x 16 heads x 2048 keys), or keys and dims in that place, and
-// then every decoded tile through shared memory; mma.sync needs neither.
+// Measured, 16 heads (k_attn_pair, its heads padded to 128, in brackets): 8 rows
+// of 64 keys 5.2 us (7.3), 300 rows of one key 5.0 (31), 256 rows of 300 keys 25
+// (52), 128 rows of 2048 keys 74 (90), 512 rows 260 (312). What bounds the long
+// ones: a tile takes a block 3,450 clocks with another on its SM and 2,180
+// alone, a third of it reading and decoding, the rest the two meetings, the
+// transposition and P V; no pipe is busy for half of it. Sixteen warps of 32
+// dims: 101 us on 128 rows (twice the partial sums); two tiles in flight: 81;
+// the maximum of every tile: 76; copies packed into six instructions for
+// eight: 73.5, but 5.4 and 5.3 us in the first two cases.
+//
+// tcgen05 would want 128 rows of something: heads padded eightfold, or keys and
+// dims in that place, and then every decoded tile through shared memory;
+// mma.sync needs neither.
 
 #include <atomic>
 #include <math.h>
@@ -43,6 +54,7 @@ constexpr int P_STRIDE = 40;                   // bf16 values from head to head
 constexpr int S_OFF = STAGES * STAGE_BYTES;
 constexpr int P_OFF = S_OFF + PARTIALS * HEADS * S_STRIDE * 4;
 constexpr int ALPHA_OFF = P_OFF + HEADS * P_STRIDE * 2;
+constexpr float REF_SLACK = 30.f;
 constexpr int SMEM = ALPHA_OFF + HEADS * 4;
 static_assert(HEADS == 16 && 2 * WARPS == HEADS && HS_VALUE_DIM == 64 * WARPS, "layout");
 static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two blocks on an SM");
@@ -95,11 +107,15 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   // a programmatic dependent launch
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
+  // (volatile, so that it is loaded here, a tile before its use, and compared
+  // only there: the compiler would load it where it is used)
   auto index = [&](int t, int key) -> int32_t {
     const int k = t * KEYS + key;
-    const int32_t id = k < K ? __ldg(idx + k) : -1;
-    return id < a.n_kv ? id : -1;
+    int32_t i = -1;
+    if (k < K) asm volatile("ld.global.nc.b32 %0, [%1];\n" : "=r"(i) : "l"(idx + k));
+    return i;
   };
+  auto valid = [&](int32_t i) { return i >= 0 && i < a.n_kv; };
   // warp w copies keys 4 w .. 4 w + 3 of a tile; lane k < 4 holds the index of the
   // k-th, read a turn before
   int32_t id = index(0, 4 * warp + j);
@@ -109,10 +125,10 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int32_t i = __shfl_sync(0xffffffffu, id, k);
-        const char *row = i >= 0 ? a.kv + (int64_t)i * HS_Q8_ROW_BYTES : reinterpret_cast<const char *>(a.q);
-        cp16(to + k * ROW_STRIDE + 16 * lane, row + (i >= 0 ? 16 * lane : 0), i >= 0);
-        if (lane < HS_Q8_ROW_BYTES / 16 - 32)
-          cp16(to + k * ROW_STRIDE + 512 + 16 * lane, row + (i >= 0 ? 512 + 16 * lane : 0), i >= 0);
+        const bool v = valid(i);       // (else a copy of no bytes)
+        const char *row = (v ? a.kv + (int64_t)i * HS_Q8_ROW_BYTES : reinterpret_cast<const char *>(a.q)) + 16 * lane;
+        cp16(to + k * ROW_STRIDE + 16 * lane, row, v);
+        if (lane < HS_Q8_ROW_BYTES / 16 - 32) cp16(to + k * ROW_STRIDE + 512 + 16 * lane, row + 512, v);
       }
       id = index(t + 1, 4 * warp + j);
     }
@@ -148,18 +164,25 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   // softmax: this lane's head and its keys 2 c, 2 c + 1 of a tile
   const int head = 2 * warp + (lane >> 4), c = lane & 15;
   float m = -INFINITY, l = 0.f;
-  bool v0 = index(0, 2 * c) >= 0, v1 = index(0, 2 * c + 1) >= 0;
+  int32_t i0 = index(0, 2 * c), i1 = index(0, 2 * c + 1);
 
   asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 1) : "memory");
   __syncthreads();
   for (int t = 0; t < T; ++t) {
     const unsigned char *raw = sm + (t % STAGES) * STAGE_BYTES;
     uint32_t kf[4][4][2];
+    uint4 code[4];
+    uint32_t byte[4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
       const unsigned char *row = raw + (8 * nt + g) * ROW_STRIDE;
-      const uint4 w = *reinterpret_cast<const uint4 *>(row + 64 * warp + 16 * j);
-      const uint64_t sc = q8_scale2(row[Q8_SCALE_OFF + 2 * warp + (j >> 1)]);
+      code[nt] = *reinterpret_cast<const uint4 *>(row + 64 * warp + 16 * j);
+      byte[nt] = row[Q8_SCALE_OFF + 2 * warp + (j >> 1)];
+    }
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const uint4 w = code[nt];
+      const uint64_t sc = q8_scale2(byte[nt]);
       const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
       float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -195,20 +218,23 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
         s0 += x.x;
         s1 += x.y;
       }
-      s0 = v0 ? s0 * a.scale_log2 : -INFINITY;
-      s1 = v1 ? s1 * a.scale_log2 : -INFINITY;
-      v0 = index(t + 1, 2 * c) >= 0;
-      v1 = index(t + 1, 2 * c + 1) >= 0;
-      float top = fmaxf(s0, s1);
+      s0 = valid(i0) ? s0 * a.scale_log2 : -INFINITY;
+      s1 = valid(i1) ? s1 * a.scale_log2 : -INFINITY;
+      i0 = index(t + 1, 2 * c);
+      i1 = index(t + 1, 2 * c + 1);
+      float top = fmaxf(s0, s1), alpha = 1.f;
+      if (__any_sync(0xffffffffu, top > m + REF_SLACK)) {
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      top = fmaxf(top, m);
-      const float ref = top == -INFINITY ? 0.f : top;      // no key yet
-      const float alpha = ex2(m - ref);
-      m = top;
+        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(top, m);
+        alpha = top == -INFINITY ? 1.f : ex2(m - top);
+        m = top;
+        l *= alpha;
+      }
+      const float ref = m == -INFINITY ? 0.f : m;          // no key yet
       s0 = ex2(s0 - ref);
       s1 = ex2(s1 - ref);
-      l = l * alpha + (s0 + s1);
+      l += s0 + s1;
       *reinterpret_cast<uint32_t *>(sm + P_OFF + (head * P_STRIDE + 2 * c) * 2) = pack(s0, s1);
       if (c == 0) s_alpha[head] = alpha;
     }

@@ -315,7 +315,9 @@ int hs_dequant_rows(const void *src, int64_t src_rows, void *dst, int32_t dst_dt
 /*
  * hs_sparse_attn_decode over a q8 cache: the same arguments, formulas, skipped
  * entries and launch, with kv [n_kv_rows][656]. The values enter the products
- * as bf16 (exactly), the softmax numerators are rounded to bf16 as there.
+ * as bf16 (exactly), the softmax numerators are rounded to bf16 as there. With
+ * H > 16 and each row in one part the results are those of
+ * hs_sparse_attn_decode over the rows read back, bit for bit.
  * scale is finite and not negative.
  *   workspace   device memory, 16-byte aligned, or NULL: with few rows the
  *               keys of a row are split over the idle SMs and the parts'
