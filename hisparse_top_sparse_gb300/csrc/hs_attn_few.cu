@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   const int part = (int)(blockIdx.x % (unsigned)a.n), r = (int)(blockIdx.x / (unsigned)a.n);
   const int K = min(a.keys, a.K - part * a.keys), T = (K + KEYS - 1) / KEYS;
   const int32_t *idx = a.idx + (int64_t)r * a.K + (int64_t)part * a.keys;
-  // a programmatic dependent launch
+  // a programmatic dependent launch (its inputs may be written until here, so
+  // none is read by the non-coherent path)
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   // (volatile, so that it is loaded here, a tile before its use, and compared
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   auto index = [&](int t, int key) -> int32_t {
     const int k = t * KEYS + key;
     int32_t i = -1;
-    if (k < K) asm volatile("ld.global.nc.b32 %0, [%1];\n" : "=r"(i) : "l"(idx + k));
+    if (k < K) asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(i) : "l"(idx + k));
     return i;
   };
   auto valid = [&](int32_t i) { return i >= 0 && i < a.n_kv; };
@@ -146,9 +147,9 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
     uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0, w2 = w0;
     if (g + 8 * hh < a.H) {
       const __nv_bfloat16 *row = a.q + ((int64_t)r * a.H + g + 8 * hh) * HS_LATENT_DIM;
-      w0 = __ldg(reinterpret_cast<const uint4 *>(row + 64 * warp + 16 * j));
-      w1 = __ldg(reinterpret_cast<const uint4 *>(row + 64 * warp + 16 * j + 8));
-      w2 = __ldg(reinterpret_cast<const uint4 *>(row + HS_VALUE_DIM + 16 * j + 8 * half));
+      w0 = *reinterpret_cast<const uint4 *>(row + 64 * warp + 16 * j);
+      w1 = *reinterpret_cast<const uint4 *>(row + 64 * warp + 16 * j + 8);
+      w2 = *reinterpret_cast<const uint4 *>(row + HS_VALUE_DIM + 16 * j + 8 * half);
     }
     qa[0][hh] = w0.x, qa[0][2 + hh] = w0.y, qa[1][hh] = w0.z, qa[1][2 + hh] = w0.w;
     qa[2][hh] = w1.x, qa[2][2 + hh] = w1.y, qa[3][hh] = w1.z, qa[3][2 + hh] = w1.w;
