@@ -27,9 +27,10 @@
 // ones: a tile takes a block 3,450 clocks with another on its SM and 2,180
 // alone, a third of it reading and decoding, the rest the two meetings, the
 // transposition and P V; no pipe is busy for half of it. Sixteen warps of 32
-// dims: 101 us on 128 rows (twice the partial sums); two tiles in flight: 81;
-// the maximum of every tile: 76; copies packed into six instructions for
-// eight: 73.5, but 5.4 and 5.3 us in the first two cases.
+// dims: 101 us on 128 rows (twice the partial sums); rows by one bulk copy each:
+// 92; two tiles in flight: 81, four: 76; the maximum of every tile: 76; copies
+// packed into six instructions for eight: 73.5, but 5.4 and 5.3 us in the first
+// two cases.
 //
 // tcgen05 would want 128 rows of something: heads padded eightfold, or keys and
 // dims in that place, and then every decoded tile through shared memory;
