@@ -22,15 +22,15 @@
 // 656 used), which spreads a warp's reads over the banks.
 //
 // Measured, 16 heads (k_attn_pair, its heads padded to 128, in brackets): 8 rows
-// of 64 keys 5.2 us (7.3), 300 rows of one key 5.0 (31), 256 rows of 300 keys 25
-// (52), 128 rows of 2048 keys 74 (90), 512 rows 260 (312). What bounds the long
-// ones: a tile takes a block 3,450 clocks with another on its SM and 2,180
-// alone, a third of it reading and decoding, the rest the two meetings, the
-// transposition and P V; no pipe is busy for half of it. Sixteen warps of 32
-// dims: 101 us on 128 rows (twice the partial sums); rows by one bulk copy each:
-// 92; two tiles in flight: 81, four: 76; the maximum of every tile: 76; copies
-// packed into six instructions for eight: 73.5, but 5.4 and 5.3 us in the first
-// two cases.
+// of 64 keys 5.0 us (7.3), 300 rows of one key 5.0 (31), 256 rows of 300 keys 24
+// (52), 128 rows of 2048 keys 67 (90), 512 rows 236 (312). What bounds the long
+// ones is sixteen warps an SM, each a chain of a tile's reading, decoding,
+// products and meetings: an instruction issues on 40 % of the cycles, no pipe is
+// busy for half of them, and fewer instructions is what has helped (sums two at
+// a time, the keys' validity from the copying warp: 74 before). Tried: sixteen
+// warps of 32 dims 101 us on 128 rows (twice the partial sums, 64 registers);
+// rows by one bulk copy each 92; two tiles in flight 81, four 76; the maximum
+// of every tile 76 (of 74).
 //
 // tcgen05 would want 128 rows of something: heads padded eightfold, or keys and
 // dims in that place, and then every decoded tile through shared memory;
@@ -56,7 +56,10 @@ constexpr int S_OFF = STAGES * STAGE_BYTES;
 constexpr int P_OFF = S_OFF + PARTIALS * HEADS * S_STRIDE * 4;
 constexpr int ALPHA_OFF = P_OFF + HEADS * P_STRIDE * 2;
 constexpr float REF_SLACK = 30.f;
-constexpr int SMEM = ALPHA_OFF + HEADS * 4;
+// which keys have a row: a byte for each warp's four, of STAGES + 1 tiles (a
+// tile's bits are read after the place of its raw rows has been given away)
+constexpr int VALID_OFF = ALPHA_OFF + HEADS * 4, VALID_TILES = STAGES + 1;
+constexpr int SMEM = VALID_OFF + VALID_TILES * WARPS;
 static_assert(HEADS == 16 && 2 * WARPS == HEADS && HS_VALUE_DIM == 64 * WARPS, "layout");
 static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two blocks on an SM");
 
@@ -90,8 +93,13 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
   return d;
+}
+// two f32 sums
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  asm("add.rn.f32x2 %0, %0, %1;\n" : "+l"(a) : "l"(b));
+  return a;
 }
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -117,27 +125,30 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
     if (k < K) asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(i) : "l"(idx + k));
     return i;
   };
-  auto valid = [&](int32_t i) { return i >= 0 && i < a.n_kv; };
   // warp w copies keys 4 w .. 4 w + 3 of a tile; lane k < 4 holds the index of the
   // k-th, read a turn before
   int32_t id = index(0, 4 * warp + j);
-  auto copy = [&](int t) {
+  const char *kv = a.kv + 16 * lane;
+  auto copy = [&](int t, int stage) {
     if (t < T) {
-      const uint32_t to = smem_addr(sm) + (t % STAGES) * STAGE_BYTES + 4 * warp * ROW_STRIDE;
+      const uint32_t to = smem_addr(sm) + stage * STAGE_BYTES + 4 * warp * ROW_STRIDE + 16 * lane;
+      const bool valid = id >= 0 && id < a.n_kv;
+      const uint32_t have = __ballot_sync(0xffffffffu, valid);
+      if (lane == 0) sm[VALID_OFF + (t % VALID_TILES) * WARPS + warp] = have & 15u;
+      if (!valid) id = 0;                      // (of which no byte is copied)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int32_t i = __shfl_sync(0xffffffffu, id, k);
-        const bool v = valid(i);       // (else a copy of no bytes)
-        const char *row = (v ? a.kv + (int64_t)i * HS_Q8_ROW_BYTES : reinterpret_cast<const char *>(a.q)) + 16 * lane;
-        cp16(to + k * ROW_STRIDE + 16 * lane, row, v);
-        if (lane < HS_Q8_ROW_BYTES / 16 - 32) cp16(to + k * ROW_STRIDE + 512 + 16 * lane, row + 512, v);
+        const char *row = kv + (int64_t)__shfl_sync(0xffffffffu, id, k) * HS_Q8_ROW_BYTES;
+        const bool v = (have >> k) & 1u;
+        cp16(to + k * ROW_STRIDE, row, v);
+        if (lane < HS_Q8_ROW_BYTES / 16 - 32) cp16(to + k * ROW_STRIDE + 512, row + 512, v);
       }
       id = index(t + 1, 4 * warp + j);
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
   };
 #pragma unroll 1
-  for (int t = 0; t < STAGES; ++t) copy(t);
+  for (int t = 0; t < STAGES; ++t) copy(t, t);
 
   // Q of the warp's 64 dims (four contractions of 16) and of the rope dims
   // [16 j + 8 half, + 8) of every column (two): heads g and g + 8
@@ -166,12 +177,11 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   // softmax: this lane's head and its keys 2 c, 2 c + 1 of a tile
   const int head = 2 * warp + (lane >> 4), c = lane & 15;
   float m = -INFINITY, l = 0.f;
-  int32_t i0 = index(0, 2 * c), i1 = index(0, 2 * c + 1);
 
   asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 1) : "memory");
   __syncthreads();
-  for (int t = 0; t < T; ++t) {
-    const unsigned char *raw = sm + (t % STAGES) * STAGE_BYTES;
+  for (int t = 0, stage = 0; t < T; ++t) {
+    const unsigned char *raw = sm + stage * STAGE_BYTES;
     uint32_t kf[4][4][2];
     uint4 code[4];
     uint32_t byte[4];
@@ -211,21 +221,22 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
       *reinterpret_cast<float2 *>(to + 8 * S_STRIDE) = make_float2(s[2], s[3]);
     }
     __syncthreads();                 // the partial sums are in place, the raw tile is free
-    copy(t + STAGES);
+    copy(t + STAGES, stage);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    bool moved = false;              // (the whole warp)
     {
-      float s0 = 0.f, s1 = 0.f;
+      uint64_t sum = 0;
 #pragma unroll
-      for (int p = 0; p < PARTIALS; ++p) {
-        const float2 x = *reinterpret_cast<const float2 *>(s_part + (p * HEADS + head) * S_STRIDE + 2 * c);
-        s0 += x.x;
-        s1 += x.y;
-      }
-      s0 = valid(i0) ? s0 * a.scale_log2 : -INFINITY;
-      s1 = valid(i1) ? s1 * a.scale_log2 : -INFINITY;
-      i0 = index(t + 1, 2 * c);
-      i1 = index(t + 1, 2 * c + 1);
+      for (int p = 0; p < PARTIALS; ++p)
+        sum = add2(sum, *reinterpret_cast<const uint64_t *>(s_part + (p * HEADS + head) * S_STRIDE + 2 * c));
+      float s0, s1;
+      asm("mov.b64 {%0, %1}, %2;\n" : "=f"(s0), "=f"(s1) : "l"(sum));
+      const uint32_t have = sm[VALID_OFF + (t % VALID_TILES) * WARPS + (c >> 1)] >> (2 * (c & 1));
+      s0 = have & 1u ? s0 * a.scale_log2 : -INFINITY;
+      s1 = have & 2u ? s1 * a.scale_log2 : -INFINITY;
       float top = fmaxf(s0, s1), alpha = 1.f;
-      if (__any_sync(0xffffffffu, top > m + REF_SLACK)) {
+      moved = __any_sync(0xffffffffu, top > m + REF_SLACK);
+      if (moved) {
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         top = fmaxf(top, m);
@@ -241,10 +252,10 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
       if (c == 0) s_alpha[head] = alpha;
     }
     asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 1) : "memory");
-    __syncthreads();                 // P and the next raw tile are in place
+    moved = __syncthreads_or(moved);       // P and the next raw tile are in place
     {
-      const float a0 = s_alpha[g], a1 = s_alpha[g + 8];
-      if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
+      if (moved) {
+        const float a0 = s_alpha[g], a1 = s_alpha[g + 8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           o[k >> 1][k & 1][0] *= a0;
