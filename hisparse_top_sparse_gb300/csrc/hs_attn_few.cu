@@ -128,14 +128,15 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   // warp w copies keys 4 w .. 4 w + 3 of a tile; lane k < 4 holds the index of the
   // k-th, read a turn before
   int32_t id = index(0, 4 * warp + j);
-  const char *kv = a.kv + 16 * lane;
+  // (a copy of no bytes has an address all the same: row 0, of an empty cache q)
+  const char *kv = (a.n_kv > 0 ? a.kv : reinterpret_cast<const char *>(a.q)) + 16 * lane;
   auto copy = [&](int t, int stage) {
     if (t < T) {
       const uint32_t to = smem_addr(sm) + stage * STAGE_BYTES + 4 * warp * ROW_STRIDE + 16 * lane;
       const bool valid = id >= 0 && id < a.n_kv;
       const uint32_t have = __ballot_sync(0xffffffffu, valid);
       if (lane == 0) sm[VALID_OFF + (t % VALID_TILES) * WARPS + warp] = have & 15u;
-      if (!valid) id = 0;                      // (of which no byte is copied)
+      if (!valid) id = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const char *row = kv + (int64_t)__shfl_sync(0xffffffffu, id, k) * HS_Q8_ROW_BYTES;
