@@ -1104,7 +1104,14 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
       }
       if (timed_out) break;
       if (n_own == 0) {
-        if (pass == 0 && !agree_ref(-INFINITY)) { timed_out = true; break; }
+        // A CTA without an own tile has seen no S, so this warp does not know yet
+        // that Q has left its staging places, one of which the peer's P lands on:
+        // its maxima, which the peer waits for before it sends any P, go out
+        // only once it has.
+        if (pass == 0 && (!warp_wait(bar(B_QSTAGED), 0) || !agree_ref(-INFINITY))) {
+          timed_out = true;
+          break;
+        }
         send_end();
       }
 
