@@ -141,10 +141,13 @@ __device__ __forceinline__ float clean(float x) {
 }
 
 template <int DTYPE>
+__device__ __forceinline__ float raw_logit_at(const void *row, int64_t i) {
+  if (DTYPE == HS_LOGITS_F32) return __ldg(reinterpret_cast<const float *>(row) + i);
+  return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(row) + i) << 16);
+}
+template <int DTYPE>
 __device__ __forceinline__ float logit_at(const void *row, int64_t i) {
-  if (DTYPE == HS_LOGITS_F32) return clean<DTYPE>(__ldg(reinterpret_cast<const float *>(row) + i));
-  const uint32_t u = __ldg(reinterpret_cast<const unsigned short *>(row) + i);
-  return clean<DTYPE>(__uint_as_float(u << 16));
+  return clean<DTYPE>(raw_logit_at<DTYPE>(row, i));
 }
 
 // (a, b) packed for the two-at-a-time f32 instructions
@@ -509,13 +512,6 @@ __device__ __forceinline__ Race race(const char *row, const float *q, const floa
                                      uint32_t rank, uint32_t log_n, const RaceRow &rr, uint4 *ring) {
   Race ra = {0.f, INT32_MAX, 0.f};
   const uint64_t nm = pack2(-rr.top, -rr.top), cc = pack2(rr.c, rr.c), ii = pack2(rr.inv, rr.inv);
-  // a logit of +inf, which counts as the row's maximum, has come out infinite:
-  // its weight is that of the maximum
-  auto mend = [&](float &r, float w, float e) {
-    float f;
-    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(f) : "f"(e));
-    if (r == INFINITY) r = (rr.inv - w) * f;
-  };
   // the block's values: whole vectors of logits
   constexpr int PER = Slice<DTYPE>::PER;
   const int32_t vecs = (V + PER - 1) / PER, lo = part_of(vecs, rank, log_n) * PER,
@@ -620,12 +616,11 @@ __device__ __forceinline__ Race race(const char *row, const float *q, const floa
         big = fmaxf(big, fmaxf(r[o], r[o + 1]));
       }
       const bool cut = v0 + UNIT > hi;             // (the places past hi: what they held)
-      if (cut || (rr.barred >= v0 && rr.barred < v0 + UNIT) || big == INFINITY) {
+      if (cut || (rr.barred >= v0 && rr.barred < v0 + UNIT)) {
         big = 0.f;
 #pragma unroll
         for (int o = 0; o < PER; ++o) {
           const int32_t v = value_at(o);
-          mend(r[o], w[o], e[o]);
           if (v >= hi || v == rr.barred) r[o] = 0.f;
           big = fmaxf(big, r[o]);
         }
@@ -646,9 +641,7 @@ __device__ __forceinline__ Race race(const char *row, const float *q, const floa
         e[u] = 1.f;
         w[u] = 0.f;
         if (v < hi) {
-          r[u] = DTYPE == HS_LOGITS_F32
-                     ? __ldg(reinterpret_cast<const float *>(row) + v)
-                     : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(row) + v) << 16);
+          r[u] = raw_logit_at<DTYPE>(row, v);
           e[u] = __ldcs(E + v);
           if (HAS_Q) w[u] = __ldcs(q + v);
         }
@@ -659,18 +652,43 @@ __device__ __forceinline__ Race race(const char *row, const float *q, const floa
         big = fmaxf(big, fmaxf(r[u], r[u + 1]));
       }
       const int32_t v0 = k0 + (int)threadIdx.x;
-      if (big == INFINITY || rr.barred >= 0) {
+      if (rr.barred >= 0) {
 #pragma unroll
-        for (int u = 0; u < NB; ++u) {
-          mend(r[u], w[u], e[u]);
+        for (int u = 0; u < NB; ++u)
           if (v0 + u * NT == rr.barred) r[u] = 0.f;
-        }
         big = 0.f;
 #pragma unroll
         for (int u = 0; u < NB; ++u) big = fmaxf(big, r[u]);
       }
       ra.template group<NB>(r, big, [&](int u) { return v0 + u * NT; });
     }
+  }
+  return ra;
+}
+
+// The race for every noise and logit. ratio2 gives 0 for a noise whose reciprocal
+// is below the normal floats, and infinity for one above them and for a logit
+// of +inf: a race whose winner is infinite, or one that a noise past E_MAX could
+// have won (no ratio reaches SMALL), is run again here, over noise within
+// [E_MIN, E_MAX] and logits as they count, each ratio times scale^2. Where both
+// races are exact their ratios are the same bits.
+constexpr float E_MIN = 0x1p-126f, E_MAX = 0x1p126f, SMALL = 0x1p-125f;
+template <int DTYPE>
+__device__ __noinline__ Race careful_race(const char *row, const float *q, const float *E, int32_t V, uint32_t rank,
+                                          uint32_t log_n, const RaceRow rr, float scale) {
+  Race ra = {0.f, INT32_MAX, 0.f};
+  const int32_t lo = part_of(V, rank, log_n), hi = part_of(V, rank + 1, log_n);
+#pragma unroll 1
+  for (int32_t k = lo; k < hi; k += NT) {
+    const int32_t v = k + (int)threadIdx.x;
+    float r[1] = {0.f};
+    if (v < hi && v != rr.barred) {
+      const float w = fmaf(ex2((logit_at<DTYPE>(row, v) - rr.top) * rr.c), rr.inv, q ? -q[v] : 0.f);
+      float f;
+      asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(f) : "f"(fminf(fmaxf(E[v], E_MIN), E_MAX)));
+      r[0] = fmaxf((w * scale) * (f * scale), 0.f);
+    }
+    ra.template group<1>(r, r[0], [&](int) { return v; });
   }
   return ra;
 }
@@ -775,23 +793,36 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
     const float *E = sa.noise + (int64_t)b * V;
     const float *q = sa.probs && m < d ? sa.probs + ((int64_t)b * d + m) * V : nullptr;
     int32_t barred = !sa.probs && m < d ? sh.draft[m] : -1;   // a sure draft's own token
+    float scale = 0.f;                                        // (0: the race proper)
     for (;;) {
       const RaceRow rr = {top, c, inv, barred};
       Race ra;
-      switch (sa.rows) {
-        case ROWS_ON_16:
-          ra = q ? race<DTYPE, ROWS_ON_16, true>(row, q, E, V, rank, log_n, rr, ring_base)
-                 : race<DTYPE, ROWS_ON_16, false>(row, q, E, V, rank, log_n, rr, ring_base);
-          break;
-        case ARRAYS_ON_16:
-          ra = q ? race<DTYPE, ARRAYS_ON_16, true>(row, q, E, V, rank, log_n, rr, ring_base)
-                 : race<DTYPE, ARRAYS_ON_16, false>(row, q, E, V, rank, log_n, rr, ring_base);
-          break;
-        default:
-          ra = q ? race<DTYPE, ROWS_ANYWHERE, true>(row, q, E, V, rank, log_n, rr, ring_base)
-                 : race<DTYPE, ROWS_ANYWHERE, false>(row, q, E, V, rank, log_n, rr, ring_base);
+      if (scale > 0.f) {
+        ra = careful_race<DTYPE>(row, q, E, V, rank, log_n, rr, scale);
+      } else {
+        switch (sa.rows) {
+          case ROWS_ON_16:
+            ra = q ? race<DTYPE, ROWS_ON_16, true>(row, q, E, V, rank, log_n, rr, ring_base)
+                   : race<DTYPE, ROWS_ON_16, false>(row, q, E, V, rank, log_n, rr, ring_base);
+            break;
+          case ARRAYS_ON_16:
+            ra = q ? race<DTYPE, ARRAYS_ON_16, true>(row, q, E, V, rank, log_n, rr, ring_base)
+                   : race<DTYPE, ARRAYS_ON_16, false>(row, q, E, V, rank, log_n, rr, ring_base);
+            break;
+          default:
+            ra = q ? race<DTYPE, ROWS_ANYWHERE, true>(row, q, E, V, rank, log_n, rr, ring_base)
+                   : race<DTYPE, ROWS_ANYWHERE, false>(row, q, E, V, rank, log_n, rr, ring_base);
+        }
       }
       cluster_join(sh, ra.best, ra.at, rank, n, 0, turn, BestOp{});
+      if (scale == 0.f && ra.best == INFINITY) {
+        scale = 1.f;
+        continue;
+      }
+      if (scale < 2.f && ra.best < SMALL) {                   // (times 2^126: none vanishes)
+        scale = 0x1p63f;
+        continue;
+      }
       if (ra.at != INT32_MAX) {
         token = (int32_t)ra.at;
         break;
@@ -801,6 +832,7 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
       // equal, up to rounding): the target's own
       q = nullptr;
       barred = -1;
+      scale = 0.f;
     }
   }
 

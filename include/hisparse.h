@@ -669,7 +669,8 @@ int hs_verify_accept_noalloc(const void *logits, int32_t logits_dtype, int32_t B
  *   draft_tokens  device int32 [B][d]
  *   draft_probs   device float [B][d][V] or NULL
  *   uniforms      device float [B][d]
- *   noise         device float [B][V], > 0
+ *   noise         device float [B][V], > 0; below 2^-126 it counts as 2^-126,
+ *                 above 2^126 as 2^126
  *   accept_len, next_token  device int32 [B]
  *   logprob       device float [B][d+1] or NULL: ln p_i of each token given
  *                 (the accepted drafts, then next_token), 0 behind them; for a

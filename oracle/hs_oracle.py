@@ -706,8 +706,9 @@ def verify_sample(logits, temperature, drafts, probs, uniforms, noise):
     draft probabilities (1 at the draft when ``probs`` is None). The next token
     is argmax ``w / noise`` (lowest index on ties, w > 0 only), ``w = max(p -
     q, 0)`` at the refused draft (p itself if that vanishes), p past the last.
-    T <= 0 or NaN: greedy. Masked logits (-inf, NaN) have p = 0, +inf counts as
-    ``logits_max``; a row of masked ones accepts nothing and gives -1.
+    Noise counts as within [2^-126, 2^126]. T <= 0 or NaN: greedy. Masked
+    logits (-inf, NaN) have p = 0, +inf counts as ``logits_max``; a row of
+    masked ones accepts nothing and gives -1.
 
     Returns ``(accept, token, logprob [B][d+1], margin [B])``: margin is the
     smallest relative distance between two numbers that a decision compared.
@@ -774,7 +775,7 @@ def verify_sample(logits, temperature, drafts, probs, uniforms, noise):
                     w[dr[b, m]] = 0.0
                 if not (w > 0).any():
                     w = p
-                r = np.where(w > 0, w / E[b], -1.0)
+                r = np.where(w > 0, w / np.clip(E[b], 2.0 ** -126, 2.0 ** 126), -1.0)
                 x = int(np.argmax(r))
                 rest = np.delete(r, x)
                 if rest.size and rest.max() > 0:
