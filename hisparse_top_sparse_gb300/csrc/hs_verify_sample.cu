@@ -29,9 +29,9 @@
 // The blocks of a cluster exchange (M, S) and the race's winner through
 // distributed shared memory, every warp joining all warps' figures in the
 // same order; the request's drafts, numbers and temperature are read once by
-// the first block and pushed to the others. So every block takes the same
+// the first block and pushed to the others. So every warp takes the same
 // decisions from the same bits, and the barriers match even if a caller
-// overwrites the inputs during the call.
+// overwrites the inputs during the call (what it then gets is unspecified).
 //
 // Measured (bf16 logits, draft probabilities given): 256 requests x 3 drafts,
 // V = 129280: 70 us, 82 % of what the 385 MB it has to move take at the
@@ -138,6 +138,21 @@ __device__ __forceinline__ float ex2(float x) {
 template <int DTYPE>
 __device__ __forceinline__ float clean(float x) {
   return fminf(fmaxf(x, -INFINITY), DTYPE == HS_LOGITS_F32 ? FLT_MAX : __uint_as_float(0x7f7f0000u));
+}
+
+// what is read once and given to every block (volatile: a second reading might
+// find something else)
+__device__ __forceinline__ uint32_t once(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(v) : "l"(p));
+  return v;
+}
+template <int DTYPE>
+__device__ __forceinline__ float logit_once(const void *row, int64_t i) {
+  if (DTYPE == HS_LOGITS_F32) return clean<DTYPE>(__uint_as_float(once(reinterpret_cast<const float *>(row) + i)));
+  unsigned short u;
+  asm volatile("ld.global.u16 %0, [%1];\n" : "=h"(u) : "l"(reinterpret_cast<const unsigned short *>(row) + i));
+  return clean<DTYPE>(__uint_as_float((uint32_t)u << 16));
 }
 
 template <int DTYPE>
@@ -388,12 +403,17 @@ struct Shared {
 // for each of the G = 2^log_g rows (row g the blocks of ranks g n / G and up).
 // Each warp joins its own threads' pairs and pushes the result to every block;
 // behind the cluster's barrier every warp joins all warps' pairs, in the same
-// order everywhere. On return lane g * 32 / G holds row g's. A place of `pair`
+// order everywhere (`behind` runs first: it may set op from what the first block
+// has pushed). On return lane g * 32 / G holds row g's. A place of `pair`
 // is written again two calls later, behind the barrier of the call between,
 // by when it has been read.
-template <typename Op>
+struct Nothing {
+  __device__ __forceinline__ void operator()() const {}
+};
+template <typename Op, typename F = Nothing>
 __device__ __forceinline__ void cluster_join(Shared &sh, float &a, uint32_t &b, uint32_t rank,
-                                             uint32_t n, uint32_t log_g, int &turn, const Op &op) {
+                                             uint32_t n, uint32_t log_g, int &turn, const Op &op,
+                                             const F &behind = F{}) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   op.across(a, b, 32);
   uint2 *pairs = sh.pair[turn];
@@ -406,6 +426,7 @@ __device__ __forceinline__ void cluster_join(Shared &sh, float &a, uint32_t &b, 
     cluster_wait();
   }
   turn ^= 1;
+  behind();
   op.empty(a, b);
   // 32 / G lanes for the pairs of each row
   const uint32_t lanes = 32u >> log_g, count = (n >> log_g) * WARPS, row = lane / lanes;
@@ -712,9 +733,10 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
   static_assert(MAX_DRAFTS <= NT, "a thread per draft");
   int32_t x = -1;
   float x_logit = -INFINITY, x_bar = 0.f;
-  const float t_read = __ldg(sa.temperature + b);
+  const float t_read = __uint_as_float(once(sa.temperature + b));
   // within the normal floats: products with it are never 0 * inf
-  float c = fminf(fmaxf(LOG2E / (t_read > 0.f ? t_read : 1.f), FLT_MIN), FLT_MAX);
+  auto scale_of = [](float t) { return fminf(fmaxf(LOG2E / (t > 0.f ? t : 1.f), FLT_MIN), FLT_MAX); };
+  float c = scale_of(t_read);
 
   // Rows m0 .. m0 + G - 1 at a time, n / G blocks a row.
   const uint32_t log_n = 31 - __clz(n), log_g = sa.log_rows, G = 1u << log_g, per_row = n >> log_g;
@@ -729,14 +751,15 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
     const Stat st = row_stat<DTYPE>(sl, row, c, ring_base + tid, [&]() {
       if (m0 != 0 || rank != 0 || tid >= d) return;
       const int64_t k = (int64_t)b * d + tid;
-      x = __ldg(sa.drafts + k);
+      x = (int32_t)once(sa.drafts + k);
       const bool ok = x >= 0 && x < V;         // any other token is refused
       if (!ok) {
         x = -1;
         if (sa.status) atomicOr(sa.status, HS_STATUS_INDEX);
       }
-      x_logit = ok ? logit_at<DTYPE>(rows + tid * row_bytes, x) : -INFINITY;
-      x_bar = __ldg(sa.uniforms + k) * (sa.probs && ok ? __ldg(sa.probs + k * V + x) : 1.f);
+      x_logit = ok ? logit_once<DTYPE>(rows + tid * row_bytes, x) : -INFINITY;
+      x_bar = __uint_as_float(once(sa.uniforms + k)) *
+              (sa.probs && ok ? __uint_as_float(once(sa.probs + k * V + x)) : 1.f);
     });
     if (m0 == 0) {
       if (n > 1) cluster_wait();
@@ -753,12 +776,15 @@ __global__ void __launch_bounds__(NT, MIN_BLOCKS) k_verify_sample(const __grid_c
     }
     float tops = st.m;
     uint32_t sums = __float_as_uint(st.s);
-    cluster_join(sh, tops, sums, rank, n, log_g, turn, StatOp{c});
-    if (m0 == 0) {
-      greedy = !(sh.temperature > 0.f);
-      T = greedy ? 1.f : sh.temperature;
-      c = fminf(fmaxf(LOG2E / T, FLT_MIN), FLT_MAX);
-    }
+    StatOp op{c};
+    cluster_join(sh, tops, sums, rank, n, log_g, turn, op, [&]() {
+      if (m0 != 0) return;
+      // from here on by the pushed temperature, the join of all warps' sums too
+      const float t = sh.temperature;
+      greedy = !(t > 0.f);
+      T = greedy ? 1.f : t;
+      op.c = c = scale_of(t);
+    });
     uint32_t firsts = INT32_MAX;
     if (greedy) {
       const float own = __shfl_sync(0xffffffffu, tops, (rank >> (log_n - log_g)) * (32 >> log_g));

@@ -100,3 +100,34 @@ def test_tiny_noise_beside_an_infinite_logit():
         got = _run(hs, logits, T, x, None, u, E)
         assert got[1].tolist() == [7, 200, 200, 200]
         assert O.verify_sample(logits, T, x, None, u, E)[1].tolist() == [7, 200, 200, 200]
+
+
+@pytest.mark.parametrize("B,d,V", [(1, 3, 40000), (2, 5, 3000), (60, 3, 20000)])
+def test_inputs_overwritten_during_the_call(B, d, V):
+    """Temperatures, numbers and drafts change while calls run: which of them a
+    call takes is not said, but all warps of a request take the same, so that
+    every call ends, with an answer of its range, and later ones are right."""
+    hs = lib()
+    c = _case(77, B, d, V, torch.bfloat16, True)
+    other = _case(78, B, d, V, torch.bfloat16, True)
+    logits, (T, x, q, u, E) = c[0].to(DEV), [_t(a) for a in c[1:]]
+    nT, nx, nu = _t(other[1]), _t(other[2]), _t(other[4])
+    nT[::2] = 0.0
+    acc = torch.empty((40, B), dtype=torch.int32, device=DEV)
+    nxt = torch.empty_like(acc)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for k in range(40):
+        hs.hs_verify_sample(logits, T, x, q, u, E, acc[k], nxt[k])
+        with torch.cuda.stream(side):
+            for a, b in ((T, nT), (x, nx), (u, nu)):
+                t = a.clone()
+                a.copy_(b)
+                b.copy_(t)
+    torch.cuda.synchronize()
+    assert int(acc.min()) >= 0 and int(acc.max()) <= d and int(nxt.min()) >= 0 and int(nxt.max()) < V
+    for a, b in zip((T, x, u), (c[1], c[2], c[4])):
+        a.copy_(_t(b))
+    got = torch.empty(B, dtype=torch.int32, device=DEV), torch.empty(B, dtype=torch.int32, device=DEV)
+    hs.hs_verify_sample(logits, T, x, q, u, E, *got)
+    _check((np_(got[0]), np_(got[1]), None), O.verify_sample(*c))
