@@ -325,6 +325,22 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity));
 }
 
+// Loads of what the kernel before may still be writing when this one starts (a
+// programmatic dependent launch): not by the non-coherent path, which is for
+// memory that nobody writes while a kernel runs, and volatile, so that they stay
+// behind griddepcontrol.wait.
+__device__ __forceinline__ int32_t ld_global(const int32_t *p) {
+  int32_t v;
+  asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_global16(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
                "r"(valid ? 16 : 0)
@@ -630,9 +646,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
   // the row's cache: the paged resident cache while its request is fully
   // resident, else the hot buffer its swap-in indices address
   // (a request id outside [0, n_reqs) leaves the row without a valid entry)
-  const int32_t req = fully_resident ? (row_req ? __ldg(row_req + r) : r) : 0;
+  const int32_t req = fully_resident ? (row_req ? ld_global(row_req + r) : r) : 0;
   const bool req_ok = !fully_resident || (req >= 0 && req < n_reqs);
-  const bool hot = req_ok && fully_resident && __ldg(fully_resident + req) == 0;
+  const bool hot = req_ok && fully_resident && ld_global(fully_resident + req) == 0;
   const char *kv = hot ? kv_hot : kv_res;
   const int64_t n_kv = !req_ok ? 0 : hot ? n_hot : n_res;
   if (!req_ok && status && tid == 0 && c == 0) atomicOr(status, HS_STATUS_INDEX);
@@ -658,7 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     const int p = 32 * lw + lane;
     auto load_id = [&](int t) -> int32_t {
       const int j = t * NK + key;
-      return (t < T && j < K) ? __ldg(idx_row + j) : -1;
+      return (t < T && j < K) ? ld_global(idx_row + j) : -1;
     };
     // 16 codes into two chunks of a swizzled 64-dim block
     auto put = [&](uint32_t to, const uint4 w, uint32_t byte) {
@@ -700,9 +716,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
           const uint4 *row = reinterpret_cast<const uint4 *>(v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q);
           const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) code[k] = v ? __ldg(row + sub + 8 * k) : zero;
-          rope = v ? __ldg(row + Q8_ROPE_OFF / 16 + sub) : zero;
-          scale = v ? __ldg(row + Q8_SCALE_OFF / 16) : zero;
+          for (int k = 0; k < 4; ++k) code[k] = v ? ld_global16(row + sub + 8 * k) : zero;
+          rope = v ? ld_global16(row + Q8_ROPE_OFF / 16 + sub) : zero;
+          scale = v ? ld_global16(row + Q8_SCALE_OFF / 16) : zero;
           copied = 1;
         } else {
           if (!warp_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
@@ -816,7 +832,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     const int sub = p & 7;            // chunk sub of every 64-dim block
     auto load_id = [&](int t) -> int32_t {
       const int j = t * NK + key;
-      return (t < T && j < K) ? __ldg(idx_row + j) : -1;
+      return (t < T && j < K) ? ld_global(idx_row + j) : -1;
     };
     int ig = 0, jg = 0;               // own / peer tiles issued, over both passes
     for (int pass = 0; pass < 2 && !timed_out; ++pass) {
@@ -1010,7 +1026,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     bool flag = false, ref_unset = false, decided = false;
     int ig = 0, last_pass = 0;
     auto load_id = [&](int t) -> int32_t {
-      return (t < T && t * NK + lane < K) ? __ldg(idx_row + t * NK + lane) : -1;
+      return (t < T && t * NK + lane < K) ? ld_global(idx_row + t * NK + lane) : -1;
     };
     // the peer's first-tile maxima, taken once
     auto agree_ref = [&](float mt) -> bool {
@@ -1451,11 +1467,13 @@ namespace {
 // a fixed order. Latency bounds a small grid: four groups read its parts in
 // as few rounds as they allow (one row of 128 heads, 16 parts: 12.8 us for the
 // whole call against 13.7 with one group, 64 parts: 17.1 against 21.2); a
-// large one fills the SMs and takes one (16 rows: 23.2 us against 26.6).
+// large one fills the SMs and takes one (16 rows: 23.2 us against 26.6). The
+// parts are written while this kernel may already run (until the wait), so they
+// are not read-only to it: no __restrict__, which would let the compiler take
+// the non-coherent path.
 template <int GROUPS>
 __global__ void __launch_bounds__(GROUPS * DV / 4)
-    k_attn_join(const float *__restrict__ o, const float *__restrict__ part_lse, int32_t n, int64_t rows,
-                __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
+    k_attn_join(const float *o, const float *part_lse, int32_t n, int64_t rows, __nv_bfloat16 *out, float *lse) {
   // a programmatic dependent launch of the kernel that writes the parts
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int64_t row = blockIdx.x;
