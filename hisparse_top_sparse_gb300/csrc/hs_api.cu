@@ -28,6 +28,13 @@ int hs_set_error(int code, const char *fmt, ...) {
 
 extern "C" const char *hs_last_error_string(void) { return g_err; }
 
+int hs_bind_context() {
+  int dev = 0;
+  HS_CUDA_TRY(cudaGetDevice(&dev));
+  HS_CUDA_TRY(cudaSetDevice(dev));
+  return HS_OK;
+}
+
 int hs_sm_count(int *sms) {
   static std::atomic<int> known[64];
   int dev = 0;
@@ -51,12 +58,16 @@ int hs_device_alias(const void *p, const void **out, const char *name, int align
   if (!p) return hs_set_error(HS_ERR_INVALID_ARG, "%s is NULL", name);
   if ((uintptr_t)p % (uintptr_t)align)
     return hs_set_error(HS_ERR_INVALID_ARG, "%s must be %d-byte aligned", name, align);
-  cudaPointerAttributes attr;
-  HS_CUDA_TRY(cudaPointerGetAttributes(&attr, p));
   *out = nullptr;
-  if (attr.type == cudaMemoryTypeHost || attr.type == cudaMemoryTypeDevice ||
-      attr.type == cudaMemoryTypeManaged)
-    *out = attr.devicePointer;
+  for (int turn = 0; turn < 2 && !*out; ++turn) {
+    int rc = turn ? hs_bind_context() : HS_OK;     // (without a context nothing is known of p)
+    if (rc) return rc;
+    cudaPointerAttributes attr;
+    HS_CUDA_TRY(cudaPointerGetAttributes(&attr, p));
+    if (attr.type == cudaMemoryTypeHost || attr.type == cudaMemoryTypeDevice ||
+        attr.type == cudaMemoryTypeManaged)
+      *out = attr.devicePointer;
+  }
   if (!*out)
     return hs_set_error(HS_ERR_INVALID_ARG,
                         "%s is not page-locked mapped host memory or device memory", name);

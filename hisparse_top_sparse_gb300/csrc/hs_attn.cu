@@ -1396,10 +1396,16 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
   const cuuint64_t gstride[2] = {(cuuint64_t)ROWB, (cuuint64_t)H * ROWB};
   const cuuint32_t box[3] = {64, HG, 1};
   const cuuint32_t estride[3] = {1, 1, 1};
-  const CUresult er = encode(&tmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), gdim,
-                             gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encode_q = [&]() {
+    return encode(&tmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), gdim, gstride, box, estride,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult er = encode_q();
+  if (er == CUDA_ERROR_INVALID_CONTEXT || er == CUDA_ERROR_NOT_INITIALIZED) {
+    if ((rc = hs_bind_context())) return rc;
+    er = encode_q();
+  }
   if (er != CUDA_SUCCESS) return hs_set_error(HS_ERR_CUDA, "tensor map of q failed (%d)", (int)er);
   // what the epilogue writes: out [R][H][512] bf16, or the parts [n R][H][512] f32
   alignas(64) CUtensorMap tmap_o;

@@ -70,6 +70,10 @@ int hs_set_error(int code, const char *fmt, ...);
                           cudaGetErrorString(e_));                             \
   } while (0)
 
+// Makes the current device's context this thread's. A thread's first runtime
+// call that needs a context does so by itself; what asks the driver for one
+// before that (a tensor map, a pointer's kind) calls this when it finds none.
+int hs_bind_context();
 // Multiprocessors of the current device (looked up once per device).
 int hs_sm_count(int *sms);
 // Attention over q8 rows for up to HS_ATTN_FEW_HEADS heads, its arguments
