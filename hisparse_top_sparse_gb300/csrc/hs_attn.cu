@@ -1316,8 +1316,8 @@ int hs_attn_wave_rows(int32_t H, int32_t *rows) {
   if (rc) return rc;
   int dev = 0;
   HS_CUDA_TRY(cudaGetDevice(&dev));
-  static int clusters[64] = {0};
-  int n = dev < 64 ? clusters[dev] : 0;
+  static std::atomic<int> clusters[64];
+  int n = dev < 64 ? clusters[dev].load(std::memory_order_relaxed) : 0;
   if (n == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
@@ -1332,7 +1332,7 @@ int hs_attn_wave_rows(int32_t H, int32_t *rows) {
     cfg.numAttrs = 1;
     HS_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_attn_pair<false>, &cfg));
     if (n < 1) n = 1;
-    if (dev < 64) clusters[dev] = n;
+    if (dev < 64) clusters[dev].store(n, std::memory_order_relaxed);
   }
   const int per_row = (H + HG - 1) / HG;
   *rows = n / per_row > 0 ? n / per_row : 1;
@@ -1381,7 +1381,8 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
   const int64_t blocks = (int64_t)R * ((H + HG - 1) / HG) * 2 * parts.n;
   if (blocks > INT32_MAX) return hs_set_error(HS_ERR_UNSUPPORTED, "R*H too large");
   // q as a [R][H][576] bf16 tensor for the prologue's tensor copies
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 encode = known.load(std::memory_order_relaxed);
   if (!encode) {
     cudaDriverEntryPointQueryResult qr;
     void *fn = nullptr;
@@ -1390,6 +1391,7 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
         qr != cudaDriverEntryPointSuccess || !fn)
       return hs_set_error(HS_ERR_CUDA, "cuTensorMapEncodeTiled not available");
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    known.store(encode, std::memory_order_relaxed);
   }
   alignas(64) CUtensorMap tmap;
   const cuuint64_t gdim[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)R};
