@@ -1544,9 +1544,10 @@ extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n
     return hs_set_error(HS_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   if (((uintptr_t)idx | (uintptr_t)lse | (uintptr_t)status) & 3)
     return hs_set_error(HS_ERR_INVALID_ARG, "idx, lse and status must be 4-byte aligned");
-  // the softmax reference is the scaled maximum, which a negative scale would not give
-  if (!(scale >= 0.f) || scale > FLT_MAX)
-    return hs_set_error(HS_ERR_INVALID_ARG, "scale must be finite and not negative");
+  // the softmax reference is the scaled maximum, which a negative scale would not
+  // give; times log2(e), as the kernels take it, the scale is to be finite too
+  if (!(scale >= 0.f) || scale > 0x1p127f)
+    return hs_set_error(HS_ERR_INVALID_ARG, "scale must be in [0, 2^127]");
   if (scale < FLT_MIN) scale = FLT_MIN;      // equal weights all the same; 0 times a masked -inf is NaN
   int rc = check_attn(q, kv, n_kv_rows, nullptr, 0, nullptr, 0, idx, R, H, K, scale, out);
   if (rc || R == 0) return rc;

@@ -318,7 +318,7 @@ int hs_dequant_rows(const void *src, int64_t src_rows, void *dst, int32_t dst_dt
  * as bf16 (exactly), the softmax numerators are rounded to bf16 as there. With
  * H > 16 and each row in one part the results are those of
  * hs_sparse_attn_decode over the rows read back, bit for bit.
- * scale is finite and not negative.
+ * 0 <= scale <= 2^127.
  *   workspace   device memory, 16-byte aligned, or NULL: with few rows the
  *               keys of a row are split over the idle SMs and the parts'
  *               outputs joined by a second kernel; the parts (f32) go here.
