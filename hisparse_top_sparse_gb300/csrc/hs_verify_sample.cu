@@ -11,9 +11,12 @@
 //   refusal and w = p_d past the last draft. With E_v exponentially
 //   distributed, that is v with probability w(v) / sum w: a race whose winner
 //   needs one pass and no running sum over the vocabulary, so that the order
-//   of additions cannot move the answer. (The ratio is taken with an
-//   approximate reciprocal, off by 2^-23 like p itself: two tokens that near
-//   each other may change places.)
+//   of additions cannot move the answer. (p is off by about (|l - M| / T + 8)
+//   2^-22 of itself: the exponent's argument is rounded four times in f32, the
+//   exponential and the sum add the rest, the ratio's approximate reciprocal
+//   2^-23. After a refusal w = p - q is off by as much as p, which is more of
+//   itself where p and q are near each other. Two tokens closer than that may
+//   change places.)
 //
 // One cluster of 1 to 16 blocks per request takes the request's rows in order,
 // one or a few at a time, and stops at the first refusal: the logits behind it,
@@ -21,8 +24,9 @@
 // bounds it: each logits row is streamed once for (M, S), and the row that
 // yields the token a second time, beside q and E, mostly from L2. M and S
 // come in one pass (a thread rescales its sum when a batch of its values
-// brings a new maximum). The sums are f32, each of a thread's few hundred
-// terms, then joined as a tree in a fixed order: results do not depend on
+// brings a new maximum). The sums are f32, each of a thread's V / 256 terms (505
+// at V = 129280) or, with more blocks, fewer, in batches of 16 or 32 that are
+// summed first, then joined as a tree in a fixed order: results do not depend on
 // scheduling. A thread copies its values ahead into places of its own in
 // shared memory (cp.async), so no barrier stands between loading and using.
 //

@@ -655,9 +655,12 @@ int hs_verify_accept_noalloc(const void *logits, int32_t logits_dtype, int32_t B
  *     m < d (p_m itself if that is 0 everywhere) and w = p_d when m = d.
  * With uniforms uniform in [0, 1) and noise exponentially distributed (mean
  * 1), all independent of the drafts, the tokens are distributed as if sampled
- * from p one by one. p, w and the quotients are f32 (quotients within a few
- * 2^-23 of each other may change places). draft_probs NULL: the drafts were chosen outright, q_i is
- * 1 at the draft and 0 elsewhere.
+ * from p one by one. p, w and the quotients are f32. p_i(v) is off by about
+ * (|l - max l| / T + 8) * 2^-22 of itself (2^-17 at the weights that matter),
+ * w = p - q by as much as p is, so by p / w times that of itself: comparisons
+ * closer than this may come out either way, the same way each time.
+ * draft_probs NULL: the drafts were chosen outright, q_i is 1 at the draft and
+ * 0 elsewhere.
  * T <= 0 (or NaN) verifies the entry greedily, as hs_verify_finalize does; its
  * numbers are not used.
  * Logits of -inf (or NaN) are masked tokens: never accepted, never drawn.
