@@ -43,6 +43,10 @@
 //     the row, and the pair then runs the row again with the exact maximum
 //     (exchanged at the end of the first pass) as the reference. The row sum
 //     l is the sum of both CTAs' partial sums.
+// P is rounded to bf16, the type of the values beside it (an MMA's operands are of
+// one type); sums and statistics take it in f32. That makes the output's error
+// against 64 bits 0.0019 to 0.0022 of its size, where f32 numerators leave the
+// 0.0017 of the output's own rounding.
 // Warp roles (480 threads): warps 0-3 softmax, P exchange and epilogue (thread
 // = head = TMEM lane), warps 4-11 gather producers (eight threads per key, one
 // 16-byte chunk of each 64-dim block per thread), warps 12-13 issue Q K^T for

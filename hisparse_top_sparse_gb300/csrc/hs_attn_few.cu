@@ -13,8 +13,8 @@
 //     decoded goes through shared memory;
 //   * the eight partial S (16 heads x 32 keys), and two of the rope dims, meet
 //     in shared memory; warp w adds those of heads 2 w and 2 w + 1, takes their
-//     maximum and sum (f32; 16 lanes a head) and writes P (bf16, as in
-//     k_attn_pair). A head's reference moves only when a score passes it by more
+//     maximum and sum (f32; 16 lanes a head) and writes P (bf16, the values'
+//     type, as in k_attn_pair: mma.sync takes one type). A head's reference moves only when a score passes it by more
 //     than 30 (of the exponent of two), so P stays below 2^30;
 //   * each warp scales its 64 dims of O (f32 registers) when a reference moved
 //     and adds P V.
