@@ -34,6 +34,14 @@ LATENT_DIM = 576
 VALUE_DIM = 512
 Q8_ROW_BYTES = 656                      # a quantised latent row (hs_quant_rows)
 ATTN_Q8_WORKSPACE_BYTES = 32 << 20      # enough for every hs_sparse_attn_decode_q8 call
+Q4_ROW_BYTES = 416                      # a latent row in 4 bits (hs_quant_rows_q4)
+ATTN_Q4_WORKSPACE_BYTES = 32 << 20      # enough for every hs_sparse_attn_decode_q4 call
+HS_ROPE_INTERLEAVED = 0                 # pairs of neighbouring dims
+HS_ROPE_HALF = 1                        # pairs i, i + rot_dim / 2
+HS_ROPE_PLAIN = 0                       # how hs_rope_freqs scales its frequencies
+HS_ROPE_LINEAR = 1
+HS_ROPE_NTK = 2
+HS_ROPE_YARN = 3
 
 EXPORTS = (
     "hs_buffer_create", "hs_buffer_destroy", "hs_request_reset", "hs_get_status",
@@ -43,7 +51,8 @@ EXPORTS = (
     "hs_sparse_attn_decode_mixed", "hs_backup_rows", "hs_backup_indexer",
     "hs_buffer_set_copy_sms", "hs_swap_in_attn_decode", "hs_step_groups",
     "hs_step_overlap_fits", "hs_quant_rows", "hs_dequant_rows", "hs_sparse_attn_decode_q8",
-    "hs_verify_sample", "hs_verify_sample_finalize",
+    "hs_verify_sample", "hs_verify_sample_finalize", "hs_quant_rows_q4", "hs_dequant_rows_q4",
+    "hs_sparse_attn_decode_q4", "hs_rope_rows", "hs_rope_freqs",
 )
 
 
@@ -67,6 +76,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _I64 = ctypes.c_int64
+_D = ctypes.c_double
 
 
 def lib() -> ctypes.CDLL:
@@ -110,6 +120,13 @@ def lib() -> ctypes.CDLL:
             "hs_dequant_rows": (_I, [_P, _I64, _P, _I, _I64, _I64, _P, _P, _I, _P, _P]),
             "hs_sparse_attn_decode_q8": (_I, [_P, _P, _I64, _P, _I, _I, _I, ctypes.c_float, _P, _P,
                                               _P, ctypes.c_size_t, _P, _P]),
+            "hs_quant_rows_q4": (_I, [_P, _I, _I64, _I64, _P, _I64, _P, _P, _I, _P, _P]),
+            "hs_dequant_rows_q4": (_I, [_P, _I64, _P, _I, _I64, _I64, _P, _P, _I, _P, _P]),
+            "hs_sparse_attn_decode_q4": (_I, [_P, _P, _I64, _P, _I, _I, _I, ctypes.c_float, _P, _P,
+                                              _P, ctypes.c_size_t, _P, _P]),
+            "hs_rope_rows": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I, _P, _P, _P, _I, _I,
+                                  _I, _I, _I, _I, _P, ctypes.c_float, _I, _P, _P]),
+            "hs_rope_freqs": (_I, [_I, _D, _I, _D, _D, _D, _D, _P, _P]),
             "hs_verify_sample": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
             "hs_verify_sample_finalize": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P,
                                                _P, _P, _P, _P, _P]),
@@ -563,15 +580,15 @@ def _elsewhere(t, name, cur) -> None:
         raise ValueError(f"{name} must be a CUDA tensor or pinned host memory")
 
 
-def _q8_cache(t, name, cur):
-    """(pointer, rows) of a q8 cache."""
+def _quantised(t, name, row_bytes, cur):
+    """(pointer, rows) of a cache of q8 or q4 rows."""
     if not isinstance(t, torch.Tensor) or t.get_device() != cur:
         _elsewhere(t, name, cur)
     if t.dtype is torch.uint8 and t.is_contiguous():
         s = t.shape
-        if len(s) == 2 and s[1] == Q8_ROW_BYTES:
+        if len(s) == 2 and s[1] == row_bytes:
             return t.data_ptr(), s[0]
-    raise ValueError(f"{name} must be a contiguous uint8 [rows][{Q8_ROW_BYTES}] tensor")
+    raise ValueError(f"{name} must be a contiguous uint8 [rows][{row_bytes}] tensor")
 
 
 _WIDE = {torch.float32: HS_LOGITS_F32, torch.bfloat16: HS_LOGITS_BF16}
@@ -620,48 +637,37 @@ def _entries(src_slots, dst_slots, src_rows, dst_rows, cur):
     return sp, dp, n
 
 
-def hs_quant_rows(src, cache, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
-    """Row dst_slots[i] of the q8 cache (uint8 [rows][656]) = row src_slots[i]
-    of src (bf16 / f32 [rows][576]), quantised; without a list entry i is row
-    i, negative slots are skipped."""
+def _quant(f, what, row_bytes, src, cache, src_slots, dst_slots, status, stream) -> None:
     cur = _device()
     sp, dt, stride, src_rows = _wide_rows(src, "src", cur)
-    dp, rows = _q8_cache(cache, "cache", cur)
+    dp, rows = _quantised(cache, "cache", row_bytes, cur)
     ss, ds, n = _entries(src_slots, dst_slots, src_rows, rows, cur)
-    _check(lib().hs_quant_rows(
-        sp, dt, stride, src_rows, dp, rows, ss, ds, n,
-        None if status is None else _on(status, "status", torch.int32, (1,), cur),
-        _on_stream(stream, cur)), "hs_quant_rows")
+    _check(f(sp, dt, stride, src_rows, dp, rows, ss, ds, n,
+             None if status is None else _on(status, "status", torch.int32, (1,), cur),
+             _on_stream(stream, cur)), what)
 
 
-def hs_dequant_rows(cache, dst, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
-    """Row dst_slots[i] of dst (bf16 / f32 [rows][576]) = the values of row
-    src_slots[i] of the q8 cache."""
+def _dequant(f, what, row_bytes, cache, dst, src_slots, dst_slots, status, stream) -> None:
     cur = _device()
-    sp, rows = _q8_cache(cache, "cache", cur)
+    sp, rows = _quantised(cache, "cache", row_bytes, cur)
     dp, dt, stride, dst_rows = _wide_rows(dst, "dst", cur)
     ss, ds, n = _entries(src_slots, dst_slots, rows, dst_rows, cur)
-    _check(lib().hs_dequant_rows(
-        sp, rows, dp, dt, stride, dst_rows, ss, ds, n,
-        None if status is None else _on(status, "status", torch.int32, (1,), cur),
-        _on_stream(stream, cur)), "hs_dequant_rows")
+    _check(f(sp, rows, dp, dt, stride, dst_rows, ss, ds, n,
+             None if status is None else _on(status, "status", torch.int32, (1,), cur),
+             _on_stream(stream, cur)), what)
 
 
-def hs_sparse_attn_decode_q8(q, kv, idx, scale: float, out, lse=None, workspace=None, status=None,
-                             stream=None) -> None:
-    """hs_sparse_attn_decode over a q8 cache (uint8 [rows][656]). workspace:
-    uint8 CUDA tensor (ATTN_Q8_WORKSPACE_BYTES is enough for every call) with
-    which few rows run split over the SMs; one per call in flight."""
+def _attend(f, what, row_bytes, q, kv, idx, scale, out, lse, workspace, status, stream) -> None:
     R, H, D = q.shape
     if D != LATENT_DIM:
         raise ValueError("q must be [R][H][576]")
-    if kv.dim() != 2 or kv.shape[1] != Q8_ROW_BYTES:
-        raise ValueError(f"kv must be [rows][{Q8_ROW_BYTES}]")
+    if kv.dim() != 2 or kv.shape[1] != row_bytes:
+        raise ValueError(f"kv must be [rows][{row_bytes}]")
     if idx.dim() != 2:
         raise ValueError("idx must be [R][K]")
     K = idx.shape[1]
     cur = _device()
-    _check(lib().hs_sparse_attn_decode_q8(
+    _check(f(
         _on(q, "q", torch.bfloat16, None, cur), _on(kv, "kv", torch.uint8, None, cur), kv.shape[0],
         _on(idx, "idx", torch.int32, (R, K), cur), R, H, K, float(scale),
         _on(out, "out", torch.bfloat16, (R, H, VALUE_DIM), cur),
@@ -669,7 +675,121 @@ def hs_sparse_attn_decode_q8(q, kv, idx, scale: float, out, lse=None, workspace=
         None if workspace is None else _on(workspace, "workspace", torch.uint8, None, cur),
         0 if workspace is None else workspace.numel(),
         None if status is None else _on(status, "status", torch.int32, (1,), cur),
-        _on_stream(stream, cur)), "hs_sparse_attn_decode_q8")
+        _on_stream(stream, cur)), what)
+
+
+def hs_quant_rows(src, cache, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
+    """Row dst_slots[i] of the q8 cache (uint8 [rows][656]) = row src_slots[i]
+    of src (bf16 / f32 [rows][576]), quantised; without a list entry i is row
+    i, negative slots are skipped."""
+    _quant(lib().hs_quant_rows, "hs_quant_rows", Q8_ROW_BYTES, src, cache, src_slots, dst_slots,
+           status, stream)
+
+
+def hs_dequant_rows(cache, dst, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
+    """Row dst_slots[i] of dst (bf16 / f32 [rows][576]) = the values of row
+    src_slots[i] of the q8 cache."""
+    _dequant(lib().hs_dequant_rows, "hs_dequant_rows", Q8_ROW_BYTES, cache, dst, src_slots,
+             dst_slots, status, stream)
+
+
+def hs_sparse_attn_decode_q8(q, kv, idx, scale: float, out, lse=None, workspace=None, status=None,
+                             stream=None) -> None:
+    """hs_sparse_attn_decode over a q8 cache (uint8 [rows][656]). workspace:
+    uint8 CUDA tensor (ATTN_Q8_WORKSPACE_BYTES is enough for every call) with
+    which few rows run split over the SMs; one per call in flight."""
+    _attend(lib().hs_sparse_attn_decode_q8, "hs_sparse_attn_decode_q8", Q8_ROW_BYTES, q, kv, idx,
+            scale, out, lse, workspace, status, stream)
+
+
+# -------------------------------------------------- latent rows in 4 bits --
+
+def hs_quant_rows_q4(src, cache, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
+    """hs_quant_rows into a q4 cache (uint8 [rows][416])."""
+    _quant(lib().hs_quant_rows_q4, "hs_quant_rows_q4", Q4_ROW_BYTES, src, cache, src_slots,
+           dst_slots, status, stream)
+
+
+def hs_dequant_rows_q4(cache, dst, src_slots=None, dst_slots=None, status=None,
+                       stream=None) -> None:
+    """hs_dequant_rows from a q4 cache (uint8 [rows][416])."""
+    _dequant(lib().hs_dequant_rows_q4, "hs_dequant_rows_q4", Q4_ROW_BYTES, cache, dst, src_slots,
+             dst_slots, status, stream)
+
+
+def hs_sparse_attn_decode_q4(q, kv, idx, scale: float, out, lse=None, workspace=None, status=None,
+                             stream=None) -> None:
+    """hs_sparse_attn_decode_q8 over a q4 cache (uint8 [rows][416])."""
+    _attend(lib().hs_sparse_attn_decode_q4, "hs_sparse_attn_decode_q4", Q4_ROW_BYTES, q, kv, idx,
+            scale, out, lse, workspace, status, stream)
+
+
+# ------------------------------------------------------- rotary positions --
+
+def _heads(t, name, cur):
+    """(pointer, rows, row stride, heads, head stride, dims) of bf16 / f32 rows
+    [rows][heads][dims] or [rows][dims], dims contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != cur:
+        _elsewhere(t, name, cur)
+    if t.dtype not in _WIDE:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    s, st = t.shape, t.stride()
+    if len(s) not in (2, 3) or (s[-1] > 1 and st[-1] != 1):
+        raise ValueError(f"{name} must be [rows][heads][dims] or [rows][dims], dims contiguous")
+    if len(s) == 2:
+        return t.data_ptr(), s[0], st[0], 1, 0, s[1]
+    return t.data_ptr(), s[0], st[0], s[1], st[1], s[2]
+
+
+def hs_rope_rows(src, dst, positions, freqs, factor: float = 1.0, rot_off: int = 0,
+                 layout: int = HS_ROPE_INTERLEAVED, inverse: bool = False, src_slots=None,
+                 dst_slots=None, status=None, stream=None) -> None:
+    """Row dst_slots[i] of dst = row src_slots[i] of src (bf16 / f32
+    [rows][heads][dims] or [rows][dims], any strides) with the 2 * len(freqs)
+    dims from rot_off on rotated by positions[i]; freqs and factor as
+    hs_rope_freqs gives them. dst may be src. Without a list entry i is row i,
+    negative slots are skipped. See include/hisparse.h."""
+    cur = _device()
+    sp, src_rows, src_row, heads, src_head, dims = _heads(src, "src", cur)
+    dp, dst_rows, dst_row, dst_heads, dst_head, dst_dims = _heads(dst, "dst", cur)
+    if dst.dtype is not src.dtype or dst_heads != heads or dst_dims != dims:
+        raise ValueError("src and dst must have one dtype, as many heads and as many dims")
+    pp, n = _slot_list(positions, "positions", cur)
+    if src_slots is None and dst_slots is None and n != src_rows:
+        raise ValueError(f"{n} positions for {src_rows} rows")
+    ss = ds = None
+    for name, t, rows in (("src_slots", src_slots, src_rows), ("dst_slots", dst_slots, dst_rows)):
+        if t is None:
+            if n > rows:
+                raise ValueError(f"{n} entries do not fit {rows} rows")
+            continue
+        p, m = _slot_list(t, name, cur)
+        if m != n:
+            raise ValueError(f"{name} must have an entry for each of the {n} positions")
+        if name == "src_slots":
+            ss = p
+        else:
+            ds = p
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be int64 [pairs]")
+    _check(lib().hs_rope_rows(
+        sp, src_row, src_head, src_rows, dp, dst_row, dst_head, dst_rows, _WIDE[src.dtype], ss, ds,
+        pp, n, heads, dims, int(rot_off), 2 * freqs.shape[0], int(layout),
+        _on(freqs, "freqs", torch.int64, None, cur), float(factor), int(bool(inverse)),
+        None if status is None else _on(status, "status", torch.int32, (1,), cur),
+        _on_stream(stream, cur)), "hs_rope_rows")
+
+
+def hs_rope_freqs(rot_dim: int, base: float = 10000.0, scaling: int = HS_ROPE_PLAIN,
+                  scale: float = 1.0, context: float = 0.0, fast: float = 32.0, slow: float = 1.0):
+    """(freqs int64 [rot_dim / 2] on the CPU, factor): the frequencies of
+    rot_dim dims for hs_rope_rows, scaled for contexts past `context`."""
+    freqs = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.int64)
+    factor = ctypes.c_float(0.0)
+    _check(lib().hs_rope_freqs(int(rot_dim), float(base), int(scaling), float(scale),
+                               float(context), float(fast), float(slow),
+                               freqs.data_ptr() or None, ctypes.byref(factor)), "hs_rope_freqs")
+    return freqs, factor.value
 
 
 # --------------------------------------------- verification by sampling --

@@ -84,6 +84,7 @@
 
 #include <atomic>
 
+#include "hs_q4.cuh"
 #include "hs_q8.cuh"
 
 namespace {
@@ -110,14 +111,14 @@ constexpr int THREADS = 480;
 // attention. 4 x 96 x 32 + 2 x 56 x 32 = 15,872; at 98 (rounded to 104) it
 // no longer fits and the copies wait for whole SMs.
 #define ATTN_MAX_REGS 96
-// The q8 kernel's 19 warps: five of them share a quarter of the register file
+// The 19 warps of the kernels for quantised rows: five of them share a quarter of the register file
 // (5 x 96 x 32 = 15,360 of 16,384; 104 would not fit).
-#define Q8_MAX_REGS 96
+#define RAW_MAX_REGS 96
 static_assert(THREADS * ATTN_MAX_REGS <= 65536, "register budget");
 constexpr int NPROD = 256;
-constexpr int Q8_HALF = 128;                                // threads decoding peer tiles' halves
-constexpr int Q8_THREADS = THREADS + Q8_HALF;
-static_assert((Q8_THREADS / 32 + 3) / 4 * 32 * Q8_MAX_REGS <= 16384, "register budget");
+constexpr int RAW_HALF = 128;                               // threads decoding peer tiles' halves
+constexpr int RAW_THREADS = THREADS + RAW_HALF;
+static_assert((RAW_THREADS / 32 + 3) / 4 * 32 * RAW_MAX_REGS <= 16384, "register budget");
 constexpr float REF_SLACK = 30.0f;        // P <= 2^30 on the shared reference
 
 // shared memory (offsets from a 1024-byte aligned base)
@@ -126,23 +127,26 @@ constexpr int QS_OFF = 0;
 constexpr int QS_BYTES = QS_BLOCKS * HG * 128;              // 49152
 constexpr int RA_SLOT_BYTES = (D / 64 - VB_BLOCKS) * KV_BLOCK_BYTES;   // 20480
 constexpr int V_SLOT_BYTES = VB_BLOCKS * KV_BLOCK_BYTES;              // 16384
-constexpr int RAWO_BYTES = NK * HS_Q8_ROW_BYTES;            // 20992: a q8 tile's rows
-constexpr int RAWH_BYTES = NK * (DV / 2 + 16);              // 8704: half the codes, the exponents
 constexpr int P_SLOT_BYTES = HG * NK * 2;                   // 8192: 128 rows x 64 B, 64-byte swizzle
 constexpr int RA_OFF = QS_OFF + QS_BYTES;
 // Ring slots, and where everything lies. The q8 kernel's rows land in raw
 // rings first (its slots are taken only once a row is decoded, about a
 // microsecond later), which its rings A and VO make room for.
-template <bool Q8>
+// (q4 rows are smaller again, and a fourth VO slot fits.)
+template <int F>
 struct Lay {
-  static constexpr int RA_SLOTS = Q8 ? 2 : 3, VO_SLOTS = Q8 ? 3 : 4, VP_SLOTS = 2;
+  static constexpr bool RAW = F != HS_ROWS_BF16;
+  static constexpr int RA_SLOTS = RAW ? 2 : 3, VO_SLOTS = F == HS_ROWS_Q8 ? 3 : 4, VP_SLOTS = 2;
+  static constexpr int RAWO_BYTES = F == HS_ROWS_Q8 ? NK * HS_Q8_ROW_BYTES : NK * HS_Q4_ROW_BYTES;   // 20992, 13312: a tile's rows
+  static constexpr int RAWH_BYTES =                                    // 8704, 4608: half the codes, the scales
+      F == HS_ROWS_Q8 ? NK * (DV / 2 + DV / Q8_GROUP) : NK * (DV / 4 + DV / Q4_GROUP / 2);
   static constexpr int VO_OFF = RA_OFF + RA_SLOTS * RA_SLOT_BYTES;
   static constexpr int XS_OFF = VO_OFF + VO_SLOTS * V_SLOT_BYTES;    // own P staged for the bulk copy
   static constexpr int XP_OFF = XS_OFF + XP_SLOTS * P_SLOT_BYTES;    // the peer's P
   static constexpr int VP_OFF = XP_OFF + XP_SLOTS * P_SLOT_BYTES;
   static constexpr int RAWO_OFF = VP_OFF + VP_SLOTS * V_SLOT_BYTES;  // raw rows of own tiles
-  static constexpr int RAWH_OFF = RAWO_OFF + (Q8 ? RAWO_SLOTS * RAWO_BYTES : 0);   // raw halves
-  static constexpr int XMAX_OFF = RAWH_OFF + (Q8 ? RAWH_SLOTS * RAWH_BYTES : 0);   // peer's first-tile maxima
+  static constexpr int RAWH_OFF = RAWO_OFF + (RAW ? RAWO_SLOTS * RAWO_BYTES : 0);   // raw halves
+  static constexpr int XMAX_OFF = RAWH_OFF + (RAW ? RAWH_SLOTS * RAWH_BYTES : 0);   // peer's first-tile maxima
   static constexpr int XEND_OFF = XMAX_OFF + HG * 4;                 // peer's (l or mark, max) per pass
   static constexpr int BAR_OFF = XEND_OFF + 2 * HG * 8;
   static constexpr int SMEM_USED = BAR_OFF + 512;
@@ -157,9 +161,9 @@ struct Lay {
                     XMAX_OFF % 16 == 0, "slot alignment");
   // Staging place of Q block a (dims 64a..64a+63, a < 6) before it moves into
   // TMEM, outside the slots of the first tiles, which are gathered meanwhile:
-  // ring A behind slot 0 (bf16: two blocks in its two slots, q8: one), ring VO
-  // behind slot 0, the P buffers (the sixth block of bf16), and for q8 ring VP
-  // behind slot 0 and the raw ring of own tiles.
+  // ring A behind slot 0 (bf16: two blocks in its two slots, else one), ring VO
+  // behind slot 0, the P buffers (the sixth block of bf16), and for quantised rows
+  // ring VP behind slot 0 and (q8) the raw ring of own tiles.
   __host__ __device__ static constexpr uint32_t q_stage_off(int a) {
     constexpr int BLK = HG * 128, in_a = (RA_SLOTS - 1) * RA_SLOT_BYTES / BLK;
     if (a < in_a) return RA_OFF + RA_SLOT_BYTES + a * BLK;
@@ -188,7 +192,7 @@ enum {
   B_FULLA = 0,                        // own tile landed (NPROD arrivals)
   B_EMPTYA = B_FULLA + MAX_RA,      // ring A slot: Q K^T done
   B_EMPTYVO = B_EMPTYA + MAX_RA,    // ring VO slot: own P V done
-  B_FULLVP = B_EMPTYVO + MAX_VO,    // peer tile's value half landed (NPROD, or Q8_HALF, arrivals)
+  B_FULLVP = B_EMPTYVO + MAX_VO,    // peer tile's value half landed (NPROD, or RAW_HALF, arrivals)
   B_EMPTYVP = B_FULLVP + MAX_VP,    // ring VP slot: P V done
   B_SFULL = B_EMPTYVP + MAX_VP,     // S ready
   B_SFREE = B_SFULL + NSB,            // own P V done with the S / P buffer
@@ -209,8 +213,9 @@ static_assert(B_COUNT * 8 + 16 <= 512, "barrier area");
 // a warp in bf16, four in f32) over Q and rings A and VO (free once the last
 // P V is done)
 constexpr int O_STG_OFF = QS_OFF, O_BLOCK = 32 * 128;
-static_assert(O_STG_OFF % 1024 == 0 && O_STG_OFF + 8 * 4 * O_BLOCK <= Lay<true>::XS_OFF &&
-                  O_STG_OFF + 8 * 2 * O_BLOCK <= Lay<false>::XS_OFF, "O staging");
+static_assert(O_STG_OFF % 1024 == 0 && O_STG_OFF + 8 * 4 * O_BLOCK <= Lay<HS_ROWS_Q8>::XS_OFF &&
+                  O_STG_OFF + 8 * 4 * O_BLOCK <= Lay<HS_ROWS_Q4>::XS_OFF &&
+                  O_STG_OFF + 8 * 2 * O_BLOCK <= Lay<HS_ROWS_BF16>::XS_OFF, "O staging");
 
 constexpr int WAIT_LIMIT = 1 << 24;
 
@@ -348,6 +353,11 @@ __device__ __forceinline__ uint4 ld_global16(const void *p) {
                : "l"(p));
   return v;
 }
+__device__ __forceinline__ uint32_t ld_global_u16(const void *p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];\n" : "=h"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
                "r"(valid ? 16 : 0)
@@ -364,6 +374,11 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(src)
                : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t src) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(src) : "memory");
   return v;
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
@@ -508,7 +523,184 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity)
   return __all_sync(0xffffffffu, bar_wait_cluster(bar, parity));
 }
 
-// What a cluster of the q8 kernel does of its row: keys [s * keys, (s + 1) * keys)
+// ---- how a tile's quantised rows come in -------------------------------------
+// OwnRow<F>: the chunks of one key of an own tile that one of its eight threads
+// copies and decodes; HalfRow<F>: those of a value half of a peer tile's key, for
+// one of its four threads. key(), sub(): which of a warp's keys and threads a
+// lane is. copy() takes a row's chunks by cp.async to the thread's places of a raw
+// slot (p: the thread's number), fetch() reads them from there, load() straight
+// from memory, put() decodes them into the slots' swizzled 64-dim blocks.
+__host__ __device__ constexpr int row_bytes(int f) { return f == HS_ROWS_Q8 ? HS_Q8_ROW_BYTES : HS_Q4_ROW_BYTES; }
+
+template <int F>
+struct OwnRow {};
+template <int F>
+struct HalfRow {};
+
+// 16 codes into two chunks of a swizzled 64-dim block
+__device__ __forceinline__ void put_q8(uint32_t to, const uint4 w, uint32_t byte) {
+  const uint64_t s = q8_scale2(byte & 0xFFu);
+  const uint2 a = q8_decode4_bf16(w.x, s), b = q8_decode4_bf16(w.y, s);
+  st_shared16(to, make_uint4(a.x, a.y, b.x, b.y));
+  const uint2 d = q8_decode4_bf16(w.z, s), e = q8_decode4_bf16(w.w, s);
+  st_shared16(to ^ 16, make_uint4(d.x, d.y, e.x, e.y));      // the chunk beside it
+}
+
+// q8, own: chunks sub + 8 k: codes (block 2 k + sub / 4, exponent word k), rope.
+// Eight neighbouring threads take four chunks of two neighbouring keys: under the
+// 128-byte swizzle their stores fall into different banks.
+template <>
+struct OwnRow<HS_ROWS_Q8> {
+  uint4 code[4], rope, scale;
+  static __device__ __forceinline__ int key(int lw, int lane) { return 4 * lw + 2 * (lane >> 4) + ((lane >> 2) & 1); }
+  static __device__ __forceinline__ int sub(int lane) { return (lane & 3) + 4 * ((lane >> 3) & 1); }
+  static __device__ __forceinline__ void copy(uint32_t to, const char *row, bool v, int p, int key, int sub) {
+    row += sub * 16;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) cp_async16(to + p * 16 + k * (NPROD * 16), row + k * 128, v);
+    if (sub == 0) cp_async16(to + 5 * NPROD * 16 + key * 16, row + Q8_SCALE_OFF, v);
+  }
+  __device__ __forceinline__ void load(const char *from, bool v, int sub) {
+    const uint4 *row = reinterpret_cast<const uint4 *>(from);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) code[k] = v ? ld_global16(row + sub + 8 * k) : zero;
+    rope = v ? ld_global16(row + Q8_ROPE_OFF / 16 + sub) : zero;
+    scale = v ? ld_global16(row + Q8_SCALE_OFF / 16) : zero;
+  }
+  __device__ __forceinline__ void fetch(uint32_t from, int p, int key, int sub) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) code[k] = ld_shared16(from + (k * NPROD + p) * 16);
+    rope = ld_shared16(from + (4 * NPROD + p) * 16);
+    scale = ld_shared16(from + 5 * NPROD * 16 + key * 16);
+  }
+  // chunk sub + 8 k goes to block 2 k + sub / 4, of the CTA's value half (ring VO)
+  // for two of the k, of the other half (ring A) for two
+  __device__ __forceinline__ void put(uint32_t ra, uint32_t rv, int c, int key, int sub) {
+    const int sh = 8 * (sub >> 1);     // this thread's byte of a word of exponents
+    const uint32_t at0 = (uint32_t)(sub >> 2) * KV_BLOCK_BYTES + sw128(key, 2 * (sub & 3));
+    const uint32_t lo = (c ? ra : rv) + at0, hi = (c ? rv : ra) + at0;   // dims below / from 256
+    put_q8(lo, code[0], scale.x >> sh);
+    put_q8(lo + 2 * KV_BLOCK_BYTES, code[1], scale.y >> sh);
+    put_q8(hi, code[2], scale.z >> sh);
+    put_q8(hi + 2 * KV_BLOCK_BYTES, code[3], scale.w >> sh);
+    st_shared16(ra + 4 * KV_BLOCK_BYTES + sw128(key, sub), rope);
+  }
+};
+
+// q8, a half: chunks sub + 4 k of its 16: block k of the slot, exponent word
+// 2 c + k / 2, byte 2 (k & 1) + sub / 2
+template <>
+struct HalfRow<HS_ROWS_Q8> {
+  uint4 code[4], scale;
+  static __device__ __forceinline__ int key(int lw, int lane) { return 8 * lw + (lane >> 2); }
+  static __device__ __forceinline__ int sub(int lane) { return lane & 3; }
+  static __device__ __forceinline__ void copy(uint32_t to, const char *row, bool v, int c, int p, int key, int sub) {
+    row += sub * 16;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      cp_async16(to + p * 16 + k * (RAW_HALF * 16), row + (DV / 2) * c + k * 64, v);
+    if (sub == 0) cp_async16(to + 4 * RAW_HALF * 16 + key * 16, row + Q8_SCALE_OFF, v);
+  }
+  __device__ __forceinline__ void fetch(uint32_t from, int p, int key, int sub) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) code[k] = ld_shared16(from + (k * RAW_HALF + p) * 16);
+    scale = ld_shared16(from + 4 * RAW_HALF * 16 + key * 16);
+  }
+  __device__ __forceinline__ void put(uint32_t slot, int c, int key, int sub) {
+    const int sh = 8 * (sub >> 1);
+    const uint32_t to = slot + sw128(key, 2 * sub);
+    const uint32_t lo = c ? scale.z : scale.x, hi = c ? scale.w : scale.y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      put_q8(to + k * KV_BLOCK_BYTES, code[k], (k < 2 ? lo : hi) >> (16 * (k & 1) + sh));
+  }
+};
+
+// A q4 chunk holds 32 dims and two scales. Its values, 2^-15 of theirs (hs_q4.cuh),
+// go to four neighbouring chunks of a key's 128 bytes in block `block` at `at`:
+// chunks 4 odd .. 4 odd + 3, swizzled.
+__device__ __forceinline__ void put_q4(uint32_t block, int key, int odd, const uint4 w, uint32_t bytes) {
+  const uint32_t s0 = q4_scale2(bytes & 0xFFu), s1 = q4_scale2(bytes >> 8 & 0xFFu);
+  const uint32_t to = block + sw128(key, 4 * odd);
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t s = k < 2 ? s0 : s1;
+    st_shared16(to ^ (16 * k), make_uint4(q4_decode2<0>(ws[k], s), q4_decode2<1>(ws[k], s),
+                                          q4_decode2<2>(ws[k], s), q4_decode2<3>(ws[k], s)));
+  }
+}
+
+// q4, own: chunks sub and sub + 8 of the codes (block sub / 2 of either value half,
+// half sub & 1 of its dims), and one of the rope's eight. Eight neighbouring
+// threads store four keys' chunks 4 (sub & 1) + k, or rope chunks 4 (sub & 1) +
+// sub / 2: different banks under the swizzle.
+template <>
+struct OwnRow<HS_ROWS_Q4> {
+  uint4 code[2], rope;
+  uint32_t scale[2];
+  static __device__ __forceinline__ int key(int lw, int lane) { return 4 * lw + (lane & 3); }
+  static __device__ __forceinline__ int sub(int lane) { return lane >> 2; }
+  static __device__ __forceinline__ int rope_chunk(int sub) { return 4 * (sub & 1) + (sub >> 1); }
+  static __device__ __forceinline__ void copy(uint32_t to, const char *row, bool v, int p, int key, int sub) {
+    cp_async16(to + p * 16, row + sub * 16, v);
+    cp_async16(to + (NPROD + p) * 16, row + 128 + sub * 16, v);
+    cp_async16(to + (2 * NPROD + p) * 16, row + Q4_ROPE_OFF + rope_chunk(sub) * 16, v);
+    if (sub < 2) cp_async16(to + 3 * NPROD * 16 + key * 32 + sub * 16, row + Q4_SCALE_OFF + sub * 16, v);
+  }
+  __device__ __forceinline__ void load(const char *row, bool v, int sub) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    code[0] = v ? ld_global16(row + sub * 16) : zero;
+    code[1] = v ? ld_global16(row + 128 + sub * 16) : zero;
+    rope = v ? ld_global16(row + Q4_ROPE_OFF + rope_chunk(sub) * 16) : zero;
+    scale[0] = v ? ld_global_u16(row + Q4_SCALE_OFF + 2 * sub) : 0u;
+    scale[1] = v ? ld_global_u16(row + Q4_SCALE_OFF + 16 + 2 * sub) : 0u;
+  }
+  __device__ __forceinline__ void fetch(uint32_t from, int p, int key, int sub) {
+    code[0] = ld_shared16(from + p * 16);
+    code[1] = ld_shared16(from + (NPROD + p) * 16);
+    rope = ld_shared16(from + (2 * NPROD + p) * 16);
+    scale[0] = ld_shared_u16(from + 3 * NPROD * 16 + key * 32 + 2 * sub);
+    scale[1] = ld_shared_u16(from + 3 * NPROD * 16 + key * 32 + 16 + 2 * sub);
+  }
+  __device__ __forceinline__ void put(uint32_t ra, uint32_t rv, int c, int key, int sub) {
+    const uint32_t at = (uint32_t)(sub >> 1) * KV_BLOCK_BYTES;
+    put_q4((c ? ra : rv) + at, key, sub & 1, code[0], scale[0]);
+    put_q4((c ? rv : ra) + at, key, sub & 1, code[1], scale[1]);
+    st_shared16(ra + 4 * KV_BLOCK_BYTES + sw128(key, rope_chunk(sub)),
+                make_uint4(q4_mul(rope.x, Q4_DOWN2), q4_mul(rope.y, Q4_DOWN2), q4_mul(rope.z, Q4_DOWN2),
+                           q4_mul(rope.w, Q4_DOWN2)));
+  }
+};
+
+// q4, a half: chunks sub and sub + 4 of its eight; eight neighbouring threads store
+// the same chunk of eight keys
+template <>
+struct HalfRow<HS_ROWS_Q4> {
+  uint4 code[2];
+  uint32_t scale[2];
+  static __device__ __forceinline__ int key(int lw, int lane) { return 8 * lw + (lane & 7); }
+  static __device__ __forceinline__ int sub(int lane) { return lane >> 3; }
+  static __device__ __forceinline__ void copy(uint32_t to, const char *row, bool v, int c, int p, int key, int sub) {
+    cp_async16(to + p * 16, row + 128 * c + sub * 16, v);
+    cp_async16(to + (RAW_HALF + p) * 16, row + 128 * c + 64 + sub * 16, v);
+    if (sub == 0) cp_async16(to + 2 * RAW_HALF * 16 + key * 16, row + Q4_SCALE_OFF + 16 * c, v);
+  }
+  __device__ __forceinline__ void fetch(uint32_t from, int p, int key, int sub) {
+    code[0] = ld_shared16(from + p * 16);
+    code[1] = ld_shared16(from + (RAW_HALF + p) * 16);
+    scale[0] = ld_shared_u16(from + 2 * RAW_HALF * 16 + key * 16 + 2 * sub);
+    scale[1] = ld_shared_u16(from + 2 * RAW_HALF * 16 + key * 16 + 8 + 2 * sub);
+  }
+  __device__ __forceinline__ void put(uint32_t slot, int c, int key, int sub) {
+    const uint32_t at = slot + (uint32_t)(sub >> 1) * KV_BLOCK_BYTES;
+    put_q4(at, key, sub & 1, code[0], scale[0]);
+    put_q4(at + 2 * KV_BLOCK_BYTES, key, sub & 1, code[1], scale[1]);
+  }
+};
+
+// What a cluster of the kernels for quantised rows does of its row: keys [s * keys, (s + 1) * keys)
 // for s = cluster % n, of the row's K. n > 1: O / l in f32 and the log-sum-exp of the
 // part go to o and lse (part s of row r, head h at index (s * R + r) * H + h),
 // which k_attn_join joins.
@@ -517,8 +709,8 @@ struct Parts {
   float *o, *lse;
 };
 
-template <bool Q8>
-__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MAX_REGS)
+template <int F>
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_MAX_REGS : RAW_MAX_REGS)
     k_attn_pair(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_o,
                 const char *__restrict__ q,
                 const char *__restrict__ kv_res, int64_t n_res, const char *__restrict__ kv_hot,
@@ -527,7 +719,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
                 const int32_t *__restrict__ idx, int32_t H, int32_t K_row, float scale_log2,
                 __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, uint32_t *status,
                 const __grid_constant__ Parts parts) {
-  using L = Lay<Q8>;
+  using L = Lay<F>;
+  constexpr bool RAW = L::RAW;         // quantised rows
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -545,15 +738,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
   const int c = (int)cluster_rank();                // value half; own tiles t = c mod 2
   const uint32_t peer = (uint32_t)(c ^ 1);
   const int n_hg = (H + HG - 1) / HG;
-  const int part = Q8 ? (int)(blockIdx.x >> 1) % parts.n : 0;
-  const int rg = Q8 ? (int)(blockIdx.x >> 1) / parts.n : blockIdx.x >> 1;
-  const int K = Q8 ? min(parts.keys, K_row - part * parts.keys) : K_row;
+  const int part = RAW ? (int)(blockIdx.x >> 1) % parts.n : 0;
+  const int rg = RAW ? (int)(blockIdx.x >> 1) / parts.n : blockIdx.x >> 1;
+  const int K = RAW ? min(parts.keys, K_row - part * parts.keys) : K_row;
   const int r = rg / n_hg;
   const int h0 = (rg % n_hg) * HG;
   const int T = (K + NK - 1) / NK;
   const int n_own = T > c ? (T - c + 1) / 2 : 0;
   const int n_peer = T - n_own;
-  const int32_t *idx_row = idx + (int64_t)r * K_row + (Q8 ? part * parts.keys : 0);
+  const int32_t *idx_row = idx + (int64_t)r * K_row + (RAW ? part * parts.keys : 0);
   // Position i of the tile sequence that the gathers and the P V issuer walk:
   // every pair of tiles with this CTA's own tile first (CTA 1 swaps the
   // pairs), so that an own tile's P V never waits behind the peer's P.
@@ -567,7 +760,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
       const bool prod = i >= B_FULLA && i < B_FULLA + MAX_RA;
       const bool half = i >= B_FULLVP && i < B_FULLVP + MAX_VP;
       const bool four = (i >= B_PFULL && i < B_PFULL + NSB) || i == B_VOTE;
-      bar_init(bar(i), prod ? NPROD : half ? (Q8 ? Q8_HALF : NPROD) : four ? 4 : 1);
+      bar_init(bar(i), prod ? NPROD : half ? (RAW ? RAW_HALF : NPROD) : four ? 4 : 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (lane == 0) {
@@ -661,259 +854,210 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
   if (!req_ok && status && tid == 0 && c == 0) atomicOr(status, HS_STATUS_INDEX);
 
 
-  if (Q8 && ((warp >= 4 && warp < 12) || warp > 12 + NSB)) {
-    // ------------------------- gather producers, q8 rows made bf16 tiles ----
-    // Rows land in raw rings (cp.async), are read into registers, their places
-    // refilled at once, and decoded into a slot when it is free. (Loads
-    // straight into registers cannot run ahead: the L1 beside this kernel's
-    // shared memory holds only some 20 KB of loads in flight.) Warps 4-11 take
-    // the own tiles, eight threads per key, warps 15-18 the peer tiles' halves,
-    // four threads per key, so that neither waits behind the other's slots.
-    // A thread copies and decodes the same 16-byte chunks, in places of its
-    // own; the exponents are copied by a key's first thread and read by all,
-    // which are of one warp. Eight neighbouring threads take four chunks of
-    // two neighbouring keys: under the 128-byte swizzle their stores fall
-    // into different banks.
-    const bool own = warp < 12;
-    const int lw = own ? warp - 4 : warp - 15;
-    const int key = own ? 4 * lw + 2 * (lane >> 4) + ((lane >> 2) & 1) : 8 * lw + (lane >> 2);
-    const int sub = (lane & 3) + (own ? 4 * ((lane >> 3) & 1) : 0);
-    const int p = 32 * lw + lane;
-    auto load_id = [&](int t) -> int32_t {
-      const int j = t * NK + key;
-      return (t < T && j < K) ? ld_global(idx_row + j) : -1;
-    };
-    // 16 codes into two chunks of a swizzled 64-dim block
-    auto put = [&](uint32_t to, const uint4 w, uint32_t byte) {
-      const uint64_t s = q8_scale2(byte & 0xFFu);
-      const uint2 a = q8_decode4_bf16(w.x, s), b = q8_decode4_bf16(w.y, s);
-      st_shared16(to, make_uint4(a.x, a.y, b.x, b.y));
-      const uint2 d = q8_decode4_bf16(w.z, s), e = q8_decode4_bf16(w.w, s);
-      st_shared16(to ^ 16, make_uint4(d.x, d.y, e.x, e.y));      // the chunk beside it
-    };
-    const int sh = 8 * (sub >> 1);     // this thread's byte of a word of exponents
-    if (own) {
-      // chunks sub + 8 k: codes (block 2 k + sub / 4, exponent word k), rope
-      const uint32_t raw = sbase + L::RAWO_OFF;
-      auto copy = [&](int32_t id, int slot) {
-        // (a copy of no bytes where the index names no row: q stands for its address)
-        const bool v = id >= 0 && id < n_kv;
-        const char *row = (v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q) + sub * 16;
-        const uint32_t to = raw + slot * RAWO_BYTES;
-#pragma unroll
-        for (int k = 0; k < 5; ++k) cp_async16(to + p * 16 + k * (NPROD * 16), row + k * 128, v);
-        if (sub == 0) cp_async16(to + 5 * NPROD * 16 + key * 16, row + Q8_SCALE_OFF, v);
-        cp_async_commit();
+  if ((warp >= 4 && warp < 12) || (RAW && warp > 12 + NSB)) {
+    if constexpr (RAW) {
+      // ------------------- gather producers, quantised rows made bf16 tiles ----
+      // Rows land in raw rings (cp.async), are read into registers, their places
+      // refilled at once, and decoded into a slot when it is free. (Loads
+      // straight into registers cannot run ahead: the L1 beside this kernel's
+      // shared memory holds only some 20 KB of loads in flight.) Warps 4-11 take
+      // the own tiles, eight threads per key, warps 15-18 the peer tiles' halves,
+      // four threads per key, so that neither waits behind the other's slots.
+      // A thread copies and decodes the same 16-byte chunks, in places of its
+      // own; the scales are copied by one or two threads of a key and read by all,
+      // which are of one warp.
+      const bool own = warp < 12;
+      const int lw = own ? warp - 4 : warp - 15;
+      const int p = 32 * lw + lane;
+      const int key = own ? OwnRow<F>::key(lw, lane) : HalfRow<F>::key(lw, lane);
+      const int sub = own ? OwnRow<F>::sub(lane) : HalfRow<F>::sub(lane);
+      auto load_id = [&](int t) -> int32_t {
+        const int j = t * NK + key;
+        return (t < T && j < K) ? ld_global(idx_row + j) : -1;
       };
-      // where chunk sub + 8 k lies: block 2 k + sub / 4, of the CTA's value half
-      // (ring VO) for two of the k, of the other half (ring A) for two
-      const uint32_t at0 = (uint32_t)(sub >> 2) * KV_BLOCK_BYTES + sw128(key, 2 * (sub & 3));
-      const uint32_t rope_at = 4 * KV_BLOCK_BYTES + sw128(key, sub);
-      int ig = 0;                      // own tiles taken, over both passes
-      int sa = 0, so = 0;              // their slots; parities of the releases waited for
-      uint32_t pa = 1, po = 1;         // (flipped to 0 before the first wait)
-      for (int pass = 0; pass < 2 && !timed_out; ++pass) {
-        uint4 code[4], rope, scale;
-        int copied = 0;
-        if (pass == 0) {
-          // the first own tile comes straight into registers: the raw ring
-          // holds staged Q until it is in TMEM
-          const int32_t id = load_id(c);
+      if (own) {
+        const uint32_t raw = sbase + L::RAWO_OFF;
+        auto copy = [&](int32_t id, int slot) {
+          // (a copy of no bytes where the index names no row: q stands for its address)
           const bool v = id >= 0 && id < n_kv;
-          const uint4 *row = reinterpret_cast<const uint4 *>(v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q);
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) code[k] = v ? ld_global16(row + sub + 8 * k) : zero;
-          rope = v ? ld_global16(row + Q8_ROPE_OFF / 16 + sub) : zero;
-          scale = v ? ld_global16(row + Q8_SCALE_OFF / 16) : zero;
-          copied = 1;
-        } else {
-          if (!warp_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
-          if (!*s_redo) break;
-        }
-        int32_t id = load_id(2 * copied + c);
-        auto next = [&]() {            // past the last tile: a copy of zeros that nothing reads
-          copy(id, copied % RAWO_SLOTS);
-          ++copied;
-          id = load_id(2 * copied + c);
+          OwnRow<F>::copy(raw + slot * L::RAWO_BYTES, v ? kv + (int64_t)id * row_bytes(F) : q, v, p, key, sub);
+          cp_async_commit();
         };
-        if (pass == 1)
-          for (int k = 0; k < RAWO_SLOTS; ++k) next();
-        for (int a = 0; a < n_own; ++a, ++ig) {
-          if (pass == 1 || a > 0) {
-            if (pass == 0 && a == 1) { // the raw ring and the other slots, once Q has left them
-              if (!warp_wait(bar(B_QSTAGED), 0)) { timed_out = true; break; }
-              for (int k = 0; k < RAWO_SLOTS; ++k) next();
+        int ig = 0;                      // own tiles taken, over both passes
+        int sa = 0, so = 0;              // their slots; parities of the releases waited for
+        uint32_t pa = 1, po = 1;         // (flipped to 0 before the first wait)
+        for (int pass = 0; pass < 2 && !timed_out; ++pass) {
+          OwnRow<F> row;
+          int copied = 0;
+          if (pass == 0) {
+            // the first own tile comes straight into registers: the raw ring
+            // (of q8 rows) holds staged Q until it is in TMEM
+            const int32_t id = load_id(c);
+            const bool v = id >= 0 && id < n_kv;
+            row.load(v ? kv + (int64_t)id * row_bytes(F) : q, v, sub);
+            copied = 1;
+          } else {
+            if (!warp_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
+            if (!*s_redo) break;
+          }
+          int32_t id = load_id(2 * copied + c);
+          auto next = [&]() {            // past the last tile: a copy of zeros that nothing reads
+            copy(id, copied % RAWO_SLOTS);
+            ++copied;
+            id = load_id(2 * copied + c);
+          };
+          if (pass == 1)
+            for (int k = 0; k < RAWO_SLOTS; ++k) next();
+          for (int a = 0; a < n_own; ++a, ++ig) {
+            if (pass == 1 || a > 0) {
+              if (pass == 0 && a == 1) { // the raw ring and the other slots, once Q has left them
+                if (!warp_wait(bar(B_QSTAGED), 0)) { timed_out = true; break; }
+                for (int k = 0; k < RAWO_SLOTS; ++k) next();
+              }
+              cp_async_wait<RAWO_SLOTS - 1>();
+              __syncwarp();
+              row.fetch(raw + (a % RAWO_SLOTS) * L::RAWO_BYTES, p, key, sub);
+              __syncwarp();
+              next();
             }
-            cp_async_wait<RAWO_SLOTS - 1>();
+            if ((ig >= L::RA_SLOTS && !warp_wait(bar(B_EMPTYA + sa), pa)) ||
+                (ig >= L::VO_SLOTS && !warp_wait(bar(B_EMPTYVO + so), po))) {
+              timed_out = true;
+              break;
+            }
+            row.put(sbase + RA_OFF + sa * RA_SLOT_BYTES, sbase + L::VO_OFF + so * V_SLOT_BYTES, c, key, sub);
+            fence_proxy_async();
+            bar_arrive(bar(B_FULLA + sa));
+            // the next tile's slots, and the parity of their next release
+            if (++sa == L::RA_SLOTS) { sa = 0; pa ^= 1; }
+            if (++so == L::VO_SLOTS) { so = 0; po ^= 1; }
+          }
+          cp_async_wait<0>();
+        }
+      } else {
+        const uint32_t raw = sbase + L::RAWH_OFF;
+        auto copy = [&](int32_t id, int slot) {
+          const bool v = id >= 0 && id < n_kv;
+          HalfRow<F>::copy(raw + slot * L::RAWH_BYTES, v ? kv + (int64_t)id * row_bytes(F) : q, v, c, p, key, sub);
+          cp_async_commit();
+        };
+        int jg = 0;                      // peer tiles taken, over both passes
+        if (!warp_wait(bar(B_QSTAGED), 0)) timed_out = true;
+        for (int pass = 0; pass < 2 && !timed_out; ++pass) {
+          if (pass == 1) {
+            if (!warp_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
+            if (!*s_redo) break;
+          }
+          int copied = 0;
+          int32_t id = load_id(1 - c);
+          auto next = [&]() {
+            copy(id, copied % RAWH_SLOTS);
+            ++copied;
+            id = load_id(2 * copied + 1 - c);
+          };
+          for (int k = 0; k < RAWH_SLOTS; ++k) next();
+          for (int b = 0; b < n_peer; ++b, ++jg) {
+            cp_async_wait<RAWH_SLOTS - 1>();
             __syncwarp();
-            const uint32_t from = raw + (a % RAWO_SLOTS) * RAWO_BYTES;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) code[k] = ld_shared16(from + (k * NPROD + p) * 16);
-            rope = ld_shared16(from + (4 * NPROD + p) * 16);
-            scale = ld_shared16(from + 5 * NPROD * 16 + key * 16);
+            HalfRow<F> row;
+            row.fetch(raw + (b % RAWH_SLOTS) * L::RAWH_BYTES, p, key, sub);
             __syncwarp();
             next();
+            const int sp = jg % L::VP_SLOTS;
+            if (jg >= L::VP_SLOTS && !warp_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
+              timed_out = true;
+              break;
+            }
+            row.put(sbase + L::VP_OFF + sp * V_SLOT_BYTES, c, key, sub);
+            fence_proxy_async();
+            bar_arrive(bar(B_FULLVP + sp));
           }
-          if ((ig >= L::RA_SLOTS && !warp_wait(bar(B_EMPTYA + sa), pa)) ||
-              (ig >= L::VO_SLOTS && !warp_wait(bar(B_EMPTYVO + so), po))) {
-            timed_out = true;
-            break;
-          }
-          const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
-          const uint32_t rv = sbase + L::VO_OFF + so * V_SLOT_BYTES;
-          const uint32_t lo = (c ? ra : rv) + at0, hi = (c ? rv : ra) + at0;   // dims below / from 256
-          put(lo, code[0], scale.x >> sh);
-          put(lo + 2 * KV_BLOCK_BYTES, code[1], scale.y >> sh);
-          put(hi, code[2], scale.z >> sh);
-          put(hi + 2 * KV_BLOCK_BYTES, code[3], scale.w >> sh);
-          st_shared16(ra + rope_at, rope);
-          fence_proxy_async();
-          bar_arrive(bar(B_FULLA + sa));
-          // the next tile's slots, and the parity of their next release
-          if (++sa == L::RA_SLOTS) { sa = 0; pa ^= 1; }
-          if (++so == L::VO_SLOTS) { so = 0; po ^= 1; }
+          cp_async_wait<0>();
         }
-        cp_async_wait<0>();
       }
     } else {
-      // chunks sub + 4 k of the half's 16: block k of the slot, exponent word
-      // 2 c + k / 2, byte 2 (k & 1) + sub / 2
-      const uint32_t raw = sbase + L::RAWH_OFF;
-      auto copy = [&](int32_t id, int slot) {
-        const bool v = id >= 0 && id < n_kv;
-        const char *row = (v ? kv + (int64_t)id * HS_Q8_ROW_BYTES : q) + sub * 16;
-        const uint32_t to = raw + slot * RAWH_BYTES;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          cp_async16(to + p * 16 + k * (Q8_HALF * 16), row + (DV / 2) * c + k * 64, v);
-        if (sub == 0) cp_async16(to + 4 * Q8_HALF * 16 + key * 16, row + Q8_SCALE_OFF, v);
-        cp_async_commit();
+      // ------------------------------------------------ gather producers ----
+      const int p = tid - 128;          // 0..255
+      const int key = p >> 3;           // 32 keys per tile, 8 threads per key
+      const int sub = p & 7;            // chunk sub of every 64-dim block
+      auto load_id = [&](int t) -> int32_t {
+        const int j = t * NK + key;
+        return (t < T && j < K) ? ld_global(idx_row + j) : -1;
       };
-      const uint32_t at0 = sw128(key, 2 * sub);
-      int jg = 0;                      // peer tiles taken, over both passes
-      if (!warp_wait(bar(B_QSTAGED), 0)) timed_out = true;
+      int ig = 0, jg = 0;               // own / peer tiles issued, over both passes
       for (int pass = 0; pass < 2 && !timed_out; ++pass) {
         if (pass == 1) {
-          if (!warp_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
+          if (!bar_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
           if (!*s_redo) break;
         }
-        int copied = 0;
-        int32_t id = load_id(1 - c);
-        auto next = [&]() {
-          copy(id, copied % RAWH_SLOTS);
-          ++copied;
-          id = load_id(2 * copied + 1 - c);
+        // gather order: the own tiles run up to PEER_LAG + 1 ahead of the
+        // peer tiles, whose value halves are read only once the peer's P has
+        // come, so that a ring VP slot is taken only shortly before its use
+        int na = 0, nb = 0;             // own / peer tiles of this pass taken
+        int la = 0, lb = 0;             // the same two steps ahead (index prefetch)
+        auto step = [&](int &a, int &b) -> int {
+          if (a < n_own && (b >= n_peer || a < b + PEER_LAG + 1)) return 2 * (a++) + c;
+          if (b < n_peer) return 2 * (b++) + (1 - c);
+          return T;
         };
-        for (int k = 0; k < RAWH_SLOTS; ++k) next();
-        for (int b = 0; b < n_peer; ++b, ++jg) {
-          cp_async_wait<RAWH_SLOTS - 1>();
-          __syncwarp();
-          const uint32_t from = raw + (b % RAWH_SLOTS) * RAWH_BYTES;
-          uint4 code[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) code[k] = ld_shared16(from + (k * Q8_HALF + p) * 16);
-          const uint4 scale = ld_shared16(from + 4 * Q8_HALF * 16 + key * 16);
-          __syncwarp();
-          next();
-          const int sp = jg % L::VP_SLOTS;
-          if (jg >= L::VP_SLOTS && !warp_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
-            timed_out = true;
-            break;
+        const int t0 = step(la, lb);
+        const int t1 = step(la, lb);
+        int32_t id0 = load_id(t0), id1 = load_id(t1);
+        for (int i = 0; i < T; ++i) {
+          const int t = step(na, nb);
+          const int32_t id = id0;
+          id0 = id1;
+          id1 = load_id(step(la, lb));
+          const bool v = id >= 0 && id < n_kv;
+          const char *src = kv + (v ? (int64_t)id * ROWB : 0);
+          if ((t & 1) == c) {
+            const int sa = ig % L::RA_SLOTS, so = ig % L::VO_SLOTS;
+            // slots 1 and 2 hold staged Q until it is in TMEM
+            if (ig == 1 && !bar_wait(bar(B_QSTAGED), 0)) {
+              timed_out = true;
+              break;
+            }
+            if (ig >= L::RA_SLOTS && !bar_wait(bar(B_EMPTYA + sa), ((ig / L::RA_SLOTS) - 1) & 1)) {
+              timed_out = true;
+              break;
+            }
+            if (ig >= L::VO_SLOTS && !bar_wait(bar(B_EMPTYVO + so), ((ig / L::VO_SLOTS) - 1) & 1)) {
+              timed_out = true;
+              break;
+            }
+            const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
+            const uint32_t rv = sbase + L::VO_OFF + so * V_SLOT_BYTES;
+            // copy k of this thread is chunk sub + 4k: swizzle block k / 2,
+            // chunk sub + 4 (k & 1) within the block's 128-byte row
+  #pragma unroll
+            for (int k = 0; k < NCH / 8; ++k) {
+              const int ch = sub + 8 * k;
+              cp_async16(kv_block(ra, rv, c, k) + sw128(key, sub), v ? src + ch * 16 : q, v);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(B_FULLA + sa))
+                         : "memory");
+            ++ig;
+          } else {
+            const int sp = jg % L::VP_SLOTS;
+            if (jg >= L::VP_SLOTS && !bar_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
+              timed_out = true;
+              break;
+            }
+            const uint32_t rv = sbase + L::VP_OFF + sp * V_SLOT_BYTES;
+            // only this CTA's value half: copies k = 8c .. 8c + 7 of the 18
+  #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int ch = 32 * c + sub + 8 * k;
+              cp_async16(rv + k * KV_BLOCK_BYTES + sw128(key, sub), v ? src + ch * 16 : q, v);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(B_FULLVP + sp))
+                         : "memory");
+            ++jg;
           }
-          const uint32_t to = sbase + L::VP_OFF + sp * V_SLOT_BYTES + at0;
-          const uint32_t lo = c ? scale.z : scale.x, hi = c ? scale.w : scale.y;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            put(to + k * KV_BLOCK_BYTES, code[k], (k < 2 ? lo : hi) >> (16 * (k & 1) + sh));
-          fence_proxy_async();
-          bar_arrive(bar(B_FULLVP + sp));
-        }
-        cp_async_wait<0>();
-      }
-    }
-  } else if (warp >= 4 && warp < 12) {
-    // ------------------------------------------------ gather producers ----
-    const int p = tid - 128;          // 0..255
-    const int key = p >> 3;           // 32 keys per tile, 8 threads per key
-    const int sub = p & 7;            // chunk sub of every 64-dim block
-    auto load_id = [&](int t) -> int32_t {
-      const int j = t * NK + key;
-      return (t < T && j < K) ? ld_global(idx_row + j) : -1;
-    };
-    int ig = 0, jg = 0;               // own / peer tiles issued, over both passes
-    for (int pass = 0; pass < 2 && !timed_out; ++pass) {
-      if (pass == 1) {
-        if (!bar_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
-        if (!*s_redo) break;
-      }
-      // gather order: the own tiles run up to PEER_LAG + 1 ahead of the
-      // peer tiles, whose value halves are read only once the peer's P has
-      // come, so that a ring VP slot is taken only shortly before its use
-      int na = 0, nb = 0;             // own / peer tiles of this pass taken
-      int la = 0, lb = 0;             // the same two steps ahead (index prefetch)
-      auto step = [&](int &a, int &b) -> int {
-        if (a < n_own && (b >= n_peer || a < b + PEER_LAG + 1)) return 2 * (a++) + c;
-        if (b < n_peer) return 2 * (b++) + (1 - c);
-        return T;
-      };
-      const int t0 = step(la, lb);
-      const int t1 = step(la, lb);
-      int32_t id0 = load_id(t0), id1 = load_id(t1);
-      for (int i = 0; i < T; ++i) {
-        const int t = step(na, nb);
-        const int32_t id = id0;
-        id0 = id1;
-        id1 = load_id(step(la, lb));
-        const bool v = id >= 0 && id < n_kv;
-        const char *src = kv + (v ? (int64_t)id * ROWB : 0);
-        if ((t & 1) == c) {
-          const int sa = ig % L::RA_SLOTS, so = ig % L::VO_SLOTS;
-          // slots 1 and 2 hold staged Q until it is in TMEM
-          if (ig == 1 && !bar_wait(bar(B_QSTAGED), 0)) {
-            timed_out = true;
-            break;
-          }
-          if (ig >= L::RA_SLOTS && !bar_wait(bar(B_EMPTYA + sa), ((ig / L::RA_SLOTS) - 1) & 1)) {
-            timed_out = true;
-            break;
-          }
-          if (ig >= L::VO_SLOTS && !bar_wait(bar(B_EMPTYVO + so), ((ig / L::VO_SLOTS) - 1) & 1)) {
-            timed_out = true;
-            break;
-          }
-          const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
-          const uint32_t rv = sbase + L::VO_OFF + so * V_SLOT_BYTES;
-          // copy k of this thread is chunk sub + 4k: swizzle block k / 2,
-          // chunk sub + 4 (k & 1) within the block's 128-byte row
-#pragma unroll
-          for (int k = 0; k < NCH / 8; ++k) {
-            const int ch = sub + 8 * k;
-            cp_async16(kv_block(ra, rv, c, k) + sw128(key, sub), v ? src + ch * 16 : q, v);
-          }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(B_FULLA + sa))
-                       : "memory");
-          ++ig;
-        } else {
-          const int sp = jg % L::VP_SLOTS;
-          if (jg >= L::VP_SLOTS && !bar_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
-            timed_out = true;
-            break;
-          }
-          const uint32_t rv = sbase + L::VP_OFF + sp * V_SLOT_BYTES;
-          // only this CTA's value half: copies k = 8c .. 8c + 7 of the 18
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int ch = 32 * c + sub + 8 * k;
-            cp_async16(rv + k * KV_BLOCK_BYTES + sw128(key, sub), v ? src + ch * 16 : q, v);
-          }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(B_FULLVP + sp))
-                       : "memory");
-          ++jg;
         }
       }
+      cp_async_wait<0>();
     }
-    cp_async_wait<0>();
   } else if (warp >= 12 && warp < 12 + NSB) {
     // ------------------------------------- Q K^T issuers (own tiles) ----
     // warp 12 + b issues own tiles ig = b, b + 2, ... into S buffer b
@@ -936,8 +1080,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
           if (ok && ig >= NSB) ok = warp_wait(bar(B_SFREE + b), ((ig / NSB) - 1) & 1);
           if (!ok) break;
           fence_after();
-          if (!Q8) fence_proxy_async();   // the tile was written by cp.async (generic proxy)
-                                          // (the q8 producers fence their own stores)
+          if (!RAW) fence_proxy_async();  // the tile was written by cp.async (generic proxy)
+                                          // (who decodes rows fences its own stores)
           const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
           const uint32_t rv = sbase + L::VO_OFF + (ig % L::VO_SLOTS) * V_SLOT_BYTES;
           const uint32_t sd = tmem + COL_S + b * NK;
@@ -1000,8 +1144,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
             }
             if (!ok) break;
             fence_after();
-            if (!Q8) fence_proxy_async();   // V by cp.async, P by a bulk copy (V fenced by its
-                                            // producers: q8)
+            if (!RAW) fence_proxy_async();  // V by cp.async, P by a bulk copy (decoded V is
+                                            // fenced by its producers)
             const uint32_t vb = sbase + L::VP_OFF + sp * V_SLOT_BYTES;
             if (elect_one()) {
 #pragma unroll
@@ -1163,11 +1307,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     if (!decided && tid == 0) bar_arrive(bar(B_DECIDE));   // lets the other roles wind down
 
     // 1 / l of the head for the epilogue (the first-tile maxima's slot is
-    // free: the reference was agreed in the first pass)
+    // free: the reference was agreed in the first pass), and what q4 values are short of
+    constexpr float out_scale = F == HS_ROWS_Q4 ? (float)(1 << Q4_SHIFT) : 1.f;
     const int h = h0 + hrow;
     const float lt = l + l_peer;
-    reinterpret_cast<volatile float *>(sm + L::XMAX_OFF)[hrow] = lt > 0.f ? 1.0f / lt : 0.f;
-    float *lse_to = Q8 && parts.n > 1 ? parts.lse + (int64_t)part * parts.R * H : lse;
+    reinterpret_cast<volatile float *>(sm + L::XMAX_OFF)[hrow] = lt > 0.f ? out_scale / lt : 0.f;
+    float *lse_to = RAW && parts.n > 1 ? parts.lse + (int64_t)part * parts.R * H : lse;
     if (lse_to && c == 0 && h < H)
       lse_to[(int64_t)r * H + h] = lt > 0.f ? (ref + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
     if (tid == 0) *s_last = (uint32_t)last_pass;
@@ -1195,7 +1340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Q8 ? Q8_MAX_REGS : ATTN_MA
     fence_after();
     const int q4 = warp & 3, half = warp >> 2;
     const int row = q4 * 32 + lane;
-    const bool f32_out = Q8 && parts.n > 1;
+    const bool f32_out = RAW && parts.n > 1;
     const float inv = ok ? reinterpret_cast<volatile float *>(sm + L::XMAX_OFF)[row] : 0.f;
     const uint32_t lane_q = tmem + ((uint32_t)(q4 * 32) << 16);
     // the warp's 32 rows in blocks of 128 bytes of each, 128-byte swizzled
@@ -1300,10 +1445,12 @@ static int set_attn_attributes() {
   HS_CUDA_TRY(cudaGetDevice(&dev));
   static std::atomic<bool> attr_done[64];
   if (dev >= 64 || !attr_done[dev]) {
-    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     Lay<false>::SMEM_ALLOC));
-    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     Lay<true>::SMEM_ALLOC));
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<HS_ROWS_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Lay<HS_ROWS_BF16>::SMEM_ALLOC));
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<HS_ROWS_Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Lay<HS_ROWS_Q8>::SMEM_ALLOC));
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_pair<HS_ROWS_Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Lay<HS_ROWS_Q4>::SMEM_ALLOC));
     if (dev < 64) attr_done[dev] = true;
   }
   return HS_OK;
@@ -1312,9 +1459,9 @@ static int set_attn_attributes() {
 int hs_attn_block_attrs(cudaFuncAttributes *attr, int *threads, size_t *dyn_smem) {
   int rc = set_attn_attributes();
   if (rc) return rc;
-  HS_CUDA_TRY(cudaFuncGetAttributes(attr, k_attn_pair<false>));
+  HS_CUDA_TRY(cudaFuncGetAttributes(attr, k_attn_pair<HS_ROWS_BF16>));
   *threads = THREADS;
-  *dyn_smem = Lay<false>::SMEM_ALLOC;
+  *dyn_smem = Lay<HS_ROWS_BF16>::SMEM_ALLOC;
   return HS_OK;
 }
 
@@ -1329,7 +1476,7 @@ int hs_attn_wave_rows(int32_t H, int32_t *rows) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Lay<false>::SMEM_ALLOC;
+    cfg.dynamicSmemBytes = Lay<HS_ROWS_BF16>::SMEM_ALLOC;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -1337,7 +1484,7 @@ int hs_attn_wave_rows(int32_t H, int32_t *rows) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    HS_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_attn_pair<false>, &cfg));
+    HS_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, k_attn_pair<HS_ROWS_BF16>, &cfg));
     if (n < 1) n = 1;
     if (dev < 64) clusters[dev].store(n, std::memory_order_relaxed);
   }
@@ -1375,9 +1522,9 @@ static int check_attn(const void *q, const void *kv_resident, int64_t n_resident
   return HS_OK;
 }
 
-// Launches k_attn_pair<Q8>, its arguments checked (parts: the q8 kernel's split
-// of the rows' keys).
-template <bool Q8>
+// Launches k_attn_pair<F>, its arguments checked (parts: the split of the rows'
+// keys, quantised rows only; scale: of the values as the kernel has them).
+template <int F>
 static int attn_launch(const void *q, const void *kv_resident, int64_t n_resident,
                        const void *kv_hot, int64_t n_hot, const int32_t *row_req,
                        const int32_t *fully_resident, int32_t n_reqs, const int32_t *idx, int32_t R,
@@ -1432,8 +1579,8 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
   // run while the previous kernel in the stream finishes
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(Q8 ? Q8_THREADS : THREADS);
-  cfg.dynamicSmemBytes = Lay<Q8>::SMEM_ALLOC;
+  cfg.blockDim = dim3(Lay<F>::RAW ? RAW_THREADS : THREADS);
+  cfg.dynamicSmemBytes = Lay<F>::SMEM_ALLOC;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1441,7 +1588,7 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   HS_CUDA_TRY(cudaLaunchKernelEx(
-      &cfg, k_attn_pair<Q8>, tmap, tmap_o, reinterpret_cast<const char *>(q),
+      &cfg, k_attn_pair<F>, tmap, tmap_o, reinterpret_cast<const char *>(q),
       reinterpret_cast<const char *>(kv_resident), n_resident,
       reinterpret_cast<const char *>(kv_hot), n_hot, row_req, fully_resident, n_reqs, idx, H, K,
       scale * 1.4426950408889634f, reinterpret_cast<__nv_bfloat16 *>(out), lse, status, parts));
@@ -1458,7 +1605,7 @@ int hs_attn_launch(const void *q, const void *kv_resident, int64_t n_resident, c
                             scale, out);
   if (rc || R == 0) return rc;
   const Parts whole = {1, K, R, nullptr, nullptr};
-  return attn_launch<false>(q, kv_resident, n_resident, kv_hot, n_hot, row_req, fully_resident,
+  return attn_launch<HS_ROWS_BF16>(q, kv_resident, n_resident, kv_hot, n_hot, row_req, fully_resident,
                             n_reqs, idx, R, H, K, scale, out, lse, status, whole, pdl, stream);
 }
 
@@ -1470,7 +1617,7 @@ extern "C" int hs_sparse_attn_decode(const void *q, const void *kv, int64_t n_kv
                                      H, K, scale, out, lse, status, stream);
 }
 
-// ---- attention over a q8 cache ----------------------------------------------
+// ---- attention over a quantised cache ----------------------------------------------
 
 namespace {
 
@@ -1542,22 +1689,25 @@ constexpr int PART_MIN_TILES = 4, PART_MIN_TILES_FEW = 2;
 
 }  // namespace
 
-extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n_kv_rows,
-                                        const int32_t *idx, int32_t R, int32_t H, int32_t K,
-                                        float scale, void *out, float *lse, void *workspace,
-                                        size_t workspace_bytes, uint32_t *status,
-                                        hs_stream_t stream) {
+// The attention over rows of format F (HS_ROWS_Q8, HS_ROWS_Q4).
+template <int F>
+static int attn_quantised(const void *q, const void *kv, int64_t n_kv_rows, const int32_t *idx, int32_t R, int32_t H,
+                          int32_t K, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                          uint32_t *status, cudaStream_t stream) {
   if ((uintptr_t)workspace & 15)
     return hs_set_error(HS_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   if (((uintptr_t)idx | (uintptr_t)lse | (uintptr_t)status) & 3)
     return hs_set_error(HS_ERR_INVALID_ARG, "idx, lse and status must be 4-byte aligned");
   // the softmax reference is the scaled maximum, which a negative scale would not
   // give; times log2(e), as the kernels take it, the scale is to be finite too
-  if (!(scale >= 0.f) || scale > 0x1p127f)
-    return hs_set_error(HS_ERR_INVALID_ARG, "scale must be in [0, 2^127]");
+  // (and so is it for scores that are 2^-15 of theirs)
+  const int most = F == HS_ROWS_Q4 ? 100 : 127;
+  if (!(scale >= 0.f) || scale > ldexpf(1.f, most))
+    return hs_set_error(HS_ERR_INVALID_ARG, "scale must be in [0, 2^%d]", most);
   if (scale < FLT_MIN) scale = FLT_MIN;      // equal weights all the same; 0 times a masked -inf is NaN
   int rc = check_attn(q, kv, n_kv_rows, nullptr, 0, nullptr, 0, idx, R, H, K, scale, out);
   if (rc || R == 0) return rc;
+  if (F == HS_ROWS_Q4) scale *= (float)(1 << Q4_SHIFT);
   const bool few_heads = H <= HS_ATTN_FEW_HEADS;
   Parts parts = {1, K, R, nullptr, nullptr};
   if (K > 0 && workspace) {
@@ -1582,9 +1732,9 @@ extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n
     }
     if (parts.n == 1) parts.keys = K;
   }
-  rc = few_heads ? hs_attn_few_launch(q, kv, n_kv_rows, idx, R, H, K, scale, out, lse, parts.n, parts.keys,
+  rc = few_heads ? hs_attn_few_launch(F, q, kv, n_kv_rows, idx, R, H, K, scale, out, lse, parts.n, parts.keys,
                                       parts.o, parts.lse, stream)
-                 : attn_launch<true>(q, kv, n_kv_rows, nullptr, 0, nullptr, nullptr, 0, idx, R, H, K, scale,
+                 : attn_launch<F>(q, kv, n_kv_rows, nullptr, 0, nullptr, nullptr, 0, idx, R, H, K, scale,
                                      out, lse, status, parts, true, stream);
   if (rc || parts.n == 1) return rc;
   const bool few = (int64_t)R * H <= JOIN_FEW;
@@ -1602,4 +1752,22 @@ extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n
                                  reinterpret_cast<__nv_bfloat16 *>(out), lse));
   HS_LAUNCH_CHECK("k_attn_join");
   return HS_OK;
+}
+
+extern "C" int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n_kv_rows,
+                                        const int32_t *idx, int32_t R, int32_t H, int32_t K,
+                                        float scale, void *out, float *lse, void *workspace,
+                                        size_t workspace_bytes, uint32_t *status,
+                                        hs_stream_t stream) {
+  return attn_quantised<HS_ROWS_Q8>(q, kv, n_kv_rows, idx, R, H, K, scale, out, lse, workspace, workspace_bytes,
+                                    status, stream);
+}
+
+extern "C" int hs_sparse_attn_decode_q4(const void *q, const void *kv, int64_t n_kv_rows,
+                                        const int32_t *idx, int32_t R, int32_t H, int32_t K,
+                                        float scale, void *out, float *lse, void *workspace,
+                                        size_t workspace_bytes, uint32_t *status,
+                                        hs_stream_t stream) {
+  return attn_quantised<HS_ROWS_Q4>(q, kv, n_kv_rows, idx, R, H, K, scale, out, lse, workspace, workspace_bytes,
+                                    status, stream);
 }

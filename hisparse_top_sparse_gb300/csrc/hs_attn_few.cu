@@ -39,6 +39,7 @@
 #include <atomic>
 #include <math.h>
 
+#include "hs_q4.cuh"
 #include "hs_q8.cuh"
 
 namespace {
@@ -47,21 +48,65 @@ constexpr int NT = 256, WARPS = NT / 32;
 constexpr int HEADS = HS_ATTN_FEW_HEADS;       // a matrix instruction's rows
 constexpr int KEYS = 32;                       // keys of a tile
 constexpr int STAGES = 3;                      // tiles of raw rows on their way
-constexpr int ROW_STRIDE = 704;
-constexpr int STAGE_BYTES = KEYS * ROW_STRIDE;
+// What differs between the row formats: a raw row and its place (whose stride
+// spreads a warp's reads over the banks), and the 16 codes of a lane.
+template <int F>
+struct Row {};
+template <>
+struct Row<HS_ROWS_Q8> {
+  static constexpr int BYTES = HS_Q8_ROW_BYTES, STRIDE = 704, ROPE_OFF = Q8_ROPE_OFF;
+  static constexpr float OUT_SCALE = 1.f;
+  uint4 code;
+  uint32_t byte;
+  __device__ __forceinline__ void fetch(const unsigned char *row, int warp, int j) {
+    code = *reinterpret_cast<const uint4 *>(row + 64 * warp + 16 * j);
+    byte = row[Q8_SCALE_OFF + 2 * warp + (j >> 1)];
+  }
+  // dims 4 k .. 4 k + 3 of the 16
+  __device__ __forceinline__ void decode(uint2 (&d)[4]) const {
+    const uint64_t s = q8_scale2(byte);
+    d[0] = q8_decode4_bf16(code.x, s), d[1] = q8_decode4_bf16(code.y, s);
+    d[2] = q8_decode4_bf16(code.z, s), d[3] = q8_decode4_bf16(code.w, s);
+  }
+  static __device__ __forceinline__ uint32_t rope(uint32_t pair) { return pair; }
+};
+template <>
+struct Row<HS_ROWS_Q4> {
+  static constexpr int BYTES = HS_Q4_ROW_BYTES, STRIDE = HS_Q4_ROW_BYTES, ROPE_OFF = Q4_ROPE_OFF;
+  static constexpr float OUT_SCALE = (float)(1 << Q4_SHIFT);      // the values are 2^-15 of theirs
+  uint2 code;
+  uint32_t byte;
+  __device__ __forceinline__ void fetch(const unsigned char *row, int warp, int j) {
+    code = *reinterpret_cast<const uint2 *>(row + 32 * warp + 8 * j);
+    byte = row[Q4_SCALE_OFF + 4 * warp + j];
+  }
+  __device__ __forceinline__ void decode(uint2 (&d)[4]) const {
+    const uint32_t s = q4_scale2(byte);
+    d[0] = make_uint2(q4_decode2<0>(code.x, s), q4_decode2<1>(code.x, s));
+    d[1] = make_uint2(q4_decode2<2>(code.x, s), q4_decode2<3>(code.x, s));
+    d[2] = make_uint2(q4_decode2<0>(code.y, s), q4_decode2<1>(code.y, s));
+    d[3] = make_uint2(q4_decode2<2>(code.y, s), q4_decode2<3>(code.y, s));
+  }
+  static __device__ __forceinline__ uint32_t rope(uint32_t pair) { return q4_mul(pair, Q4_DOWN2); }
+};
 constexpr int PARTIALS = WARPS + 2;            // 512 dims by warps, the rope dims in halves
 constexpr int S_STRIDE = 40;                   // floats from head to head
 constexpr int P_STRIDE = 40;                   // bf16 values from head to head
-constexpr int S_OFF = STAGES * STAGE_BYTES;
-constexpr int P_OFF = S_OFF + PARTIALS * HEADS * S_STRIDE * 4;
-constexpr int ALPHA_OFF = P_OFF + HEADS * P_STRIDE * 2;
 constexpr float REF_SLACK = 30.f;
 // which keys have a row: a byte for each warp's four, of STAGES + 1 tiles (a
 // tile's bits are read after the place of its raw rows has been given away)
-constexpr int VALID_OFF = ALPHA_OFF + HEADS * 4, VALID_TILES = STAGES + 1;
-constexpr int SMEM = VALID_OFF + VALID_TILES * WARPS;
+constexpr int VALID_TILES = STAGES + 1;
+template <int F>
+struct Lay {
+  static constexpr int STAGE_BYTES = KEYS * Row<F>::STRIDE;
+  static constexpr int S_OFF = STAGES * STAGE_BYTES;
+  static constexpr int P_OFF = S_OFF + PARTIALS * HEADS * S_STRIDE * 4;
+  static constexpr int ALPHA_OFF = P_OFF + HEADS * P_STRIDE * 2;
+  static constexpr int VALID_OFF = ALPHA_OFF + HEADS * 4;
+  static constexpr int SMEM = VALID_OFF + VALID_TILES * WARPS;
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two blocks on an SM");
+};
 static_assert(HEADS == 16 && 2 * WARPS == HEADS && HS_VALUE_DIM == 64 * WARPS, "layout");
-static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two blocks on an SM");
 
 struct FewArgs {
   const __nv_bfloat16 *q;
@@ -106,7 +151,10 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+template <int F>
 __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewArgs a) {
+  using L = Lay<F>;
+  constexpr int ROW_STRIDE = Row<F>::STRIDE, CHUNKS = Row<F>::BYTES / 16;
   extern __shared__ __align__(16) unsigned char sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, j = lane & 3;           // a fragment's row / column of four
@@ -132,17 +180,17 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   const char *kv = (a.n_kv > 0 ? a.kv : reinterpret_cast<const char *>(a.q)) + 16 * lane;
   auto copy = [&](int t, int stage) {
     if (t < T) {
-      const uint32_t to = smem_addr(sm) + stage * STAGE_BYTES + 4 * warp * ROW_STRIDE + 16 * lane;
+      const uint32_t to = smem_addr(sm) + stage * L::STAGE_BYTES + 4 * warp * ROW_STRIDE + 16 * lane;
       const bool valid = id >= 0 && id < a.n_kv;
       const uint32_t have = __ballot_sync(0xffffffffu, valid);
-      if (lane == 0) sm[VALID_OFF + (t % VALID_TILES) * WARPS + warp] = have & 15u;
+      if (lane == 0) sm[L::VALID_OFF + (t % VALID_TILES) * WARPS + warp] = have & 15u;
       if (!valid) id = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const char *row = kv + (int64_t)__shfl_sync(0xffffffffu, id, k) * HS_Q8_ROW_BYTES;
+        const char *row = kv + (int64_t)__shfl_sync(0xffffffffu, id, k) * Row<F>::BYTES;
         const bool v = (have >> k) & 1u;
-        cp16(to + k * ROW_STRIDE, row, v);
-        if (lane < HS_Q8_ROW_BYTES / 16 - 32) cp16(to + k * ROW_STRIDE + 512, row + 512, v);
+        if (CHUNKS >= 32 || lane < CHUNKS) cp16(to + k * ROW_STRIDE, row, v);
+        if (CHUNKS > 32 && lane < CHUNKS - 32) cp16(to + k * ROW_STRIDE + 512, row + 512, v);
       }
       id = index(t + 1, 4 * warp + j);
     }
@@ -173,8 +221,8 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   float o[4][2][4];
 #pragma unroll
   for (int k = 0; k < 32; ++k) o[k >> 3][(k >> 2) & 1][k & 3] = 0.f;
-  float *s_part = reinterpret_cast<float *>(sm + S_OFF);
-  float *s_alpha = reinterpret_cast<float *>(sm + ALPHA_OFF);
+  float *s_part = reinterpret_cast<float *>(sm + L::S_OFF);
+  float *s_alpha = reinterpret_cast<float *>(sm + L::ALPHA_OFF);
   // softmax: this lane's head and its keys 2 c, 2 c + 1 of a tile
   const int head = 2 * warp + (lane >> 4), c = lane & 15;
   float m = -INFINITY, l = 0.f;
@@ -182,28 +230,21 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 1) : "memory");
   __syncthreads();
   for (int t = 0, stage = 0; t < T; ++t) {
-    const unsigned char *raw = sm + stage * STAGE_BYTES;
+    const unsigned char *raw = sm + stage * L::STAGE_BYTES;
     uint32_t kf[4][4][2];
-    uint4 code[4];
-    uint32_t byte[4];
+    Row<F> row[4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) row[nt].fetch(raw + (8 * nt + g) * ROW_STRIDE, warp, j);
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      const unsigned char *row = raw + (8 * nt + g) * ROW_STRIDE;
-      code[nt] = *reinterpret_cast<const uint4 *>(row + 64 * warp + 16 * j);
-      byte[nt] = row[Q8_SCALE_OFF + 2 * warp + (j >> 1)];
-    }
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const uint4 w = code[nt];
-      const uint64_t sc = q8_scale2(byte[nt]);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      uint2 d[4];
+      row[nt].decode(d);
       float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint2 d = q8_decode4_bf16(ws[k], sc);
-        kf[nt][k][0] = d.x;
-        kf[nt][k][1] = d.y;
-        mma(s, qa[k][0], qa[k][1], qa[k][2], qa[k][3], d.x, d.y);
+        kf[nt][k][0] = d[k].x;
+        kf[nt][k][1] = d[k].y;
+        mma(s, qa[k][0], qa[k][1], qa[k][2], qa[k][3], d[k].x, d[k].y);
       }
       float *to = s_part + (warp * HEADS + g) * S_STRIDE + 8 * nt + 2 * j;
       *reinterpret_cast<float2 *>(to) = make_float2(s[0], s[1]);
@@ -212,11 +253,11 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
     {
       // the rope dims of eight keys, half of each row's
       const int nt = warp & 3;
-      const uint4 w = *reinterpret_cast<const uint4 *>(raw + (8 * nt + g) * ROW_STRIDE + Q8_ROPE_OFF +
+      const uint4 w = *reinterpret_cast<const uint4 *>(raw + (8 * nt + g) * ROW_STRIDE + Row<F>::ROPE_OFF +
                                                        2 * (16 * j + 8 * half));
       float s[4] = {0.f, 0.f, 0.f, 0.f};
-      mma(s, qr[0][0], qr[0][1], qr[0][2], qr[0][3], w.x, w.y);
-      mma(s, qr[1][0], qr[1][1], qr[1][2], qr[1][3], w.z, w.w);
+      mma(s, qr[0][0], qr[0][1], qr[0][2], qr[0][3], Row<F>::rope(w.x), Row<F>::rope(w.y));
+      mma(s, qr[1][0], qr[1][1], qr[1][2], qr[1][3], Row<F>::rope(w.z), Row<F>::rope(w.w));
       float *to = s_part + ((WARPS + half) * HEADS + g) * S_STRIDE + 8 * nt + 2 * j;
       *reinterpret_cast<float2 *>(to) = make_float2(s[0], s[1]);
       *reinterpret_cast<float2 *>(to + 8 * S_STRIDE) = make_float2(s[2], s[3]);
@@ -232,7 +273,7 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
         sum = add2(sum, *reinterpret_cast<const uint64_t *>(s_part + (p * HEADS + head) * S_STRIDE + 2 * c));
       float s0, s1;
       asm("mov.b64 {%0, %1}, %2;\n" : "=f"(s0), "=f"(s1) : "l"(sum));
-      const uint32_t have = sm[VALID_OFF + (t % VALID_TILES) * WARPS + (c >> 1)] >> (2 * (c & 1));
+      const uint32_t have = sm[L::VALID_OFF + (t % VALID_TILES) * WARPS + (c >> 1)] >> (2 * (c & 1));
       s0 = have & 1u ? s0 * a.scale_log2 : -INFINITY;
       s1 = have & 2u ? s1 * a.scale_log2 : -INFINITY;
       float top = fmaxf(s0, s1), alpha = 1.f;
@@ -249,7 +290,7 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
       s0 = ex2(s0 - ref);
       s1 = ex2(s1 - ref);
       l += s0 + s1;
-      *reinterpret_cast<uint32_t *>(sm + P_OFF + (head * P_STRIDE + 2 * c) * 2) = pack(s0, s1);
+      *reinterpret_cast<uint32_t *>(sm + L::P_OFF + (head * P_STRIDE + 2 * c) * 2) = pack(s0, s1);
       if (c == 0) s_alpha[head] = alpha;
     }
     asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 1) : "memory");
@@ -267,7 +308,7 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(sm + P_OFF) + g * (P_STRIDE / 2) + 8 * u + j;
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(sm + L::P_OFF) + g * (P_STRIDE / 2) + 8 * u + j;
         const uint32_t p0 = p[0], p1 = p[8 * (P_STRIDE / 2)], p2 = p[4], p3 = p[8 * (P_STRIDE / 2) + 4];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -283,7 +324,7 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
   for (int d = 1; d < 16; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   __syncthreads();                   // alpha has been read
   if (c == 0) {
-    s_alpha[head] = l == 0.f ? 0.f : 1.f / l;
+    s_alpha[head] = l == 0.f ? 0.f : Row<F>::OUT_SCALE / l;
     float *to = a.n > 1 ? a.part_lse + (int64_t)part * a.R * a.H : a.lse;
     if (to && head < a.H)
       to[(int64_t)r * a.H + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
@@ -321,30 +362,34 @@ int hs_attn_few_places(int *places) {
   return rc;
 }
 
-int hs_attn_few_launch(const void *q, const void *kv, int64_t n_kv, const int32_t *idx, int32_t R, int32_t H,
-                       int32_t K, float scale, void *out, float *lse, int32_t n, int32_t keys, float *part_o,
-                       float *part_lse, cudaStream_t stream) {
+int hs_attn_few_launch(int format, const void *q, const void *kv, int64_t n_kv, const int32_t *idx, int32_t R,
+                       int32_t H, int32_t K, float scale, void *out, float *lse, int32_t n, int32_t keys,
+                       float *part_o, float *part_lse, cudaStream_t stream) {
   if ((int64_t)R * n > INT32_MAX) return hs_set_error(HS_ERR_UNSUPPORTED, "R too large");
   int dev = 0;
   HS_CUDA_TRY(cudaGetDevice(&dev));
   static std::atomic<bool> attr_done[64];
   if (dev >= 64 || !attr_done[dev]) {
-    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_few, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_few<HS_ROWS_Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Lay<HS_ROWS_Q8>::SMEM));
+    HS_CUDA_TRY(cudaFuncSetAttribute(k_attn_few<HS_ROWS_Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Lay<HS_ROWS_Q4>::SMEM));
     if (dev < 64) attr_done[dev] = true;
   }
+  const bool q4 = format == HS_ROWS_Q4;
   FewArgs a = {reinterpret_cast<const __nv_bfloat16 *>(q), reinterpret_cast<const char *>(kv), n_kv, idx, R, H, K, n,
                keys, scale * 1.4426950408889634f, reinterpret_cast<__nv_bfloat16 *>(out), lse, part_o, part_lse};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(R * n));
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.dynamicSmemBytes = q4 ? Lay<HS_ROWS_Q4>::SMEM : Lay<HS_ROWS_Q8>::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  HS_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_attn_few, a));
+  HS_CUDA_TRY(cudaLaunchKernelEx(&cfg, q4 ? k_attn_few<HS_ROWS_Q4> : k_attn_few<HS_ROWS_Q8>, a));
   HS_LAUNCH_CHECK("k_attn_few");
   return HS_OK;
 }

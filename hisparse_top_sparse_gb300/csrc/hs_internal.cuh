@@ -76,13 +76,15 @@ int hs_set_error(int code, const char *fmt, ...);
 int hs_bind_context();
 // Multiprocessors of the current device (looked up once per device).
 int hs_sm_count(int *sms);
-// Attention over q8 rows for up to HS_ATTN_FEW_HEADS heads, its arguments
-// checked: n parts of `keys` keys a row (n > 1: O / l and the log-sum-exp of a
+// Formats of a cache's rows, as the attention kernels are told them.
+enum { HS_ROWS_BF16 = 0, HS_ROWS_Q8 = 1, HS_ROWS_Q4 = 2 };
+// Attention over q8 or q4 rows (format) for up to HS_ATTN_FEW_HEADS heads, its
+// arguments checked (scale: of the values as the kernel has them): n parts of `keys` keys a row (n > 1: O / l and the log-sum-exp of a
 // part in f32 to part_o and part_lse); blocks that run at once.
 constexpr int HS_ATTN_FEW_HEADS = 16;
 int hs_attn_few_places(int *places);
-int hs_attn_few_launch(const void *q, const void *kv, int64_t n_kv, const int32_t *idx, int32_t R, int32_t H,
-                       int32_t K, float scale, void *out, float *lse, int32_t n, int32_t keys, float *part_o,
+int hs_attn_few_launch(int format, const void *q, const void *kv, int64_t n_kv, const int32_t *idx, int32_t R,
+                       int32_t H, int32_t K, float scale, void *out, float *lse, int32_t n, int32_t keys, float *part_o,
                        float *part_lse, cudaStream_t stream);
 
 int hs_check_device_ptr(const void *p, const char *name, bool allow_null);

@@ -1,0 +1,88 @@
+// The q4 latent row (HS_Q4_ROW_BYTES bytes) and the conversions its kernels share.
+//
+//   [0, 256)    e2m1 codes of dims 0..511, a word of four bytes for eight dims:
+//               dim 2 i of the eight in nibble i, dim 2 i + 1 in nibble 4 + i
+//   [256, 384)  dims 512..575 (rope) in bf16, as they are
+//   [384, 416)  one scale byte for each 16 dims of the first 512: five bits of
+//               exponent x, three of fraction f, (8 + f) * 2^(x - 19)
+//
+// The value of a code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) is code *
+// scale. A group's scale is the smallest whose largest code, 6 * scale, reaches
+// the group's largest magnitude. A code has two significant bits and a scale
+// four, so every value is a bf16 number and reading a row back rounds nothing.
+// Four bits leave a group one step in six of its size: sixteen dims a scale and
+// three bits of fraction, rather than 32 and a power of two, halve the squared
+// error of normally distributed rows (their codes come out 1.05 to 1.0 times as
+// large as they need be, not up to 2), for 16 bytes more a row. Scales run from
+// 2^-16 to 1.75 * 2^15; byte 255 marks a group that held a NaN or an infinity,
+// all of whose values are NaN.
+// The order of the nibbles is that of a pair of bf16 values: nibble i and nibble
+// 4 + i lie 16 bits apart, so a shift and a mask take a pair out of a word.
+#pragma once
+
+#include <cuda_fp4.h>
+
+#include "hs_internal.cuh"
+
+constexpr int Q4_GROUP = 16;
+constexpr int Q4_ROPE_OFF = HS_VALUE_DIM / 2;                                    // 256
+constexpr int Q4_SCALE_OFF = Q4_ROPE_OFF + 2 * (HS_LATENT_DIM - HS_VALUE_DIM);   // 384
+static_assert(Q4_SCALE_OFF + HS_VALUE_DIM / Q4_GROUP == HS_Q4_ROW_BYTES, "q4 row");
+constexpr int Q4_BYTE_MAX = 254;           // the largest scale
+constexpr uint32_t Q4_BYTE_NAN = 255;
+constexpr int Q4_BIAS = (127 - 16) << 3;   // a scale byte and a float's top 12 bits (sign 0)
+
+// Scale byte of a group whose largest magnitude has the bits `amax` (infinities and
+// NaNs are the largest of all).
+__device__ __forceinline__ uint32_t q4_scale_byte(uint32_t amax) {
+  if (amax >= 0x7f800000u) return Q4_BYTE_NAN;
+  const float a = __uint_as_float(amax);
+  // a / 6 from above (1/6 rounded up, the product rounded up), cut to three bits
+  // of fraction: the scale wanted or the one below it
+  const uint32_t t = __float_as_uint(__fmul_ru(a, 0.166666671633720397949f)) >> 20;
+  const int b = (int)t - Q4_BIAS + (6.f * __uint_as_float(t << 20) < a);
+  return (uint32_t)min(max(b, 0), Q4_BYTE_MAX);
+}
+__device__ __forceinline__ float q4_scale(uint32_t byte) { return __uint_as_float((byte + Q4_BIAS) << 20); }
+
+// a / s of two values, correctly rounded, given the correctly rounded 1 / s: the
+// product's remainder, exact in an fma, corrects it (P. Markstein, Computation of
+// elementary functions on the IBM RISC System/6000 processor, 1990). Codes then
+// are what the exact quotients round to: a quotient lies on a middle between two
+// codes only if it is exactly that. (For the eight fractions of a scale and every
+// float this was checked against a division, on the host.)
+__device__ __forceinline__ float2 q4_over(float2 a, float s, float inv) {
+  const float x = a.x * inv, y = a.y * inv;
+  // (in this order of signs a zero keeps its own)
+  return make_float2(fmaf(-fmaf(s, x, -a.x), inv, x), fmaf(-fmaf(s, y, -a.y), inv, y));
+}
+// Two values over the scale to two codes, the first in the low nibble: to nearest,
+// ties to even, saturated.
+__device__ __forceinline__ uint32_t q4_encode2(float lo, float hi, float s, float inv) {
+  return (uint32_t)__nv_cvt_float2_to_fp4x2(q4_over(make_float2(lo, hi), s, inv), __NV_E2M1, cudaRoundNearest);
+}
+
+// Decoding, two codes at a time. The three bits of a magnitude, moved to where a
+// bf16 number has its last exponent bits and its first fraction bit, are the code
+// times 2^-126 (0.5 a subnormal one); a product with the scale times 2^111 gives
+// the value times 2^-15, exactly, and no scale overflows.
+constexpr int Q4_SHIFT = 15;               // q4_decode2's values are 2^-15 of theirs
+__device__ __forceinline__ uint32_t q4_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// a scale byte to the multiplier of q4_decode2, in both halves
+__device__ __forceinline__ uint32_t q4_scale2(uint32_t byte) {
+  const uint32_t s = byte == Q4_BYTE_NAN ? 0x7fc0u : (byte << 4) + ((127 - 16 + 126 - Q4_SHIFT) << 7);
+  return s * 0x10001u;
+}
+// dims 2 I and 2 I + 1 of a word's eight
+template <int I>
+__device__ __forceinline__ uint32_t q4_decode2(uint32_t word, uint32_t scale2) {
+  const uint32_t sign = I < 3 ? word << (12 - 4 * I) : word;
+  const uint32_t mag = I < 2 ? word << (6 - 4 * I) : word >> (4 * I - 6);
+  return q4_mul((sign & 0x80008000u) | (mag & 0x01c001c0u), scale2);
+}
+// 2^15 and 2^-15 in both halves
+constexpr uint32_t Q4_UP2 = ((127 + Q4_SHIFT) << 7) * 0x10001u, Q4_DOWN2 = ((127 - Q4_SHIFT) << 7) * 0x10001u;

@@ -16,14 +16,10 @@
 // row in flight 180, 40 warps 193); 131072 rows read back to bf16 40 us (89 %),
 // 131072 f32 rows there and back 128 us.
 
-#include <type_traits>
-
 #include "hs_q8.cuh"
+#include "hs_rows.cuh"
 
 namespace {
-
-constexpr int QT_THREADS = 256;
-constexpr int QT_BLOCKS = 4;    // blocks per SM, at most and at least
 
 template <typename T>
 struct Lay {
@@ -33,47 +29,6 @@ struct Lay {
   static constexpr int ROPE_LANES = (HS_LATENT_DIM - HS_VALUE_DIM) / VEC;
   static constexpr int ROWS = sizeof(T) == 2 ? 2 : 1;      // rows of one warp in flight
 };
-
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4 w, float (&f)[Lay<T>::VEC]) {
-  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-  if constexpr (std::is_same<T, float>::value) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(ws[k]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(ws[k] << 16);
-      f[2 * k + 1] = __uint_as_float(ws[k] & 0xFFFF0000u);
-    }
-  }
-}
-
-// The slots of a warp's next rows, loaded while the rows before them are on
-// their way: entries base, base + step, ...; without a list entry i is row i;
-// -1 past the last.
-template <int ROWS>
-struct Slots {
-  int32_t s[ROWS], d[ROWS];
-  __device__ __forceinline__ Slots(const int32_t *src_slots, const int32_t *dst_slots, int64_t base,
-                                   int64_t step, int32_t n) {
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-      const int64_t i = base + u * step;
-      s[u] = i >= n ? -1 : src_slots ? __ldg(src_slots + i) : (int32_t)i;
-      d[u] = i >= n ? -1 : dst_slots ? __ldg(dst_slots + i) : (int32_t)i;
-    }
-  }
-};
-
-// -1: no entry; a slot at or past `rows` gives -1 and sets bad.
-__device__ __forceinline__ int64_t row_of(int32_t s, int64_t rows, bool &bad) {
-  if (s >= rows) {
-    bad = true;
-    return -1;
-  }
-  return s;
-}
 
 template <typename T>
 __global__ void __launch_bounds__(QT_THREADS, QT_BLOCKS) k_quant_rows(
@@ -226,39 +181,6 @@ __global__ void __launch_bounds__(QT_THREADS, QT_BLOCKS) k_dequant_rows(
   if (bad && status) atomicOr(status, HS_STATUS_INDEX);
 }
 
-// Checks shared by both directions; wide: the bf16 / f32 side, q8: the other.
-int check_rows(const void *wide, int32_t dtype, int64_t wide_stride, int64_t wide_rows, const void *q8,
-               int64_t q8_rows, const int32_t *src_slots, const int32_t *dst_slots,
-               const uint32_t *status, int32_t n, const void **wide_dev, const void **q8_dev) {
-  if (dtype != HS_LOGITS_F32 && dtype != HS_LOGITS_BF16)
-    return hs_set_error(HS_ERR_INVALID_ARG, "row dtype %d", dtype);
-  const int64_t elem = dtype == HS_LOGITS_F32 ? 4 : 2;
-  if (n < 0 || wide_rows < 0 || q8_rows < 0 || wide_stride < HS_LATENT_DIM ||
-      wide_stride > (int64_t)1 << 30 || (wide_stride * elem) % 16)
-    return hs_set_error(HS_ERR_INVALID_ARG,
-                        "bad sizes n=%d rows=%lld/%lld stride=%lld (elements: at least 576, a "
-                        "multiple of 16 bytes)",
-                        n, (long long)wide_rows, (long long)q8_rows, (long long)wide_stride);
-  if (n == 0) return HS_OK;
-  if (!wide || !q8 || (((uintptr_t)wide | (uintptr_t)q8) & 15))
-    return hs_set_error(HS_ERR_INVALID_ARG, "src and dst must be 16-byte aligned and not NULL");
-  if (((uintptr_t)src_slots | (uintptr_t)dst_slots | (uintptr_t)status) & 3)
-    return hs_set_error(HS_ERR_INVALID_ARG, "slot lists and status must be 4-byte aligned");
-  int rc = hs_device_alias(wide, wide_dev, "the bf16 / f32 rows");
-  if (rc) return rc;
-  return hs_device_alias(q8, q8_dev, "the q8 rows");
-}
-
-// Blocks for n rows: a warp per row, up to QT_BLOCKS on every SM.
-int row_blocks(int32_t n, int *blocks) {
-  int sms = 0;
-  int rc = hs_sm_count(&sms);
-  if (rc) return rc;
-  const int64_t want = ((int64_t)n + QT_THREADS / 32 - 1) / (QT_THREADS / 32);
-  *blocks = (int)(want < (int64_t)sms * QT_BLOCKS ? want : (int64_t)sms * QT_BLOCKS);
-  return HS_OK;
-}
-
 }  // namespace
 
 extern "C" int hs_quant_rows(const void *src, int32_t src_dtype, int64_t src_stride, int64_t src_rows,
@@ -266,11 +188,11 @@ extern "C" int hs_quant_rows(const void *src, int32_t src_dtype, int64_t src_str
                              const int32_t *dst_slots, int32_t n, uint32_t *status,
                              hs_stream_t stream) {
   const void *s = nullptr, *d = nullptr;
-  int rc = check_rows(src, src_dtype, src_stride, src_rows, dst, dst_rows, src_slots, dst_slots,
+  int rc = hs_check_rows(src, src_dtype, src_stride, src_rows, dst, dst_rows, src_slots, dst_slots,
                       status, n, &s, &d);
   if (rc || n == 0) return rc;
   int blocks = 0;
-  if ((rc = row_blocks(n, &blocks))) return rc;
+  if ((rc = hs_row_blocks(n, &blocks))) return rc;
   const char *sp = reinterpret_cast<const char *>(s);
   char *dp = reinterpret_cast<char *>(const_cast<void *>(d));
   if (src_dtype == HS_LOGITS_F32)
@@ -288,11 +210,11 @@ extern "C" int hs_dequant_rows(const void *src, int64_t src_rows, void *dst, int
                                const int32_t *dst_slots, int32_t n, uint32_t *status,
                                hs_stream_t stream) {
   const void *s = nullptr, *d = nullptr;
-  int rc = check_rows(dst, dst_dtype, dst_stride, dst_rows, src, src_rows, src_slots, dst_slots,
+  int rc = hs_check_rows(dst, dst_dtype, dst_stride, dst_rows, src, src_rows, src_slots, dst_slots,
                       status, n, &d, &s);
   if (rc || n == 0) return rc;
   int blocks = 0;
-  if ((rc = row_blocks(n, &blocks))) return rc;
+  if ((rc = hs_row_blocks(n, &blocks))) return rc;
   const char *sp = reinterpret_cast<const char *>(s);
   char *dp = reinterpret_cast<char *>(const_cast<void *>(d));
   if (dst_dtype == HS_LOGITS_F32)

@@ -79,6 +79,16 @@ enum hs_status_code {
 #define HS_Q8_ROW_BYTES 656 /* a quantised latent row, see hs_quant_rows   */
 #define HS_ATTN_Q8_WORKSPACE_BYTES 33554432 /* enough for every call of
                                 hs_sparse_attn_decode_q8               */
+#define HS_Q4_ROW_BYTES 416 /* a latent row in 4 bits, see hs_quant_rows_q4 */
+#define HS_ATTN_Q4_WORKSPACE_BYTES 33554432 /* enough for every call of
+                                hs_sparse_attn_decode_q4               */
+
+#define HS_ROPE_INTERLEAVED 0 /* pairs of neighbouring dims 2 i, 2 i + 1   */
+#define HS_ROPE_HALF 1        /* pairs i, i + rot_dim / 2                  */
+#define HS_ROPE_PLAIN 0       /* how hs_rope_freqs scales its frequencies  */
+#define HS_ROPE_LINEAR 1
+#define HS_ROPE_NTK 2
+#define HS_ROPE_YARN 3
 
 /* ------------------------------------------------------------------------ */
 /* Hot buffer ([MTP] section 1 and core state maps; [VLLM] HiSparseHotSpec)  */
@@ -333,6 +343,119 @@ int hs_sparse_attn_decode_q8(const void *q, const void *kv, int64_t n_kv_rows,
                              const int32_t *idx, int32_t R, int32_t H, int32_t K, float scale,
                              void *out, float *lse, void *workspace, size_t workspace_bytes,
                              uint32_t *status, hs_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* q4: the same cache in 4 bits ("vllm 分析(十二) HiSparse 下篇", section      */
+/*     c4a kv cache 写入, names an FP4 cache: use_fp4_cache, quant_block,      */
+/*     scale_dim)                                                            */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A q4 row holds one latent row in 416 bytes, 16-byte aligned:
+ *   [0, 256)    e2m1 codes of dims 0..511, four bytes (a little-endian word) for
+ *               eight dims: of the word's nibbles, i holds dim 2 i and 4 + i
+ *               dim 2 i + 1, i < 4
+ *   [256, 384)  dims 512..575 (rope) in bf16
+ *   [384, 416)  a scale byte for each 16 dims of the first 512: x = byte >> 3
+ *               and f = byte & 7 give (8 + f) * 2^(x - 19);
+ * the value of a code (0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 negates it) is code *
+ * scale. A group's scale is the smallest of bytes 0 .. 254 with max |x| <= 6 *
+ * scale (254 where none is: larger values then become 6 * scale of their sign),
+ * its codes x / scale rounded to nearest, ties to the even code: within max(|x|
+ * / 4, scale / 4), and within scale, of x. A group with a NaN or an infinity has
+ * byte 255, and all its values are NaN. Every value of a row is a bf16 number, so
+ * reading rows back, in bf16 or f32, and attending over them rounds nothing. A
+ * row of zero bytes is a row of zeros. Rope dims are kept as bf16 keeps them.
+ *
+ * hs_swap_apply_plan, hs_backup_pages and hs_backup_rows move such rows with
+ * row_bytes = 416; the slot table of an hs_swap_in indexes a q4 follower cache
+ * for hs_sparse_attn_decode_q4.
+ */
+
+/* hs_quant_rows and hs_dequant_rows for q4 rows: arguments, skipped entries,
+ * status and requirements are theirs, with cache rows of 416 bytes. */
+int hs_quant_rows_q4(const void *src, int32_t src_dtype, int64_t src_stride, int64_t src_rows,
+                     void *dst, int64_t dst_rows, const int32_t *src_slots,
+                     const int32_t *dst_slots, int32_t n, uint32_t *status, hs_stream_t stream);
+int hs_dequant_rows_q4(const void *src, int64_t src_rows, void *dst, int32_t dst_dtype,
+                       int64_t dst_stride, int64_t dst_rows, const int32_t *src_slots,
+                       const int32_t *dst_slots, int32_t n, uint32_t *status, hs_stream_t stream);
+
+/* hs_sparse_attn_decode_q8 over a q4 cache, kv [n_kv_rows][416]: its arguments,
+ * formulas, workspace and launch. With H > 16 and each row in one part the
+ * results are those of hs_sparse_attn_decode over the rows read back, bit for
+ * bit, for rope dims that are 0 or of magnitudes in [2^-110, 2^127).
+ * 0 <= scale <= 2^100. */
+int hs_sparse_attn_decode_q4(const void *q, const void *kv, int64_t n_kv_rows,
+                             const int32_t *idx, int32_t R, int32_t H, int32_t K, float scale,
+                             void *out, float *lse, void *workspace, size_t workspace_bytes,
+                             uint32_t *status, hs_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions (beside the writes of a cache: the last 64 dims of q and  */
+/* of a latent row arrive rotated)                                           */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * For every entry i < n (row s = src_slots ? src_slots[i] : i of src, row d =
+ * dst_slots ? dst_slots[i] : i of dst) and every head: the rot_dim dims from
+ * rot_off on are rotated, pair by pair, the others copied. With (a, b) the pair
+ * j's dims (layout HS_ROPE_INTERLEAVED: 2 j and 2 j + 1 of the rotated part,
+ * HS_ROPE_HALF: j and j + rot_dim / 2) and
+ *   t = 2 pi * (positions[i] * freqs[j] / 2^64),
+ *   a' = factor * (a cos t - b sin t),   b' = factor * (b cos t + a sin t),
+ * computed in f32 and rounded once to the rows' type. freqs[j] is a pair's turns
+ * a position in units of 2^-64 (hs_rope_freqs), and the product wraps at whole
+ * turns: the angle is as exact at position 10^9 as at 1. Any int32 position.
+ * inverse != 0 rotates by -t: the gradient of the call (with factor 1 its
+ * inverse).
+ *   src, dst    bf16 or f32 (dtype HS_LOGITS_BF16 / HS_LOGITS_F32), element (row,
+ *               head, dim) at row * row_stride + head * head_stride + dim; device
+ *               memory or page-locked mapped host memory. src may be dst, with
+ *               the same strides and slots (in place: only the rotated dims are
+ *               touched); otherwise they do not overlap
+ *   src_slots, dst_slots  device int32 [n] or NULL. An entry with a negative slot
+ *               is skipped; a slot (or row) at or past src_rows / dst_rows is
+ *               skipped and sets HS_STATUS_INDEX in status. Destination rows are
+ *               distinct within a call; rows that no entry names stay as they were
+ *   positions   device int32 [n]
+ *   freqs       device int64 [rot_dim / 2]
+ *   status      device uint32 or NULL
+ * Requirements: n >= 0, 1 <= heads <= 65535, rot_dim even, 2 <= rot_dim, rot_off +
+ * rot_dim <= head_dim <= 65536, heads * head_dim <= 2^30, strides (in elements)
+ * in 0..2^40, no two rows or heads of dst overlapping, factor finite, arrays
+ * aligned to their elements. Any alignment and stride will do; where they allow
+ * 16-byte accesses those are used.
+ */
+int hs_rope_rows(const void *src, int64_t src_row_stride, int64_t src_head_stride, int64_t src_rows,
+                 void *dst, int64_t dst_row_stride, int64_t dst_head_stride, int64_t dst_rows,
+                 int32_t dtype, const int32_t *src_slots, const int32_t *dst_slots,
+                 const int32_t *positions, int32_t n, int32_t heads, int32_t head_dim,
+                 int32_t rot_off, int32_t rot_dim, int32_t layout, const int64_t *freqs,
+                 float factor, int32_t inverse, uint32_t *status, hs_stream_t stream);
+
+/*
+ * The frequencies of rot_dim dims, on the host: with w_j = base^(-2 j / rot_dim)
+ * radians a position,
+ *   HS_ROPE_PLAIN   w_j
+ *   HS_ROPE_LINEAR  w_j / scale (positions scaled down)
+ *   HS_ROPE_NTK     w_j of base * scale^(rot_dim / (rot_dim - 2)): the slowest
+ *                   pair scaled, the fastest as it was
+ *   HS_ROPE_YARN    w_j (1 - r_j) + w_j / scale * r_j, r_j rising from 0 to 1
+ *                   between the pairs that turn `fast` and `slow` times over
+ *                   `context` positions: low = floor(p(fast)), high = ceil(p(slow)),
+ *                   p(x) = rot_dim ln(context / (2 pi x)) / (2 ln base), within [0,
+ *                   rot_dim - 1], r_j = (j - low) / (high - low) within [0, 1];
+ *                   *factor is 0.1 ln(scale) + 1
+ * go to freqs[j] as round(w_j / (2 pi) * 2^64); *factor is 1 but for yarn.
+ *   freqs    host int64 [rot_dim / 2]
+ *   factor   host float
+ * scale >= 1 is not used by HS_ROPE_PLAIN, context > 0 and 0 < slow <= fast only by
+ * HS_ROPE_YARN. Requirements: rot_dim even, 2..65536 (4 or more for HS_ROPE_NTK),
+ * base > 1.
+ */
+int hs_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double scale, double context,
+                  double fast, double slow, int64_t *freqs, float *factor);
 
 /* ------------------------------------------------------------------------ */
 /* a2-a6 in one call: swap-in and attention of a decode step, with the host  */

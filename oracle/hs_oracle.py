@@ -697,6 +697,86 @@ def q8_values(rows) -> np.ndarray:
 
 
 # --------------------------------------------------------------------------
+# Latent rows in 4 bits
+# --------------------------------------------------------------------------
+
+Q4_ROW, Q4_GROUP = 416, 16
+E2M1_MAGS = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+Q4_SCALES = np.array([(8 + (b & 7)) * 2.0 ** ((b >> 3) - 19) for b in range(255)])
+
+
+def q4_quantise(x) -> np.ndarray:
+    """Latent rows [n][576] (float64 of bf16 or f32 values) -> uint8 [n][416].
+    Per group of 16 dims: the smallest scale whose 6-fold reaches the largest
+    magnitude (the last one where none does); byte 255 and zero codes where a
+    number is not finite."""
+    x = np.asarray(x, np.float64)
+    n = x.shape[0]
+    out = np.zeros((n, Q4_ROW), np.uint8)
+    v = x[:, :VALUE_DIM].reshape(n, -1, Q4_GROUP)
+    fine = np.isfinite(v).all(axis=2)
+    v = np.where(fine[:, :, None], v, 0.0)
+    byte = np.minimum(np.searchsorted(6.0 * Q4_SCALES, np.abs(v).max(axis=2), side="left"), 254)
+    a, s = np.abs(v), Q4_SCALES[byte][:, :, None]
+    code = np.zeros(v.shape, np.uint8)
+    for k in range(7):                             # past the middle of k and k + 1, or on it and k odd
+        mid = (E2M1_MAGS[k] + E2M1_MAGS[k + 1]) / 2 * s
+        code += (a > mid) | ((a == mid) & (k % 2 == 1))
+    code = np.where(np.signbit(v), code + 8, code).reshape(n, -1, 8)
+    for w in range(4):                             # byte w of a word: nibbles 2 w and 2 w + 1
+        dims = [[0, 2], [4, 6], [1, 3], [5, 7]][w]
+        out[:, w:VALUE_DIM // 2:4] = code[:, :, dims[0]] | (code[:, :, dims[1]] << 4)
+    out[:, VALUE_DIM // 2:384] = f64_to_bf16_bits(x[:, VALUE_DIM:]).view(np.uint8).reshape(n, -1)
+    out[:, 384:] = np.where(fine, byte, 255)
+    return out
+
+
+def q4_values(rows) -> np.ndarray:
+    """float64 values [n][576] of q4 rows."""
+    rows = np.ascontiguousarray(rows)
+    n = rows.shape[0]
+    word = np.ascontiguousarray(rows[:, :VALUE_DIM // 2]).view("<u4")
+    code = np.stack([(word >> (4 * (d // 2) + 16 * (d % 2))) & 15 for d in range(8)], axis=2).reshape(n, VALUE_DIM)
+    scale = np.append(Q4_SCALES, np.nan)[rows[:, 384:]]
+    v = np.where(code >= 8, -1.0, 1.0) * E2M1_MAGS[code & 7] * np.repeat(scale, Q4_GROUP, axis=1)
+    rope = bf16_bits_to_f64(np.ascontiguousarray(rows[:, VALUE_DIM // 2:384]).view(np.uint16))
+    return np.concatenate([v, rope], axis=1)
+
+
+# --------------------------------------------------------------------------
+# Rotary positions
+# --------------------------------------------------------------------------
+
+def rope_freqs(rot_dim, base=10000.0, scaling="plain", scale=1.0, context=0.0, fast=32.0, slow=1.0):
+    """(radians a position of each pair, factor), by the definition."""
+    w = base ** (-2.0 * np.arange(rot_dim // 2) / rot_dim)
+    if scaling == "linear":
+        return w / scale, 1.0
+    if scaling == "ntk":
+        return (base * scale ** (rot_dim / (rot_dim - 2))) ** (-2.0 * np.arange(rot_dim // 2) / rot_dim), 1.0
+    if scaling == "yarn":
+        p = lambda r: rot_dim * np.log(context / (2 * np.pi * r)) / (2 * np.log(base))
+        low, high = max(np.floor(p(fast)), 0), min(np.ceil(p(slow)), rot_dim - 1)
+        r = np.clip((np.arange(rot_dim // 2) - low) / max(high - low, 0.001), 0, 1)
+        return w * (1 - r) + w / scale * r, 0.1 * np.log(scale) + 1
+    return w, 1.0
+
+
+def rope_rows(x, positions, freqs, factor=1.0, rot_off=0, half=False, inverse=False) -> np.ndarray:
+    """float64 rows [n][heads][dims], a complex product per pair; freqs: whole
+    numbers, turns a position in units of 2^-64."""
+    y = np.array(x, np.float64)
+    r = len(freqs)
+    for j, f in enumerate(freqs):
+        a, b = (rot_off + j, rot_off + j + r) if half else (rot_off + 2 * j, rot_off + 2 * j + 1)
+        turn = [(int(p) * int(f)) % 2 ** 64 / 2.0 ** 64 for p in positions]
+        z = np.exp((-2j if inverse else 2j) * np.pi * np.array(turn))[:, None] * factor
+        v = (x[:, :, a] + 1j * x[:, :, b]) * z
+        y[:, :, a], y[:, :, b] = v.real, v.imag
+    return y
+
+
+# --------------------------------------------------------------------------
 # Verification by sampling, from given random numbers
 # --------------------------------------------------------------------------
 
