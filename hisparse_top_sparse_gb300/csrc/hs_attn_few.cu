@@ -62,11 +62,11 @@ struct Row<HS_ROWS_Q8> {
     code = *reinterpret_cast<const uint4 *>(row + 64 * warp + 16 * j);
     byte = row[Q8_SCALE_OFF + 2 * warp + (j >> 1)];
   }
+  using Scale = uint64_t;
+  __device__ __forceinline__ Scale scale() const { return q8_scale2(byte); }
   // dims 4 k .. 4 k + 3 of the 16
-  __device__ __forceinline__ void decode(uint2 (&d)[4]) const {
-    const uint64_t s = q8_scale2(byte);
-    d[0] = q8_decode4_bf16(code.x, s), d[1] = q8_decode4_bf16(code.y, s);
-    d[2] = q8_decode4_bf16(code.z, s), d[3] = q8_decode4_bf16(code.w, s);
+  __device__ __forceinline__ uint2 decode(int k, Scale s) const {
+    return q8_decode4_bf16(k == 0 ? code.x : k == 1 ? code.y : k == 2 ? code.z : code.w, s);
   }
   static __device__ __forceinline__ uint32_t rope(uint32_t pair) { return pair; }
 };
@@ -80,12 +80,12 @@ struct Row<HS_ROWS_Q4> {
     code = *reinterpret_cast<const uint2 *>(row + 32 * warp + 8 * j);
     byte = row[Q4_SCALE_OFF + 4 * warp + j];
   }
-  __device__ __forceinline__ void decode(uint2 (&d)[4]) const {
-    const uint32_t s = q4_scale2(byte);
-    d[0] = make_uint2(q4_decode2<0>(code.x, s), q4_decode2<1>(code.x, s));
-    d[1] = make_uint2(q4_decode2<2>(code.x, s), q4_decode2<3>(code.x, s));
-    d[2] = make_uint2(q4_decode2<0>(code.y, s), q4_decode2<1>(code.y, s));
-    d[3] = make_uint2(q4_decode2<2>(code.y, s), q4_decode2<3>(code.y, s));
+  using Scale = uint32_t;
+  __device__ __forceinline__ Scale scale() const { return q4_scale2(byte); }
+  __device__ __forceinline__ uint2 decode(int k, Scale s) const {
+    const uint32_t w = k < 2 ? code.x : code.y;
+    return k & 1 ? make_uint2(q4_decode2<2>(w, s), q4_decode2<3>(w, s))
+                 : make_uint2(q4_decode2<0>(w, s), q4_decode2<1>(w, s));
   }
   static __device__ __forceinline__ uint32_t rope(uint32_t pair) { return q4_mul(pair, Q4_DOWN2); }
 };
@@ -237,14 +237,14 @@ __global__ void __launch_bounds__(NT, 2) k_attn_few(const __grid_constant__ FewA
     for (int nt = 0; nt < 4; ++nt) row[nt].fetch(raw + (8 * nt + g) * ROW_STRIDE, warp, j);
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      uint2 d[4];
-      row[nt].decode(d);
+      const typename Row<F>::Scale sc = row[nt].scale();
       float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        kf[nt][k][0] = d[k].x;
-        kf[nt][k][1] = d[k].y;
-        mma(s, qa[k][0], qa[k][1], qa[k][2], qa[k][3], d[k].x, d[k].y);
+        const uint2 d = row[nt].decode(k, sc);
+        kf[nt][k][0] = d.x;
+        kf[nt][k][1] = d.y;
+        mma(s, qa[k][0], qa[k][1], qa[k][2], qa[k][3], d.x, d.y);
       }
       float *to = s_part + (warp * HEADS + g) * S_STRIDE + 8 * nt + 2 * j;
       *reinterpret_cast<float2 *>(to) = make_float2(s[0], s[1]);

@@ -45,22 +45,40 @@ __device__ __forceinline__ uint32_t q4_scale_byte(uint32_t amax) {
 }
 __device__ __forceinline__ float q4_scale(uint32_t byte) { return __uint_as_float((byte + Q4_BIAS) << 20); }
 
-// a / s of two values, correctly rounded, given the correctly rounded 1 / s: the
-// product's remainder, exact in an fma, corrects it (P. Markstein, Computation of
-// elementary functions on the IBM RISC System/6000 processor, 1990). Codes then
-// are what the exact quotients round to: a quotient lies on a middle between two
-// codes only if it is exactly that. (For the eight fractions of a scale and every
-// float this was checked against a division, on the host.)
-__device__ __forceinline__ float2 q4_over(float2 a, float s, float inv) {
-  const float x = a.x * inv, y = a.y * inv;
-  // (in this order of signs a zero keeps its own)
-  return make_float2(fmaf(-fmaf(s, x, -a.x), inv, x), fmaf(-fmaf(s, y, -a.y), inv, y));
+// Codes. A value's quotient by the scale has to fall on the right side of the
+// middles between codes, and on a middle exactly when it is there (a tie goes to
+// the even code); the product with a reciprocal is off by a unit or two. One step
+// of the product's remainder, which an fma gives exactly, mends it (P. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor,
+// 1990): the result's error before its rounding is the reciprocal's times the
+// correction, some 2^-45, where a middle is exact and any other quotient of a float
+// by a four-bit scale is further than half a unit from it. (Checked on the host
+// for the eight fractions, reciprocals off by up to two units, and the 20000 floats
+// on either side of every middle.)
+__device__ __forceinline__ float q4_reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(s));
+  return r;
+}
+__device__ __forceinline__ uint64_t q4_pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
 // Two values over the scale to two codes, the first in the low nibble: to nearest,
-// ties to even, saturated.
-__device__ __forceinline__ uint32_t q4_encode2(float lo, float hi, float s, float inv) {
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(q4_over(make_float2(lo, hi), s, inv), __NV_E2M1, cudaRoundNearest);
+// ties to even, saturated; with every sign the other way round (so that a zero's
+// comes out right: Q4_SIGNS).
+__device__ __forceinline__ uint32_t q4_encode2(float lo, float hi, uint64_t s, uint64_t minus_inv) {
+  const uint64_t a = q4_pair(lo, hi);
+  uint64_t b, e;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(b) : "l"(a), "l"(minus_inv));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(e) : "l"(s), "l"(b), "l"(a));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(b) : "l"(e), "l"(minus_inv), "l"(b));
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f.x), "=f"(f.y) : "l"(b));
+  return (uint32_t)__nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest);
 }
+constexpr uint32_t Q4_SIGNS = 0x88888888u;
 
 // Decoding, two codes at a time. The three bits of a magnitude, moved to where a
 // bf16 number has its last exponent bits and its first fraction bit, are the code

@@ -27,6 +27,25 @@ __device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// The bits of the largest magnitude of a scale group, this lane's 16 bytes and its
+// neighbours' (as whole numbers: infinities and NaNs come out on top).
+template <typename T>
+__device__ __forceinline__ uint32_t group_amax(const uint4 w) {
+  if constexpr (sizeof(T) == 2) {
+    constexpr uint32_t M = 0x7fff7fffu;           // both halves at once
+    uint32_t a = __vmaxs2(__vimax3_s16x2(w.x & M, w.y & M, w.z & M), w.w & M);
+#pragma unroll
+    for (int o = 1; o < Lay<T>::GL; o <<= 1) a = __vmaxs2(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return max(a << 16, a & 0xffff0000u);
+  } else {
+    constexpr uint32_t M = 0x7fffffffu;
+    uint32_t a = max(max(w.x & M, w.y & M), max(w.z & M, w.w & M));
+#pragma unroll
+    for (int o = 1; o < Lay<T>::GL; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(QT_THREADS, QT_BLOCKS) k_quant_rows_q4(
     const char *__restrict__ src, int64_t src_stride, int64_t src_rows, char *__restrict__ dst,
@@ -62,23 +81,19 @@ __global__ void __launch_bounds__(QT_THREADS, QT_BLOCKS) k_quant_rows_q4(
       for (int k = 0; k < L::PASSES; ++k) {
         float f[L::VEC];
         unpack<T>(w[u][k], f);
-        uint32_t amax = 0;                        // (as bits: infinities and NaNs come out on top)
-#pragma unroll
-        for (int j = 0; j < L::VEC; ++j) amax = max(amax, __float_as_uint(f[j]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = 1; o < L::GL; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const uint32_t byte = q4_scale_byte(amax);
-        const float s = q4_scale(byte), inv = __frcp_rn(s);
+        const uint32_t byte = q4_scale_byte(group_amax<T>(w[u][k]));
+        const float scale = q4_scale(byte), minus_inv = -q4_reciprocal(scale);
+        const uint64_t s = q4_pair(scale, scale), inv = q4_pair(minus_inv, minus_inv);
         // the word of eight dims: bytes (0, 2), (4, 6), (1, 3), (5, 7)
         if constexpr (L::VEC == 8) {
           const uint32_t c = q4_encode2(f[0], f[2], s, inv) | q4_encode2(f[4], f[6], s, inv) << 8 |
                              q4_encode2(f[1], f[3], s, inv) << 16 | q4_encode2(f[5], f[7], s, inv) << 24;
-          *reinterpret_cast<uint32_t *>(d[u] + (32 * k + lane) * 4) = c;
+          *reinterpret_cast<uint32_t *>(d[u] + (32 * k + lane) * 4) = c ^ Q4_SIGNS;
         } else {
           // half of it each in two neighbouring lanes
           uint32_t c = (q4_encode2(f[0], f[2], s, inv) | q4_encode2(f[1], f[3], s, inv) << 16) << (8 * (lane & 1));
           c |= __shfl_xor_sync(0xffffffffu, c, 1);
-          if (!(lane & 1)) *reinterpret_cast<uint32_t *>(d[u] + (32 * k + lane) * 2) = c;
+          if (!(lane & 1)) *reinterpret_cast<uint32_t *>(d[u] + (32 * k + lane) * 2) = c ^ Q4_SIGNS;
         }
         // the bytes of four neighbouring groups into one word
         uint32_t b = byte << (8 * ((lane / L::GL) & 3));

@@ -6,19 +6,28 @@
 // The angle of a pair at position p is p * w. In f32 an angle of 10^5 radians is
 // off by up to 0.004; in 64-bit whole fractions of a turn (w / 2 pi * 2^64, kept in
 // `freqs`) the product wraps as the angle does and is exact modulo a turn at any
-// position, for one integer multiplication a pair; its top 32 bits go to
-// sincospif.
+// position, for one integer multiplication a pair; the sine and the cosine are
+// taken of its top 32 bits.
 //
 // A thread takes one unit of a head: as many pairs as 16-byte accesses hold
 // (interleaved: 16 bytes; half: 16 bytes of each half), or 16 bytes of the dims
-// beside the rotated part, which it copies. It computes the unit's cosines and
-// sines once and applies them to every STEP-th head of its row.
+// beside the rotated part, which it copies. HBM bounds large calls, so a thread has
+// several loads in flight (src may be dst, and the compiler would keep each load behind
+// the store before it): of four heads of a row, whose cosines and sines it computes
+// once, or, where heads are few, of eight rows (the rotated units then a row each).
+
+#include <type_traits>
 
 #include "hs_internal.cuh"
 
 namespace {
 
 constexpr int RT = 256;               // threads of a block, at most
+// A thread has HEAD_BATCH heads of a row in flight, of at most HEADS, or copies
+// dims of ROW_BATCH rows. Measured (8192 rows x 128 heads x 64 dims; 65535 rows of
+// 576 dims; the floors are 39.5 and 22.3 us): at most 4 / 8 / 16 heads 53 / 46 / 47
+// us; 2 / 4 / 8 rows 36 / 29 / 26 us.
+constexpr int HEAD_BATCH = 4, HEADS = 8, ROW_BATCH = 8;
 
 struct RopeArgs {
   const char *src;
@@ -28,24 +37,33 @@ struct RopeArgs {
   const int32_t *src_slots, *dst_slots, *positions;
   const int64_t *freqs;
   uint32_t *status;
-  int32_t n, heads, step;             // a thread's heads are h, h + step, ...
+  int32_t n, heads, step;             // a thread's heads are h, h + step, ... (ROWS: h alone)
   int32_t half;                       // pairs of a head
   int32_t off;                        // bytes before the rotated part
-  int32_t rot_units, units;           // units of a head: rotated, and all
-  int32_t chunks, per_block;          // blocks of an entry, or (chunks 1) entries of a block
+  int32_t rot_units, copy_units;      // units of a head
+  // blocks of an entry (ROWS: of ROW_BATCH entries), and, where that is one, entries (or
+  // batches of them) of a block
+  int32_t chunks, per_block;
   float factor, sign;
 };
 
-// the elements of one access and their values
+// one access: 16 bytes, or one element
 template <typename T, bool VECTOR>
 struct Access {
-  static constexpr int N = VECTOR ? 16 / (int)sizeof(T) : 1;
-  static __device__ __forceinline__ void load(const char *p, float (&f)[N]) {
+  using Raw = typename std::conditional<VECTOR, uint4, T>::type;
+  static constexpr int BYTES = (int)sizeof(Raw), N = BYTES / (int)sizeof(T);
+  static __device__ __forceinline__ Raw load(const char *p) {
+    if constexpr (VECTOR)
+      return __ldcs(reinterpret_cast<const uint4 *>(p));
+    else
+      return *reinterpret_cast<const T *>(p);
+  }
+  static __device__ __forceinline__ void store(char *p, const Raw &v) { *reinterpret_cast<Raw *>(p) = v; }
+  static __device__ __forceinline__ void unpack(const Raw &v, float (&f)[N]) {
     if constexpr (!VECTOR) {
-      f[0] = (float)*reinterpret_cast<const T *>(p);
+      f[0] = (float)v;
     } else {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if constexpr (sizeof(T) == 4) {
@@ -57,9 +75,9 @@ struct Access {
       }
     }
   }
-  static __device__ __forceinline__ void store(char *p, const float (&f)[N]) {
+  static __device__ __forceinline__ Raw pack(const float (&f)[N]) {
     if constexpr (!VECTOR) {
-      *reinterpret_cast<T *>(p) = (T)f[0];
+      return (T)f[0];
     } else {
       uint32_t ws[4];
 #pragma unroll
@@ -71,110 +89,202 @@ struct Access {
           ws[k] = *reinterpret_cast<const uint32_t *>(&v);
         }
       }
-      *reinterpret_cast<uint4 *>(p) = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+      return make_uint4(ws[0], ws[1], ws[2], ws[3]);
     }
   }
 };
 
-template <typename T, bool HALF, bool VECTOR>
-__global__ void __launch_bounds__(RT) k_rope_rows(const __grid_constant__ RopeArgs a) {
+// Sine and cosine of a 32-bit fraction of a turn. The nearest quarter turn leaves
+// exactly, in whole numbers; what is left, at most pi / 4, goes through the Taylor
+// series (of 9th and 10th degree: cut off below 2^-29 and 2^-33), and the quarter
+// swaps and signs the two. Off by at most 2^-22: the angle's rounding to f32 and its
+// product with 2 pi 2^-32 (pi / 4 * 2^-23 together), and the series' roundings.
+__device__ __forceinline__ void sincos_turn(uint32_t turn, float &sine, float &cosine) {
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(turn - (quarter << 30)) * (6.283185307179586f * 0x1p-32f), y = x * x;
+  float s = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+  s = fmaf(y, s, 1.f / 120.f);
+  s = fmaf(y, s, -1.f / 6.f);
+  s = fmaf(x * y, s, x);
+  float c = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
+  c = fmaf(y, c, -1.f / 720.f);
+  c = fmaf(y, c, 1.f / 24.f);
+  c = fmaf(y, c, -0.5f);
+  c = fmaf(y, c, 1.f);
+  const bool odd = quarter & 1;
+  sine = __uint_as_float(__float_as_uint(odd ? c : s) ^ (quarter & 2) << 30);
+  cosine = __uint_as_float(__float_as_uint(odd ? s : c) ^ ((quarter + 1) & 2) << 30);
+}
+
+template <typename T, bool HALF, bool VECTOR, bool ROWS>
+__global__ void __launch_bounds__(RT, 3) k_rope_rows(const __grid_constant__ RopeArgs a) {
   using A = Access<T, VECTOR>;
+  using Raw = typename A::Raw;
   constexpr int N = A::N;
   constexpr bool TWO = HALF || !VECTOR;           // a unit's pairs lie in two accesses
   constexpr int PAIRS = TWO ? N : N / 2;
-  int64_t i;                                      // the entry
-  int w;                                          // this thread's place in it
-  const int width = a.units * a.step;
+  constexpr int BATCH = ROWS ? ROW_BATCH : HEAD_BATCH, SET = ROWS ? BATCH : 1;
+  // The rotated units of a block's entries come first, then, from the next warp on,
+  // the others: a warp with both would spend the cosines' time on the latter too.
+  int w = (int)threadIdx.x;
+  int64_t i = blockIdx.x;                         // the block's first entry
   if (a.chunks > 1) {
+    w += (int)(blockIdx.x % (unsigned)a.chunks) * RT;
     i = blockIdx.x / (unsigned)a.chunks;
-    w = (int)(blockIdx.x % (unsigned)a.chunks) * RT + (int)threadIdx.x;
-    if (w >= width) return;
-  } else {
-    const int e = (int)threadIdx.x / width;
-    i = (int64_t)blockIdx.x * a.per_block + e;
-    w = (int)threadIdx.x - e * width;
-    if (e >= a.per_block || i >= a.n) return;
   }
-  const int64_t s = a.src_slots ? a.src_slots[i] : i, d = a.dst_slots ? a.dst_slots[i] : i;
-  if (s >= a.src_rows || d >= a.dst_rows) {
-    if (a.status && w == 0) atomicOr(a.status, HS_STATUS_INDEX);
-    return;
+  i *= a.per_block * SET;
+  const int turning = a.rot_units * a.step * a.per_block * SET;
+  const bool rotated = w < turning;
+  if (!rotated) {
+    w -= (turning + 31) & ~31;
+    if (w < 0 || w >= a.copy_units * a.step * a.per_block) return;
   }
-  if (s < 0 || d < 0) return;
-  const int unit = w % a.units;
-  int h = w / a.units;
-  const char *src = a.src + s * a.src_row + (int64_t)h * a.src_head;
-  char *dst = a.dst + d * a.dst_row + (int64_t)h * a.dst_head;
-  const int64_t src_step = a.step * a.src_head, dst_step = a.step * a.dst_head;
-  if (unit < a.rot_units) {
-    const uint64_t p = (uint64_t)(int64_t)a.positions[i];
-    float c[PAIRS], sn[PAIRS];
-#pragma unroll
-    for (int k = 0; k < PAIRS; ++k) {
-      // the angle in half turns, within [-1, 1)
-      const uint64_t turn = p * (uint64_t)a.freqs[unit * PAIRS + k];
-      sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn[k], &c[k]);
-      c[k] *= a.factor;
-      sn[k] *= a.sign;
+  const int units = rotated ? a.rot_units : a.copy_units;
+  const int unit = w % units;
+  w /= units;
+  int h = w % a.step;                             // the (first) head
+  i += w / a.step;
+  auto slots = [&](int64_t e, int64_t &s, int64_t &d) {
+    s = d = -1;
+    if (e < a.n) {
+      s = a.src_slots ? a.src_slots[e] : e;
+      d = a.dst_slots ? a.dst_slots[e] : e;
     }
-    // the unit's first access, and its second
-    const int at = a.off + unit * (HALF ? N : 2 * PAIRS) * (int)sizeof(T);
+    if (s < a.src_rows && d < a.dst_rows) return true;
+    s = -1;
+    return false;
+  };
+  if (rotated) {
+    if (i >= a.n) return;
+    int64_t s, d;
+    if (!slots(i, s, d) && a.status && unit == 0 && h == 0) atomicOr(a.status, HS_STATUS_INDEX);
+    if (s < 0 || d < 0) return;
+    // the unit's first access, and (TWO) its second
+    const int at = a.off + unit * (HALF || !TWO ? 1 : 2) * A::BYTES;
     const int second = HALF ? a.half * (int)sizeof(T) : (int)sizeof(T);
-#pragma unroll 4
-    for (; h < a.heads; h += a.step, src += src_step, dst += dst_step) {
+    const char *p = a.src + s * a.src_row + (int64_t)h * a.src_head + at;
+    char *q = a.dst + d * a.dst_row + (int64_t)h * a.dst_head + at;
+    const int64_t src_step = a.step * a.src_head, dst_step = a.step * a.dst_head;
+    const uint64_t position = (uint64_t)(int64_t)a.positions[i];
+    float c[PAIRS], sn[PAIRS];
+    auto angles = [&]() {
+#pragma unroll
+      for (int k = 0; k < PAIRS; ++k) {
+        const uint64_t turn = position * (uint64_t)a.freqs[unit * PAIRS + k];
+        sincos_turn((uint32_t)(turn >> 32), sn[k], c[k]);
+        c[k] *= a.factor;
+        sn[k] *= a.sign;
+      }
+    };
+    auto turn = [&](Raw &x, Raw &y) {
       float f[N];
-      A::load(src + at, f);
+      A::unpack(x, f);
       if constexpr (TWO) {
         float g[N];
-        A::load(src + at + second, g);
+        A::unpack(y, g);
 #pragma unroll
         for (int k = 0; k < PAIRS; ++k) {
-          const float x = f[k], y = g[k];
-          f[k] = x * c[k] - y * sn[k];
-          g[k] = y * c[k] + x * sn[k];
+          const float u = f[k], v = g[k];
+          f[k] = u * c[k] - v * sn[k];
+          g[k] = v * c[k] + u * sn[k];
         }
-        A::store(dst + at, f);
-        A::store(dst + at + second, g);
+        y = A::pack(g);
       } else {
 #pragma unroll
         for (int k = 0; k < PAIRS; ++k) {
-          const float x = f[2 * k], y = f[2 * k + 1];
-          f[2 * k] = x * c[k] - y * sn[k];
-          f[2 * k + 1] = y * c[k] + x * sn[k];
+          const float u = f[2 * k], v = f[2 * k + 1];
+          f[2 * k] = u * c[k] - v * sn[k];
+          f[2 * k + 1] = v * c[k] + u * sn[k];
         }
-        A::store(dst + at, f);
+      }
+      x = A::pack(f);
+    };
+    if constexpr (ROWS) {
+      Raw x = A::load(p), y;
+      if (TWO) y = A::load(p + second);
+      angles();
+      turn(x, y);
+      if (TWO) A::store(q + second, y);
+      A::store(q, x);
+    } else {
+      bool fresh = true;
+      for (; h < a.heads; h += BATCH * a.step, p += BATCH * src_step, q += BATCH * dst_step) {
+        Raw x[BATCH], y[BATCH];
+#pragma unroll
+        for (int r = 0; r < BATCH; ++r)
+          if (h + r * a.step < a.heads) {
+            x[r] = A::load(p + r * src_step);
+            if (TWO) y[r] = A::load(p + r * src_step + second);
+          }
+        if (fresh) angles();                      // (while the first loads are on their way)
+        fresh = false;
+#pragma unroll
+        for (int r = 0; r < BATCH; ++r)
+          if (h + r * a.step < a.heads) {
+            turn(x[r], y[r]);
+            if (TWO) A::store(q + r * dst_step + second, y[r]);
+            A::store(q + r * dst_step, x[r]);
+          }
       }
     }
   } else {
-    // a unit beside the rotated part, moved as it is
-    const int bytes = VECTOR ? 16 : (int)sizeof(T);
-    int at = (unit - a.rot_units) * bytes;
+    // beside the rotated part, moved as it is
+    int at = unit * A::BYTES;
     if (at >= a.off) at += 2 * a.half * (int)sizeof(T);
-#pragma unroll 4
-    for (; h < a.heads; h += a.step, src += src_step, dst += dst_step) {
-      if constexpr (VECTOR)
-        *reinterpret_cast<uint4 *>(dst + at) = __ldcs(reinterpret_cast<const uint4 *>(src + at));
-      else
-        *reinterpret_cast<T *>(dst + at) = *reinterpret_cast<const T *>(src + at);
+    const char *p[BATCH];
+    char *q[BATCH];
+    Raw x[BATCH];
+    if constexpr (ROWS) {
+#pragma unroll
+      for (int r = 0; r < BATCH; ++r) {
+        int64_t s, d;
+        slots(i + (int64_t)r * a.per_block, s, d);
+        p[r] = s >= 0 && d >= 0 ? a.src + s * a.src_row + (int64_t)h * a.src_head + at : nullptr;
+        q[r] = a.dst + d * a.dst_row + (int64_t)h * a.dst_head + at;
+      }
+    } else {
+      int64_t s, d;
+      slots(i, s, d);
+      if (s < 0 || d < 0) return;
+      p[0] = a.src + s * a.src_row + at;
+      q[0] = a.dst + d * a.dst_row + at;
+    }
+    if constexpr (ROWS) {
+#pragma unroll
+      for (int r = 0; r < BATCH; ++r)
+        if (p[r]) x[r] = A::load(p[r]);
+#pragma unroll
+      for (int r = 0; r < BATCH; ++r)
+        if (p[r]) A::store(q[r], x[r]);
+    } else {
+      for (; h < a.heads; h += BATCH * a.step) {
+#pragma unroll
+        for (int r = 0; r < BATCH; ++r)
+          if (h + r * a.step < a.heads) x[r] = A::load(p[0] + (int64_t)(h + r * a.step) * a.src_head);
+#pragma unroll
+        for (int r = 0; r < BATCH; ++r)
+          if (h + r * a.step < a.heads) A::store(q[0] + (int64_t)(h + r * a.step) * a.dst_head, x[r]);
+      }
     }
   }
 }
 
-template <typename T>
-int launch(const RopeArgs &a, bool half, bool vector, unsigned blocks, int threads, cudaStream_t stream) {
-  if (half) {
-    if (vector)
-      k_rope_rows<T, true, true><<<blocks, threads, 0, stream>>>(a);
-    else
-      k_rope_rows<T, true, false><<<blocks, threads, 0, stream>>>(a);
-  } else {
-    if (vector)
-      k_rope_rows<T, false, true><<<blocks, threads, 0, stream>>>(a);
-    else
-      k_rope_rows<T, false, false><<<blocks, threads, 0, stream>>>(a);
-  }
+template <typename T, bool HALF, bool VECTOR>
+int launch(const RopeArgs &a, bool rows, unsigned blocks, int threads, cudaStream_t stream) {
+  if (rows)
+    k_rope_rows<T, HALF, VECTOR, true><<<blocks, threads, 0, stream>>>(a);
+  else
+    k_rope_rows<T, HALF, VECTOR, false><<<blocks, threads, 0, stream>>>(a);
   HS_LAUNCH_CHECK("k_rope_rows");
   return HS_OK;
+}
+template <typename T>
+int launch(const RopeArgs &a, bool half, bool vector, bool rows, unsigned blocks, int threads, cudaStream_t stream) {
+  if (half)
+    return vector ? launch<T, true, true>(a, rows, blocks, threads, stream)
+                  : launch<T, true, false>(a, rows, blocks, threads, stream);
+  return vector ? launch<T, false, true>(a, rows, blocks, threads, stream)
+                : launch<T, false, false>(a, rows, blocks, threads, stream);
 }
 
 }  // namespace
@@ -219,7 +329,11 @@ extern "C" int hs_rope_rows(const void *src, int64_t src_row_stride, int64_t src
     return hs_set_error(HS_ERR_INVALID_ARG, "arrays must be aligned to their elements");
   const void *s = nullptr, *d = nullptr;
   int rc = hs_device_alias(src, &s, "src", (int)elem);
-  if (rc || (rc = hs_device_alias(dst, &d, "dst", (int)elem))) return rc;
+  if (rc) return rc;
+  if (src == dst)
+    d = s;
+  else if ((rc = hs_device_alias(dst, &d, "dst", (int)elem)))
+    return rc;
 
   // In place nothing beside the rotated part moves.
   const bool same = s == d && src_row_stride == dst_row_stride && src_slots == dst_slots &&
@@ -252,23 +366,30 @@ extern "C" int hs_rope_rows(const void *src, int64_t src_row_stride, int64_t src
   const bool vector = parts % 16 == 0;
   const int per = vector ? (int)(16 / elem) : 1;
   a.rot_units = !vector || half ? a.half / per : rot_dim / per;
-  a.units = a.rot_units + (same ? 0 : (head_dim - rot_dim) / per);
-  // Heads of a thread: one while that leaves threads for every SM, up to eight
-  // (whose cosines and sines it then computes once).
+  a.copy_units = same ? 0 : (head_dim - rot_dim) / per;
+  // Units of a thread: one up to 256 threads an SM, then up to HEADS heads of a row
+  // or, where there are fewer heads than a batch, ROW_BATCH rows (with one unit up to
+  // 2048 threads an SM 8191 rows of 576 dims took 10.7 us, now 4.7, and 512 rows of
+  // 128 heads 9.1, now 4.5).
   int sms = 0;
   if ((rc = hs_sm_count(&sms))) return rc;
-  int64_t each = (int64_t)n * heads * a.units / ((int64_t)sms * 2048);
-  each = each < 1 ? 1 : each > 8 ? 8 : each;
-  a.step = (int32_t)((heads + each - 1) / each);
-  const int64_t width = (int64_t)a.units * a.step;
-  a.chunks = (int32_t)((width + RT - 1) / RT);
-  a.per_block = width <= RT ? (int32_t)(RT / width) : 1;
-  if (a.per_block > n) a.per_block = n;
-  const int threads = a.chunks > 1 ? RT : (int)((width * a.per_block + 31) / 32 * 32);
-  const int64_t blocks = a.chunks > 1 ? (int64_t)n * a.chunks : ((int64_t)n + a.per_block - 1) / a.per_block;
+  int64_t each = (int64_t)n * heads * (a.rot_units + a.copy_units) / ((int64_t)sms * 256);
+  each = each < 1 ? 1 : each > HEADS ? HEADS : each;
+  const bool rows = heads < HEAD_BATCH && each > 1;
+  a.step = rows ? heads : (int32_t)((heads + each - 1) / each);
+  const int set = rows ? ROW_BATCH : 1;
+  const auto threads_of = [&](int64_t sets) {
+    return (sets * set * a.rot_units * a.step + 31) / 32 * 32 + sets * a.copy_units * a.step;
+  };
+  const int64_t sets = ((int64_t)n + set - 1) / set;       // entries, or batches of them
+  a.chunks = (int32_t)((threads_of(1) + RT - 1) / RT);
+  a.per_block = 1;
+  while (a.chunks == 1 && a.per_block < sets && threads_of(a.per_block + 1) <= RT) ++a.per_block;
+  const int threads = a.chunks > 1 ? RT : (int)((threads_of(a.per_block) + 31) / 32 * 32);
+  const int64_t blocks = (sets + a.per_block - 1) / a.per_block * a.chunks;
   if (blocks > INT32_MAX) return hs_set_error(HS_ERR_UNSUPPORTED, "n * heads * head_dim too large");
-  return dtype == HS_LOGITS_F32 ? launch<float>(a, half, vector, (unsigned)blocks, threads, stream)
-                                : launch<__nv_bfloat16>(a, half, vector, (unsigned)blocks, threads, stream);
+  return dtype == HS_LOGITS_F32 ? launch<float>(a, half, vector, rows, (unsigned)blocks, threads, stream)
+                                : launch<__nv_bfloat16>(a, half, vector, rows, (unsigned)blocks, threads, stream);
 }
 
 extern "C" int hs_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double scale, double context,
