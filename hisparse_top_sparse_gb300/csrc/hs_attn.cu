@@ -127,26 +127,27 @@ constexpr int QS_OFF = 0;
 constexpr int QS_BYTES = QS_BLOCKS * HG * 128;              // 49152
 constexpr int RA_SLOT_BYTES = (D / 64 - VB_BLOCKS) * KV_BLOCK_BYTES;   // 20480
 constexpr int V_SLOT_BYTES = VB_BLOCKS * KV_BLOCK_BYTES;              // 16384
+constexpr int RAWO_BYTES = NK * HS_Q8_ROW_BYTES;            // 20992: a q8 tile's rows
+constexpr int RAWH_BYTES = NK * (DV / 2 + 16);              // 8704: half the codes, the exponents
 constexpr int P_SLOT_BYTES = HG * NK * 2;                   // 8192: 128 rows x 64 B, 64-byte swizzle
 constexpr int RA_OFF = QS_OFF + QS_BYTES;
 // Ring slots, and where everything lies. The q8 kernel's rows land in raw
 // rings first (its slots are taken only once a row is decoded, about a
 // microsecond later), which its rings A and VO make room for.
-// (q4 rows are smaller again, and a fourth VO slot fits.)
+// A q4 tile and a half are so small that both come straight into registers (18 KB
+// of loads in flight, a tile ahead), and with three VO slots the kernel's shared
+// memory leaves the L1 room for them.
 template <int F>
 struct Lay {
-  static constexpr bool RAW = F != HS_ROWS_BF16;
-  static constexpr int RA_SLOTS = RAW ? 2 : 3, VO_SLOTS = F == HS_ROWS_Q8 ? 3 : 4, VP_SLOTS = 2;
-  static constexpr int RAWO_BYTES = F == HS_ROWS_Q8 ? NK * HS_Q8_ROW_BYTES : NK * HS_Q4_ROW_BYTES;   // 20992, 13312: a tile's rows
-  static constexpr int RAWH_BYTES =                                    // 8704, 4608: half the codes, the scales
-      F == HS_ROWS_Q8 ? NK * (DV / 2 + DV / Q8_GROUP) : NK * (DV / 4 + DV / Q4_GROUP / 2);
+  static constexpr bool RAW = F != HS_ROWS_BF16, RINGS = F == HS_ROWS_Q8;     // decoded; through raw rings
+  static constexpr int RA_SLOTS = RAW ? 2 : 3, VO_SLOTS = RAW ? 3 : 4, VP_SLOTS = 2;
   static constexpr int VO_OFF = RA_OFF + RA_SLOTS * RA_SLOT_BYTES;
   static constexpr int XS_OFF = VO_OFF + VO_SLOTS * V_SLOT_BYTES;    // own P staged for the bulk copy
   static constexpr int XP_OFF = XS_OFF + XP_SLOTS * P_SLOT_BYTES;    // the peer's P
   static constexpr int VP_OFF = XP_OFF + XP_SLOTS * P_SLOT_BYTES;
   static constexpr int RAWO_OFF = VP_OFF + VP_SLOTS * V_SLOT_BYTES;  // raw rows of own tiles
-  static constexpr int RAWH_OFF = RAWO_OFF + (RAW ? RAWO_SLOTS * RAWO_BYTES : 0);   // raw halves
-  static constexpr int XMAX_OFF = RAWH_OFF + (RAW ? RAWH_SLOTS * RAWH_BYTES : 0);   // peer's first-tile maxima
+  static constexpr int RAWH_OFF = RAWO_OFF + (RINGS ? RAWO_SLOTS * RAWO_BYTES : 0);   // raw halves
+  static constexpr int XMAX_OFF = RAWH_OFF + (RINGS ? RAWH_SLOTS * RAWH_BYTES : 0);   // peer's first-tile maxima
   static constexpr int XEND_OFF = XMAX_OFF + HG * 4;                 // peer's (l or mark, max) per pass
   static constexpr int BAR_OFF = XEND_OFF + 2 * HG * 8;
   static constexpr int SMEM_USED = BAR_OFF + 512;
@@ -172,8 +173,9 @@ struct Lay {
     a -= VO_SLOTS - 1;
     if (a < XP_SLOTS) return XS_OFF + a * BLK;
     a -= XP_SLOTS;
-    if (a < VP_SLOTS - 1) return VP_OFF + (a + 1) * BLK;
-    a -= VP_SLOTS - 1;
+    constexpr int in_vp = F == HS_ROWS_Q4 ? VP_SLOTS : VP_SLOTS - 1;
+    if (a < in_vp) return VP_OFF + (VP_SLOTS - in_vp + a) * BLK;
+    a -= in_vp;
     return RAWO_OFF + a * BLK;
   }
   static_assert(q_stage_off(0) % 1024 == 0 && q_stage_off(1) % 1024 == 0 && q_stage_off(2) % 1024 == 0 &&
@@ -376,11 +378,6 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t src) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(src) : "memory");
-  return v;
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -525,11 +522,11 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity)
 
 // ---- how a tile's quantised rows come in -------------------------------------
 // OwnRow<F>: the chunks of one key of an own tile that one of its eight threads
-// copies and decodes; HalfRow<F>: those of a value half of a peer tile's key, for
+// brings in and decodes; HalfRow<F>: those of a value half of a peer tile's key, for
 // one of its four threads. key(), sub(): which of a warp's keys and threads a
-// lane is. copy() takes a row's chunks by cp.async to the thread's places of a raw
-// slot (p: the thread's number), fetch() reads them from there, load() straight
-// from memory, put() decodes them into the slots' swizzled 64-dim blocks.
+// lane is. load() reads a row's chunks, put() decodes them into the slots' swizzled
+// 64-dim blocks; copy() takes them by cp.async to the thread's places of a raw slot
+// (p: the thread's number), fetch() reads them from there.
 __host__ __device__ constexpr int row_bytes(int f) { return f == HS_ROWS_Q8 ? HS_Q8_ROW_BYTES : HS_Q4_ROW_BYTES; }
 
 template <int F>
@@ -643,12 +640,6 @@ struct OwnRow<HS_ROWS_Q4> {
   static __device__ __forceinline__ int key(int lw, int lane) { return 4 * lw + (lane & 3); }
   static __device__ __forceinline__ int sub(int lane) { return lane >> 2; }
   static __device__ __forceinline__ int rope_chunk(int sub) { return 4 * (sub & 1) + (sub >> 1); }
-  static __device__ __forceinline__ void copy(uint32_t to, const char *row, bool v, int p, int key, int sub) {
-    cp_async16(to + p * 16, row + sub * 16, v);
-    cp_async16(to + (NPROD + p) * 16, row + 128 + sub * 16, v);
-    cp_async16(to + (2 * NPROD + p) * 16, row + Q4_ROPE_OFF + rope_chunk(sub) * 16, v);
-    if (sub < 2) cp_async16(to + 3 * NPROD * 16 + key * 32 + sub * 16, row + Q4_SCALE_OFF + sub * 16, v);
-  }
   __device__ __forceinline__ void load(const char *row, bool v, int sub) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
     code[0] = v ? ld_global16(row + sub * 16) : zero;
@@ -656,13 +647,6 @@ struct OwnRow<HS_ROWS_Q4> {
     rope = v ? ld_global16(row + Q4_ROPE_OFF + rope_chunk(sub) * 16) : zero;
     scale[0] = v ? ld_global_u16(row + Q4_SCALE_OFF + 2 * sub) : 0u;
     scale[1] = v ? ld_global_u16(row + Q4_SCALE_OFF + 16 + 2 * sub) : 0u;
-  }
-  __device__ __forceinline__ void fetch(uint32_t from, int p, int key, int sub) {
-    code[0] = ld_shared16(from + p * 16);
-    code[1] = ld_shared16(from + (NPROD + p) * 16);
-    rope = ld_shared16(from + (2 * NPROD + p) * 16);
-    scale[0] = ld_shared_u16(from + 3 * NPROD * 16 + key * 32 + 2 * sub);
-    scale[1] = ld_shared_u16(from + 3 * NPROD * 16 + key * 32 + 16 + 2 * sub);
   }
   __device__ __forceinline__ void put(uint32_t ra, uint32_t rv, int c, int key, int sub) {
     const uint32_t at = (uint32_t)(sub >> 1) * KV_BLOCK_BYTES;
@@ -682,16 +666,12 @@ struct HalfRow<HS_ROWS_Q4> {
   uint32_t scale[2];
   static __device__ __forceinline__ int key(int lw, int lane) { return 8 * lw + (lane & 7); }
   static __device__ __forceinline__ int sub(int lane) { return lane >> 3; }
-  static __device__ __forceinline__ void copy(uint32_t to, const char *row, bool v, int c, int p, int key, int sub) {
-    cp_async16(to + p * 16, row + 128 * c + sub * 16, v);
-    cp_async16(to + (RAW_HALF + p) * 16, row + 128 * c + 64 + sub * 16, v);
-    if (sub == 0) cp_async16(to + 2 * RAW_HALF * 16 + key * 16, row + Q4_SCALE_OFF + 16 * c, v);
-  }
-  __device__ __forceinline__ void fetch(uint32_t from, int p, int key, int sub) {
-    code[0] = ld_shared16(from + p * 16);
-    code[1] = ld_shared16(from + (RAW_HALF + p) * 16);
-    scale[0] = ld_shared_u16(from + 2 * RAW_HALF * 16 + key * 16 + 2 * sub);
-    scale[1] = ld_shared_u16(from + 2 * RAW_HALF * 16 + key * 16 + 8 + 2 * sub);
+  __device__ __forceinline__ void load(const char *row, bool v, int c, int sub) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    code[0] = v ? ld_global16(row + 128 * c + sub * 16) : zero;
+    code[1] = v ? ld_global16(row + 128 * c + 64 + sub * 16) : zero;
+    scale[0] = v ? ld_global_u16(row + Q4_SCALE_OFF + 16 * c + 2 * sub) : 0u;
+    scale[1] = v ? ld_global_u16(row + Q4_SCALE_OFF + 16 * c + 8 + 2 * sub) : 0u;
   }
   __device__ __forceinline__ void put(uint32_t slot, int c, int key, int sub) {
     const uint32_t at = slot + (uint32_t)(sub >> 1) * KV_BLOCK_BYTES;
@@ -857,15 +837,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
   if ((warp >= 4 && warp < 12) || (RAW && warp > 12 + NSB)) {
     if constexpr (RAW) {
       // ------------------- gather producers, quantised rows made bf16 tiles ----
-      // Rows land in raw rings (cp.async), are read into registers, their places
-      // refilled at once, and decoded into a slot when it is free. (Loads
-      // straight into registers cannot run ahead: the L1 beside this kernel's
-      // shared memory holds only some 20 KB of loads in flight.) Warps 4-11 take
-      // the own tiles, eight threads per key, warps 15-18 the peer tiles' halves,
-      // four threads per key, so that neither waits behind the other's slots.
-      // A thread copies and decodes the same 16-byte chunks, in places of its
-      // own; the scales are copied by one or two threads of a key and read by all,
-      // which are of one warp.
+      // Warps 4-11 take the own tiles, eight threads per key, warps 15-18 the
+      // peer tiles' halves, four threads per key, so that neither waits behind
+      // the other's slots. A thread takes the same 16-byte chunks of every key.
       const bool own = warp < 12;
       const int lw = own ? warp - 4 : warp - 15;
       const int p = 32 * lw + lane;
@@ -875,104 +849,144 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
         const int j = t * NK + key;
         return (t < T && j < K) ? ld_global(idx_row + j) : -1;
       };
+      // (where the index names no row nothing is read: q stands for its address)
+      auto row_at = [&](int32_t id) { return id >= 0 && id < n_kv ? kv + (int64_t)id * row_bytes(F) : q; };
+      auto has_row = [&](int32_t id) { return id >= 0 && id < n_kv; };
+      // the next pass is run (pass 0: always)
+      auto begins = [&](int pass) -> bool {
+        if (pass == 0) return true;
+        if (!warp_wait(bar(B_DECIDE), 0)) timed_out = true;
+        return !timed_out && *s_redo;
+      };
       if (own) {
-        const uint32_t raw = sbase + L::RAWO_OFF;
-        auto copy = [&](int32_t id, int slot) {
-          // (a copy of no bytes where the index names no row: q stands for its address)
-          const bool v = id >= 0 && id < n_kv;
-          OwnRow<F>::copy(raw + slot * L::RAWO_BYTES, v ? kv + (int64_t)id * row_bytes(F) : q, v, p, key, sub);
-          cp_async_commit();
-        };
         int ig = 0;                      // own tiles taken, over both passes
         int sa = 0, so = 0;              // their slots; parities of the releases waited for
         uint32_t pa = 1, po = 1;         // (flipped to 0 before the first wait)
-        for (int pass = 0; pass < 2 && !timed_out; ++pass) {
+        // decodes a tile into its slots, once they are free
+        auto deliver = [&](OwnRow<F> &row) -> bool {
+          if ((ig >= L::RA_SLOTS && !warp_wait(bar(B_EMPTYA + sa), pa)) ||
+              (ig >= L::VO_SLOTS && !warp_wait(bar(B_EMPTYVO + so), po))) {
+            timed_out = true;
+            return false;
+          }
+          row.put(sbase + RA_OFF + sa * RA_SLOT_BYTES, sbase + L::VO_OFF + so * V_SLOT_BYTES, c, key, sub);
+          fence_proxy_async();
+          bar_arrive(bar(B_FULLA + sa));
+          // the next tile's slots, and the parity of their next release
+          if (++sa == L::RA_SLOTS) { sa = 0; pa ^= 1; }
+          if (++so == L::VO_SLOTS) { so = 0; po ^= 1; }
+          ++ig;
+          return true;
+        };
+        for (int pass = 0; pass < 2 && begins(pass); ++pass) {
           OwnRow<F> row;
-          int copied = 0;
-          if (pass == 0) {
-            // the first own tile comes straight into registers: the raw ring
-            // (of q8 rows) holds staged Q until it is in TMEM
-            const int32_t id = load_id(c);
-            const bool v = id >= 0 && id < n_kv;
-            row.load(v ? kv + (int64_t)id * row_bytes(F) : q, v, sub);
-            copied = 1;
-          } else {
-            if (!warp_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
-            if (!*s_redo) break;
-          }
-          int32_t id = load_id(2 * copied + c);
-          auto next = [&]() {            // past the last tile: a copy of zeros that nothing reads
-            copy(id, copied % RAWO_SLOTS);
-            ++copied;
-            id = load_id(2 * copied + c);
-          };
-          if (pass == 1)
-            for (int k = 0; k < RAWO_SLOTS; ++k) next();
-          for (int a = 0; a < n_own; ++a, ++ig) {
-            if (pass == 1 || a > 0) {
-              if (pass == 0 && a == 1) { // the raw ring and the other slots, once Q has left them
-                if (!warp_wait(bar(B_QSTAGED), 0)) { timed_out = true; break; }
-                for (int k = 0; k < RAWO_SLOTS; ++k) next();
+          int32_t id = load_id(c);
+          if constexpr (L::RINGS) {
+            // Rows land in raw rings (cp.async), are read into registers, their
+            // places refilled at once. (Loads straight into registers cannot run
+            // ahead: the L1 beside this kernel's shared memory holds only some
+            // 20 KB of loads in flight.) The scales are copied by a key's first
+            // thread and read by all, which are of one warp.
+            const uint32_t raw = sbase + L::RAWO_OFF;
+            int copied = 0;
+            auto next = [&]() {          // past the last tile: a copy of zeros that nothing reads
+              OwnRow<F>::copy(raw + (copied % RAWO_SLOTS) * RAWO_BYTES, row_at(id), has_row(id), p, key, sub);
+              cp_async_commit();
+              ++copied;
+              id = load_id(2 * copied + c);
+            };
+            if (pass == 0) {
+              // the first own tile comes straight into registers: the raw ring
+              // holds staged Q until it is in TMEM
+              row.load(row_at(id), has_row(id), sub);
+              copied = 1;
+              id = load_id(2 + c);
+            } else {
+              for (int k = 0; k < RAWO_SLOTS; ++k) next();
+            }
+            for (int a = 0; a < n_own; ++a) {
+              if (pass == 1 || a > 0) {
+                if (pass == 0 && a == 1) {   // the raw ring and the other slots, once Q has left them
+                  if (!warp_wait(bar(B_QSTAGED), 0)) { timed_out = true; break; }
+                  for (int k = 0; k < RAWO_SLOTS; ++k) next();
+                }
+                cp_async_wait<RAWO_SLOTS - 1>();
+                __syncwarp();
+                row.fetch(raw + (a % RAWO_SLOTS) * RAWO_BYTES, p, key, sub);
+                __syncwarp();
+                next();
               }
-              cp_async_wait<RAWO_SLOTS - 1>();
-              __syncwarp();
-              row.fetch(raw + (a % RAWO_SLOTS) * L::RAWO_BYTES, p, key, sub);
-              __syncwarp();
-              next();
+              if (!deliver(row)) break;
             }
-            if ((ig >= L::RA_SLOTS && !warp_wait(bar(B_EMPTYA + sa), pa)) ||
-                (ig >= L::VO_SLOTS && !warp_wait(bar(B_EMPTYVO + so), po))) {
-              timed_out = true;
-              break;
+            cp_async_wait<0>();
+          } else {
+            // straight into registers, a tile ahead
+            OwnRow<F> ahead;
+            auto next = [&](int a) {
+              ahead.load(row_at(id), has_row(id), sub);
+              id = load_id(2 * (a + 1) + c);
+            };
+            next(0);
+            for (int a = 0; a < n_own; ++a) {
+              row = ahead;
+              next(a + 1);
+              // the slots behind the first ones, once Q has left them
+              if (pass == 0 && a == 1 && !warp_wait(bar(B_QSTAGED), 0)) { timed_out = true; break; }
+              if (!deliver(row)) break;
             }
-            row.put(sbase + RA_OFF + sa * RA_SLOT_BYTES, sbase + L::VO_OFF + so * V_SLOT_BYTES, c, key, sub);
-            fence_proxy_async();
-            bar_arrive(bar(B_FULLA + sa));
-            // the next tile's slots, and the parity of their next release
-            if (++sa == L::RA_SLOTS) { sa = 0; pa ^= 1; }
-            if (++so == L::VO_SLOTS) { so = 0; po ^= 1; }
           }
-          cp_async_wait<0>();
         }
       } else {
-        const uint32_t raw = sbase + L::RAWH_OFF;
-        auto copy = [&](int32_t id, int slot) {
-          const bool v = id >= 0 && id < n_kv;
-          HalfRow<F>::copy(raw + slot * L::RAWH_BYTES, v ? kv + (int64_t)id * row_bytes(F) : q, v, c, p, key, sub);
-          cp_async_commit();
-        };
         int jg = 0;                      // peer tiles taken, over both passes
+        auto deliver = [&](HalfRow<F> &row) -> bool {
+          const int sp = jg % L::VP_SLOTS;
+          if (jg >= L::VP_SLOTS && !warp_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
+            timed_out = true;
+            return false;
+          }
+          row.put(sbase + L::VP_OFF + sp * V_SLOT_BYTES, c, key, sub);
+          fence_proxy_async();
+          bar_arrive(bar(B_FULLVP + sp));
+          ++jg;
+          return true;
+        };
+        // (staged Q may lie where the first halves go)
         if (!warp_wait(bar(B_QSTAGED), 0)) timed_out = true;
-        for (int pass = 0; pass < 2 && !timed_out; ++pass) {
-          if (pass == 1) {
-            if (!warp_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
-            if (!*s_redo) break;
-          }
-          int copied = 0;
+        for (int pass = 0; pass < 2 && !timed_out && begins(pass); ++pass) {
+          HalfRow<F> row;
           int32_t id = load_id(1 - c);
-          auto next = [&]() {
-            copy(id, copied % RAWH_SLOTS);
-            ++copied;
-            id = load_id(2 * copied + 1 - c);
-          };
-          for (int k = 0; k < RAWH_SLOTS; ++k) next();
-          for (int b = 0; b < n_peer; ++b, ++jg) {
-            cp_async_wait<RAWH_SLOTS - 1>();
-            __syncwarp();
-            HalfRow<F> row;
-            row.fetch(raw + (b % RAWH_SLOTS) * L::RAWH_BYTES, p, key, sub);
-            __syncwarp();
-            next();
-            const int sp = jg % L::VP_SLOTS;
-            if (jg >= L::VP_SLOTS && !warp_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
-              timed_out = true;
-              break;
+          if constexpr (L::RINGS) {
+            const uint32_t raw = sbase + L::RAWH_OFF;
+            int copied = 0;
+            auto next = [&]() {
+              HalfRow<F>::copy(raw + (copied % RAWH_SLOTS) * RAWH_BYTES, row_at(id), has_row(id), c, p, key, sub);
+              cp_async_commit();
+              ++copied;
+              id = load_id(2 * copied + 1 - c);
+            };
+            for (int k = 0; k < RAWH_SLOTS; ++k) next();
+            for (int b = 0; b < n_peer; ++b) {
+              cp_async_wait<RAWH_SLOTS - 1>();
+              __syncwarp();
+              row.fetch(raw + (b % RAWH_SLOTS) * RAWH_BYTES, p, key, sub);
+              __syncwarp();
+              next();
+              if (!deliver(row)) break;
             }
-            row.put(sbase + L::VP_OFF + sp * V_SLOT_BYTES, c, key, sub);
-            fence_proxy_async();
-            bar_arrive(bar(B_FULLVP + sp));
+            cp_async_wait<0>();
+          } else {
+            HalfRow<F> ahead;
+            auto next = [&](int b) {
+              ahead.load(row_at(id), has_row(id), c, sub);
+              id = load_id(2 * (b + 1) + 1 - c);
+            };
+            next(0);
+            for (int b = 0; b < n_peer; ++b) {
+              row = ahead;
+              next(b + 1);
+              if (!deliver(row)) break;
+            }
           }
-          cp_async_wait<0>();
         }
       }
     } else {

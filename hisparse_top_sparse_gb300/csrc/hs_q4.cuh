@@ -95,12 +95,13 @@ __device__ __forceinline__ uint32_t q4_scale2(uint32_t byte) {
   const uint32_t s = byte == Q4_BYTE_NAN ? 0x7fc0u : (byte << 4) + ((127 - 16 + 126 - Q4_SHIFT) << 7);
   return s * 0x10001u;
 }
-// dims 2 I and 2 I + 1 of a word's eight
+// dims 2 I and 2 I + 1 of a word's eight: one product with a sum of two powers of two
+// brings a nibble's sign and its magnitude where they belong at once
 template <int I>
 __device__ __forceinline__ uint32_t q4_decode2(uint32_t word, uint32_t scale2) {
-  const uint32_t sign = I < 3 ? word << (12 - 4 * I) : word;
-  const uint32_t mag = I < 2 ? word << (6 - 4 * I) : word >> (4 * I - 6);
-  return q4_mul((sign & 0x80008000u) | (mag & 0x01c001c0u), scale2);
+  const uint32_t w = I < 2 ? word : word >> 8;
+  const uint32_t n = I & 1 ? (w & 0x00f000f0u) * 0x104u : (w & 0x000f000fu) * 0x1040u;
+  return q4_mul(n & 0x81c081c0u, scale2);
 }
 // 2^15 and 2^-15 in both halves
 constexpr uint32_t Q4_UP2 = ((127 + Q4_SHIFT) << 7) * 0x10001u, Q4_DOWN2 = ((127 - Q4_SHIFT) << 7) * 0x10001u;
