@@ -734,11 +734,11 @@ def _heads(t, name, cur):
     if t.dtype not in _WIDE:
         raise TypeError(f"{name} must be float32 or bfloat16")
     s, st = t.shape, t.stride()
-    if len(s) not in (2, 3) or (s[-1] > 1 and st[-1] != 1):
-        raise ValueError(f"{name} must be [rows][heads][dims] or [rows][dims], dims contiguous")
-    if len(s) == 2:
+    if len(s) == 3 and (st[2] == 1 or s[2] <= 1):
+        return t.data_ptr(), s[0], st[0], s[1], st[1], s[2]
+    if len(s) == 2 and (st[1] == 1 or s[1] <= 1):
         return t.data_ptr(), s[0], st[0], 1, 0, s[1]
-    return t.data_ptr(), s[0], st[0], s[1], st[1], s[2]
+    raise ValueError(f"{name} must be [rows][heads][dims] or [rows][dims], dims contiguous")
 
 
 def hs_rope_rows(src, dst, positions, freqs, factor: float = 1.0, rot_off: int = 0,
@@ -755,27 +755,25 @@ def hs_rope_rows(src, dst, positions, freqs, factor: float = 1.0, rot_off: int =
     if dst.dtype is not src.dtype or dst_heads != heads or dst_dims != dims:
         raise ValueError("src and dst must have one dtype, as many heads and as many dims")
     pp, n = _slot_list(positions, "positions", cur)
-    if src_slots is None and dst_slots is None and n != src_rows:
-        raise ValueError(f"{n} positions for {src_rows} rows")
     ss = ds = None
-    for name, t, rows in (("src_slots", src_slots, src_rows), ("dst_slots", dst_slots, dst_rows)):
-        if t is None:
-            if n > rows:
-                raise ValueError(f"{n} entries do not fit {rows} rows")
-            continue
-        p, m = _slot_list(t, name, cur)
+    if src_slots is not None:
+        ss, m = _slot_list(src_slots, "src_slots", cur)
         if m != n:
-            raise ValueError(f"{name} must have an entry for each of the {n} positions")
-        if name == "src_slots":
-            ss = p
-        else:
-            ds = p
-    if freqs.dim() != 1:
+            raise ValueError(f"src_slots must have an entry for each of the {n} positions")
+    elif n > src_rows or (dst_slots is None and n < src_rows):
+        raise ValueError(f"{n} positions for {src_rows} rows")
+    if dst_slots is not None:
+        ds, m = _slot_list(dst_slots, "dst_slots", cur)
+        if m != n:
+            raise ValueError(f"dst_slots must have an entry for each of the {n} positions")
+    elif n > dst_rows:
+        raise ValueError(f"{n} entries do not fit {dst_rows} rows")
+    fp, pairs = _on(freqs, "freqs", torch.int64, None, cur), freqs.shape
+    if len(pairs) != 1:
         raise ValueError("freqs must be int64 [pairs]")
     _check(lib().hs_rope_rows(
         sp, src_row, src_head, src_rows, dp, dst_row, dst_head, dst_rows, _WIDE[src.dtype], ss, ds,
-        pp, n, heads, dims, int(rot_off), 2 * freqs.shape[0], int(layout),
-        _on(freqs, "freqs", torch.int64, None, cur), float(factor), int(bool(inverse)),
+        pp, n, heads, dims, rot_off, 2 * pairs[0], layout, fp, factor, 1 if inverse else 0,
         None if status is None else _on(status, "status", torch.int32, (1,), cur),
         _on_stream(stream, cur)), "hs_rope_rows")
 
