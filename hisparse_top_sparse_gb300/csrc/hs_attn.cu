@@ -834,7 +834,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
   if (!req_ok && status && tid == 0 && c == 0) atomicOr(status, HS_STATUS_INDEX);
 
 
-  if ((warp >= 4 && warp < 12) || (RAW && warp > 12 + NSB)) {
+  if (RAW && ((warp >= 4 && warp < 12) || warp > 12 + NSB)) {
     if constexpr (RAW) {
       // ------------------- gather producers, quantised rows made bf16 tiles ----
       // Warps 4-11 take the own tiles, eight threads per key, warps 15-18 the
@@ -989,89 +989,89 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
           }
         }
       }
-    } else {
-      // ------------------------------------------------ gather producers ----
-      const int p = tid - 128;          // 0..255
-      const int key = p >> 3;           // 32 keys per tile, 8 threads per key
-      const int sub = p & 7;            // chunk sub of every 64-dim block
-      auto load_id = [&](int t) -> int32_t {
-        const int j = t * NK + key;
-        return (t < T && j < K) ? ld_global(idx_row + j) : -1;
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------ gather producers ----
+    const int p = tid - 128;          // 0..255
+    const int key = p >> 3;           // 32 keys per tile, 8 threads per key
+    const int sub = p & 7;            // chunk sub of every 64-dim block
+    auto load_id = [&](int t) -> int32_t {
+      const int j = t * NK + key;
+      return (t < T && j < K) ? ld_global(idx_row + j) : -1;
+    };
+    int ig = 0, jg = 0;               // own / peer tiles issued, over both passes
+    for (int pass = 0; pass < 2 && !timed_out; ++pass) {
+      if (pass == 1) {
+        if (!bar_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
+        if (!*s_redo) break;
+      }
+      // gather order: the own tiles run up to PEER_LAG + 1 ahead of the
+      // peer tiles, whose value halves are read only once the peer's P has
+      // come, so that a ring VP slot is taken only shortly before its use
+      int na = 0, nb = 0;             // own / peer tiles of this pass taken
+      int la = 0, lb = 0;             // the same two steps ahead (index prefetch)
+      auto step = [&](int &a, int &b) -> int {
+        if (a < n_own && (b >= n_peer || a < b + PEER_LAG + 1)) return 2 * (a++) + c;
+        if (b < n_peer) return 2 * (b++) + (1 - c);
+        return T;
       };
-      int ig = 0, jg = 0;               // own / peer tiles issued, over both passes
-      for (int pass = 0; pass < 2 && !timed_out; ++pass) {
-        if (pass == 1) {
-          if (!bar_wait(bar(B_DECIDE), 0)) { timed_out = true; break; }
-          if (!*s_redo) break;
-        }
-        // gather order: the own tiles run up to PEER_LAG + 1 ahead of the
-        // peer tiles, whose value halves are read only once the peer's P has
-        // come, so that a ring VP slot is taken only shortly before its use
-        int na = 0, nb = 0;             // own / peer tiles of this pass taken
-        int la = 0, lb = 0;             // the same two steps ahead (index prefetch)
-        auto step = [&](int &a, int &b) -> int {
-          if (a < n_own && (b >= n_peer || a < b + PEER_LAG + 1)) return 2 * (a++) + c;
-          if (b < n_peer) return 2 * (b++) + (1 - c);
-          return T;
-        };
-        const int t0 = step(la, lb);
-        const int t1 = step(la, lb);
-        int32_t id0 = load_id(t0), id1 = load_id(t1);
-        for (int i = 0; i < T; ++i) {
-          const int t = step(na, nb);
-          const int32_t id = id0;
-          id0 = id1;
-          id1 = load_id(step(la, lb));
-          const bool v = id >= 0 && id < n_kv;
-          const char *src = kv + (v ? (int64_t)id * ROWB : 0);
-          if ((t & 1) == c) {
-            const int sa = ig % L::RA_SLOTS, so = ig % L::VO_SLOTS;
-            // slots 1 and 2 hold staged Q until it is in TMEM
-            if (ig == 1 && !bar_wait(bar(B_QSTAGED), 0)) {
-              timed_out = true;
-              break;
-            }
-            if (ig >= L::RA_SLOTS && !bar_wait(bar(B_EMPTYA + sa), ((ig / L::RA_SLOTS) - 1) & 1)) {
-              timed_out = true;
-              break;
-            }
-            if (ig >= L::VO_SLOTS && !bar_wait(bar(B_EMPTYVO + so), ((ig / L::VO_SLOTS) - 1) & 1)) {
-              timed_out = true;
-              break;
-            }
-            const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
-            const uint32_t rv = sbase + L::VO_OFF + so * V_SLOT_BYTES;
-            // copy k of this thread is chunk sub + 4k: swizzle block k / 2,
-            // chunk sub + 4 (k & 1) within the block's 128-byte row
-  #pragma unroll
-            for (int k = 0; k < NCH / 8; ++k) {
-              const int ch = sub + 8 * k;
-              cp_async16(kv_block(ra, rv, c, k) + sw128(key, sub), v ? src + ch * 16 : q, v);
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(B_FULLA + sa))
-                         : "memory");
-            ++ig;
-          } else {
-            const int sp = jg % L::VP_SLOTS;
-            if (jg >= L::VP_SLOTS && !bar_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
-              timed_out = true;
-              break;
-            }
-            const uint32_t rv = sbase + L::VP_OFF + sp * V_SLOT_BYTES;
-            // only this CTA's value half: copies k = 8c .. 8c + 7 of the 18
-  #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int ch = 32 * c + sub + 8 * k;
-              cp_async16(rv + k * KV_BLOCK_BYTES + sw128(key, sub), v ? src + ch * 16 : q, v);
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(B_FULLVP + sp))
-                         : "memory");
-            ++jg;
+      const int t0 = step(la, lb);
+      const int t1 = step(la, lb);
+      int32_t id0 = load_id(t0), id1 = load_id(t1);
+      for (int i = 0; i < T; ++i) {
+        const int t = step(na, nb);
+        const int32_t id = id0;
+        id0 = id1;
+        id1 = load_id(step(la, lb));
+        const bool v = id >= 0 && id < n_kv;
+        const char *src = kv + (v ? (int64_t)id * ROWB : 0);
+        if ((t & 1) == c) {
+          const int sa = ig % L::RA_SLOTS, so = ig % L::VO_SLOTS;
+          // slots 1 and 2 hold staged Q until it is in TMEM
+          if (ig == 1 && !bar_wait(bar(B_QSTAGED), 0)) {
+            timed_out = true;
+            break;
           }
+          if (ig >= L::RA_SLOTS && !bar_wait(bar(B_EMPTYA + sa), ((ig / L::RA_SLOTS) - 1) & 1)) {
+            timed_out = true;
+            break;
+          }
+          if (ig >= L::VO_SLOTS && !bar_wait(bar(B_EMPTYVO + so), ((ig / L::VO_SLOTS) - 1) & 1)) {
+            timed_out = true;
+            break;
+          }
+          const uint32_t ra = sbase + RA_OFF + sa * RA_SLOT_BYTES;
+          const uint32_t rv = sbase + L::VO_OFF + so * V_SLOT_BYTES;
+          // copy k of this thread is chunk sub + 4k: swizzle block k / 2,
+          // chunk sub + 4 (k & 1) within the block's 128-byte row
+#pragma unroll
+          for (int k = 0; k < NCH / 8; ++k) {
+            const int ch = sub + 8 * k;
+            cp_async16(kv_block(ra, rv, c, k) + sw128(key, sub), v ? src + ch * 16 : q, v);
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(B_FULLA + sa))
+                       : "memory");
+          ++ig;
+        } else {
+          const int sp = jg % L::VP_SLOTS;
+          if (jg >= L::VP_SLOTS && !bar_wait(bar(B_EMPTYVP + sp), ((jg / L::VP_SLOTS) - 1) & 1)) {
+            timed_out = true;
+            break;
+          }
+          const uint32_t rv = sbase + L::VP_OFF + sp * V_SLOT_BYTES;
+          // only this CTA's value half: copies k = 8c .. 8c + 7 of the 18
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int ch = 32 * c + sub + 8 * k;
+            cp_async16(rv + k * KV_BLOCK_BYTES + sw128(key, sub), v ? src + ch * 16 : q, v);
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar(B_FULLVP + sp))
+                       : "memory");
+          ++jg;
         }
       }
-      cp_async_wait<0>();
     }
+    cp_async_wait<0>();
   } else if (warp >= 12 && warp < 12 + NSB) {
     // ------------------------------------- Q K^T issuers (own tiles) ----
     // warp 12 + b issues own tiles ig = b, b + 2, ... into S buffer b
