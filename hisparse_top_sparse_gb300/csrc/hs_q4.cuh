@@ -20,8 +20,6 @@
 // 4 + i lie 16 bits apart, so a shift and a mask take a pair out of a word.
 #pragma once
 
-#include <cuda_fp4.h>
-
 #include "hs_internal.cuh"
 
 constexpr int Q4_GROUP = 16;
@@ -65,18 +63,31 @@ __device__ __forceinline__ uint64_t q4_pair(float x, float y) {
   asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
   return r;
 }
-// Two values over the scale to two codes, the first in the low nibble: to nearest,
-// ties to even, saturated; with every sign the other way round (so that a zero's
+// Two values over the scale, with every sign the other way round (so that a zero's
 // comes out right: Q4_SIGNS).
-__device__ __forceinline__ uint32_t q4_encode2(float lo, float hi, uint64_t s, uint64_t minus_inv) {
-  const uint64_t a = q4_pair(lo, hi);
+__device__ __forceinline__ float2 q4_minus_over(float x, float y, uint64_t s, uint64_t minus_inv) {
+  const uint64_t a = q4_pair(x, y);
   uint64_t b, e;
   asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(b) : "l"(a), "l"(minus_inv));
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(e) : "l"(s), "l"(b), "l"(a));
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(b) : "l"(e), "l"(minus_inv), "l"(b));
   float2 f;
   asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f.x), "=f"(f.y) : "l"(b));
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest);
+  return f;
+}
+// Four bytes of two codes each, x in the low nibble: to nearest, ties to even,
+// saturated.
+__device__ __forceinline__ uint32_t q4_codes(float2 a, float2 b, float2 c, float2 d) {
+  uint32_t w;
+  asm("{\n.reg .b8 p, q, r, s;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n"
+      "mov.b32 %0, {p, q, r, s};\n}\n"
+      : "=r"(w)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+  return w;
 }
 constexpr uint32_t Q4_SIGNS = 0x88888888u;
 

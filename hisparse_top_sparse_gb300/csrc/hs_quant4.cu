@@ -6,7 +6,7 @@
 // A warp takes a row: lane l holds VEC = 16 / sizeof(T) consecutive dims of every
 // pass, so the wide side moves in contiguous 16-byte accesses and the codes in
 // contiguous words; a group of 16 dims is 16 / VEC neighbouring lanes, whose
-// largest magnitude and scale bytes take shuffles only.
+// largest magnitude takes shuffles only.
 
 #include "hs_q4.cuh"
 #include "hs_rows.cuh"
@@ -86,21 +86,18 @@ __global__ void __launch_bounds__(QT_THREADS, QT_BLOCKS) k_quant_rows_q4(
         const uint64_t s = q4_pair(scale, scale), inv = q4_pair(minus_inv, minus_inv);
         // the word of eight dims: bytes (0, 2), (4, 6), (1, 3), (5, 7)
         if constexpr (L::VEC == 8) {
-          const uint32_t c = q4_encode2(f[0], f[2], s, inv) | q4_encode2(f[4], f[6], s, inv) << 8 |
-                             q4_encode2(f[1], f[3], s, inv) << 16 | q4_encode2(f[5], f[7], s, inv) << 24;
+          const uint32_t c = q4_codes(q4_minus_over(f[0], f[2], s, inv), q4_minus_over(f[4], f[6], s, inv),
+                                      q4_minus_over(f[1], f[3], s, inv), q4_minus_over(f[5], f[7], s, inv));
           *reinterpret_cast<uint32_t *>(d[u] + (32 * k + lane) * 4) = c ^ Q4_SIGNS;
         } else {
           // half of it each in two neighbouring lanes
-          uint32_t c = (q4_encode2(f[0], f[2], s, inv) | q4_encode2(f[1], f[3], s, inv) << 16) << (8 * (lane & 1));
+          const float2 zero = make_float2(0.f, 0.f);
+          uint32_t c = q4_codes(q4_minus_over(f[0], f[2], s, inv), zero, q4_minus_over(f[1], f[3], s, inv), zero)
+                       << (8 * (lane & 1));
           c |= __shfl_xor_sync(0xffffffffu, c, 1);
           if (!(lane & 1)) *reinterpret_cast<uint32_t *>(d[u] + (32 * k + lane) * 2) = c ^ Q4_SIGNS;
         }
-        // the bytes of four neighbouring groups into one word
-        uint32_t b = byte << (8 * ((lane / L::GL) & 3));
-        b |= __shfl_xor_sync(0xffffffffu, b, L::GL);
-        b |= __shfl_xor_sync(0xffffffffu, b, 2 * L::GL);
-        if (lane % (4 * L::GL) == 0)
-          *reinterpret_cast<uint32_t *>(d[u] + Q4_SCALE_OFF + (32 * k + lane) / L::GL) = b;
+        if (lane % L::GL == 0) d[u][Q4_SCALE_OFF + (32 * k + lane) / L::GL] = (char)byte;
       }
       if (lane < L::ROPE_LANES) {
         char *at = d[u] + Q4_ROPE_OFF + lane * (2 * L::VEC);
