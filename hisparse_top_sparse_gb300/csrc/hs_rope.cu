@@ -23,11 +23,14 @@
 namespace {
 
 constexpr int RT = 256;               // threads of a block, at most
-// A thread has HEAD_BATCH heads of a row in flight, of at most HEADS, or copies
-// dims of ROW_BATCH rows. Measured (8192 rows x 128 heads x 64 dims; 65535 rows of
-// 576 dims; the floors are 39.5 and 22.3 us): at most 4 / 8 / 16 heads 53 / 46 / 47
-// us; 2 / 4 / 8 rows 36 / 29 / 26 us.
-constexpr int HEAD_BATCH = 4, HEADS = 8, ROW_BATCH = 8;
+// A thread has HEAD_BATCH heads of a row in flight, of at most most_heads(), or copies
+// dims of ROW_BATCH rows. Measured, before the closing fence: 65535 rows of 576
+// dims, 2 / 4 / 8 rows in flight 36 / 29 / 26 us (the floor is 22.3); 8192 rows x 128
+// heads x 64 dims, with it: interleaved, five blocks an SM, at most 8 / 16 / 32 heads
+// 52 / 48.5 / 49.5 us; half, three blocks (16 bytes of either half take registers),
+// 8 heads 50, four blocks and 16 heads 57 (the floor is 39.5).
+constexpr int HEAD_BATCH = 4, ROW_BATCH = 8;
+constexpr int most_heads(bool half) { return half ? 8 : 16; }
 
 struct RopeArgs {
   const char *src;
@@ -117,7 +120,7 @@ __device__ __forceinline__ void sincos_turn(uint32_t turn, float &sine, float &c
 }
 
 template <typename T, bool HALF, bool VECTOR, bool ROWS>
-__global__ void __launch_bounds__(RT, 3) k_rope_rows(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(RT, HALF || ROWS ? 3 : 5) k_rope_rows(const __grid_constant__ RopeArgs a) {
   using A = Access<T, VECTOR>;
   using Raw = typename A::Raw;
   constexpr int N = A::N;
@@ -267,6 +270,11 @@ __global__ void __launch_bounds__(RT, 3) k_rope_rows(const __grid_constant__ Rop
       }
     }
   }
+  // An attention call behind this one (a programmatic dependent launch) reads q, by
+  // tensor copies, once every block here has ended, without waiting for the end of
+  // the grid: what was written is in place by then. (5 us of the largest calls.)
+  __threadfence();
+  asm volatile("fence.proxy.async.global;\n" ::: "memory");
 }
 
 template <typename T, bool HALF, bool VECTOR>
@@ -367,15 +375,15 @@ extern "C" int hs_rope_rows(const void *src, int64_t src_row_stride, int64_t src
   const int per = vector ? (int)(16 / elem) : 1;
   a.rot_units = !vector || half ? a.half / per : rot_dim / per;
   a.copy_units = same ? 0 : (head_dim - rot_dim) / per;
-  // Units of a thread: one up to 256 threads an SM, then up to HEADS heads of a row
-  // or, where there are fewer heads than a batch, ROW_BATCH rows (with one unit up to
-  // 2048 threads an SM 8191 rows of 576 dims took 10.7 us, now 4.7, and 512 rows of
-  // 128 heads 9.1, now 4.5).
+  // Units of a thread: one up to 512 threads an SM, then up to most_heads() heads of a
+  // row or, where there are fewer heads than a batch, ROW_BATCH rows (with one unit up
+  // to 2048 threads an SM 8191 rows of 576 dims took 10.7 us, now 5.1, and 512 rows of
+  // 128 heads 9.1, now 5).
   int sms = 0;
   if ((rc = hs_sm_count(&sms))) return rc;
-  int64_t each = (int64_t)n * heads * (a.rot_units + a.copy_units) / ((int64_t)sms * 256);
-  each = each < 1 ? 1 : each > HEADS ? HEADS : each;
-  const bool rows = heads < HEAD_BATCH && each > 1;
+  const int64_t full = (int64_t)n * heads * (a.rot_units + a.copy_units) / ((int64_t)sms * 512);
+  const int64_t each = full < 1 ? 1 : full > most_heads(half) ? most_heads(half) : full;
+  const bool rows = heads < HEAD_BATCH && full > 0;
   a.step = rows ? heads : (int32_t)((heads + each - 1) / each);
   const int set = rows ? ROW_BATCH : 1;
   const auto threads_of = [&](int64_t sets) {

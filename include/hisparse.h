@@ -264,8 +264,9 @@ int hs_swap_in(hs_buffer *buf, const int32_t *req_id_per_row,
  * finished, if that kernel lets its dependents start early, as
  * hs_resolve_topk does; idx, kv and the request flags are read only after
  * the previous kernel has finished. So q must not be written by such an
- * early-releasing kernel immediately before this call (no call of this
- * library writes q).
+ * early-releasing kernel immediately before this call (hs_rope_rows, the call
+ * of this library that writes q, is none, and has its writes in place before it
+ * ends).
  */
 int hs_sparse_attn_decode(const void *q, const void *kv, int64_t n_kv_rows,
                           const int32_t *idx, int32_t R, int32_t H, int32_t K,

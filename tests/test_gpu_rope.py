@@ -20,10 +20,10 @@ def _f64(x):
 
 
 def _bound(x, want, factor, dtype):
-    """A cosine or sine is off by at most 2^-22 (its argument's rounding to f32,
-    pi 2^-25, its own two units of 2^-24, and the factor's product), the two
-    products and their sum by 2^-22 of the magnitudes more; then the rounding to
-    the type, half a step."""
+    """A cosine or sine is off by at most 2^-22 (its argument's roundings to f32,
+    pi / 4 2^-23, a unit or two of 2^-24 for itself, and the factor's product), the
+    two products and their sum by 2^-22 of the magnitudes more; then the rounding
+    to the type, half a step."""
     a = np.abs(x).max(-1, keepdims=True)
     half = torch.finfo(dtype).eps / 2
     return 2 * a * abs(factor) * 2.0 ** -21 * (1 + half) + np.abs(want) * half + 1e-38
@@ -81,8 +81,7 @@ def test_far_and_negative_positions(half):
     want = O.rope_rows(x.astype(np.float64), pos, freqs.numpy(), 1.0, 0, half)
     assert (np.abs(_f64(out) - want) <= _bound(x, want, 1.0, torch.float32)).all()
     # any 64-bit fraction of a turn, negative ones and halves among them
-    odd = np.array([-1, 1 << 63, 1 << 62, (1 << 63) - 1, 12345678901234567], np.uint64 if False else object)
-    odd = np.array([int(v) - (1 << 64) if int(v) >= 1 << 63 else int(v) for v in odd], np.int64)
+    odd = np.array([-1, -(1 << 63), 1 << 62, (1 << 63) - 1, 12345678901234567], np.int64)
     y = x[:, :, :10].copy()
     hs.hs_rope_rows(_t(y), out[:, :, :10], _t(pos), _t(odd), layout=int(half))
     want = O.rope_rows(y.astype(np.float64), pos, odd, 1.0, 0, half)
