@@ -56,7 +56,7 @@
 // distributed shared memory about half a microsecond after the CTA's own P
 // of the same pair, and an own tile queued behind it would hold its ring
 // slots that much longer.
-// k_attn_pair<true> reads q8 rows (hs_q8.cuh). Its products, softmax and
+// k_attn_pair<HS_ROWS_Q8> reads q8 rows (hs_q8.cuh). Its products, softmax and
 // exchange are the same, over the same bf16 tiles: their values are exact in
 // bf16, so the output is bit for bit that of the bf16 kernel over the rows read
 // back. Four more warps and different rings bring the rows in: they land raw,
@@ -66,6 +66,19 @@
 // softmax and its P V, about 2.9 pairs, and three fit beside the raw rings.
 // Rows decoded by the gather warps of both kinds of tile in turn: 124 us;
 // rows loaded into registers one tile ahead: 112, two ahead: 137.
+// k_attn_pair<HS_ROWS_Q4> reads q4 rows (hs_q4.cuh), whose values enter the tiles as
+// 2^-15 of themselves (exactly; the softmax's scale and the output's make up for
+// it). Its rows come straight into registers, a tile ahead: 18 KB of them are in
+// flight a tile pair, which the L1 holds, and without raw rings a pair moves some
+// 190 KB through shared memory, not 230. 128 / 512 rows x 128 heads x 2048 keys 81.3 /
+// 281 us (through raw rings 91.6 / 316), a tile pair per 1.05 us. That bandwidth is
+// what bounds it: the products' operands (124 KB, 48 of them Q's dims 384..575 read
+// anew for every tile), the decoded rows (52), P (32) and the loads take 1850 of a
+// pair's 2070 cycles at 128 bytes each; per-warp stamps show Q K^T of one tile or
+// the other in issue all the time, 1960 cycles for what takes 860 alone. Measured
+// and not kept: P V's operand P from shared memory, so that S is free once it is
+// read, 85.5 us; two exchange slots 82.9; ring A, VP or VO a slot longer 83, 84.7,
+// 82.8 (of 81.8).
 // Few rows: the keys of a row are split over clusters (parts of whole tiles,
 // each a row of its own to the kernel) and k_attn_join joins the parts.
 // 17 to 64 heads take what 128 take (128 rows x 2048 keys: 17 / 32 / 64 / 128 heads

@@ -1,4 +1,4 @@
-// a6 over a q8 cache for up to 16 heads (a query's heads divided over several
+// a6 over a q8 or q4 cache for up to 16 heads (a query's heads divided over several
 // devices, or a small model): the formulas of hs_attn.cu, another shape.
 //
 // With 128 heads a row's products are what k_attn_pair is built around; with 16
@@ -19,7 +19,8 @@
 //   * each warp scales its 64 dims of O (f32 registers) when a reference moved
 //     and adds P V.
 // Raw rows come by cp.async, three tiles in flight, in places of 704 bytes (of
-// 656 used), which spreads a warp's reads over the banks.
+// 656 used), which spreads a warp's reads over the banks; q4
+// rows two tiles, in places of their 416 bytes.
 //
 // Measured, 16 heads (k_attn_pair, its heads padded to 128, in brackets): 8 rows
 // of 64 keys 5.0 us (7.3), 300 rows of one key 5.0 (31), 256 rows of 300 keys 24
@@ -32,9 +33,18 @@
 // rows by one bulk copy each 92; two tiles in flight 81, four 76; the maximum
 // of every tile 76 (of 74).
 //
+// q4 rows: 8 rows of 64 keys 4.7 us, 300 rows of one key 5.0, 256 rows of 300 keys 19,
+// 128 rows of 2048 keys 57 (two / three / four / five tiles in flight 57.3 / 59.7 /
+// 58.2 / 58.7), 512 rows 198; an instruction issues on 47 % of the cycles, the shared
+// memory pipe is busy for 50 %, the matrix pipe for 32. Codes of four keys decoded
+// dim by dim, so that products in a row do not wait for one another: 60.3.
+//
 // tcgen05 would want 128 rows of something: heads padded eightfold, or keys and
-// dims in that place, and then every decoded tile through shared memory;
-// mma.sync needs neither.
+// dims in that place, and then every decoded tile through shared memory; mma.sync
+// needs neither. (The latter was built for q4 rows: tiles of 64 keys, S^T = K Q^T of
+// 64 rows and O^T += V^T P^T of 128, 16 columns each, two blocks an SM. 67.9 us on
+// 128 rows, 8.1 on 8 of 64 keys: 36 instructions of some 30 cycles and 16 of 66, the
+// transposed ones, a tile, and the decoding, softmax and hand-overs beside them.)
 
 #include <atomic>
 #include <math.h>

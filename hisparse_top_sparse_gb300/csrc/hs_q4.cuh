@@ -10,10 +10,9 @@
 // scale. A group's scale is the smallest whose largest code, 6 * scale, reaches
 // the group's largest magnitude. A code has two significant bits and a scale
 // four, so every value is a bf16 number and reading a row back rounds nothing.
-// Four bits leave a group one step in six of its size: sixteen dims a scale and
-// three bits of fraction, rather than 32 and a power of two, halve the squared
-// error of normally distributed rows (their codes come out 1.05 to 1.0 times as
-// large as they need be, not up to 2), for 16 bytes more a row. Scales run from
+// Sixteen dims a scale and three bits of its fraction leave rows of normally
+// distributed dims, alike or unlike in size, a squared error of 1.0 % of theirs;
+// 32 dims and a power of two, 16 bytes less a row, 1.3 to 2.0 %. Scales run from
 // 2^-16 to 1.75 * 2^15; byte 255 marks a group that held a NaN or an infinity,
 // all of whose values are NaN.
 // The order of the nibbles is that of a pair of bf16 values: nibble i and nibble
