@@ -1648,40 +1648,81 @@ extern "C" int hs_sparse_attn_decode(const void *q, const void *kv, int64_t n_kv
 
 namespace {
 
+constexpr int JOIN_MOST = 512;      // parts of a row, at most
+
 // Joins the parts of every (row, head): with L = max_s lse_s and w_s =
 // exp(lse_s - L), out = sum_s w_s O_s / sum_s w_s and lse = L + ln(sum_s w_s).
 // Parts without a valid key have lse_s = -inf and weigh nothing. A block per
 // (row, head); GROUPS groups of 128 threads (four dims each) take every
-// GROUPS-th part, four loads in flight, and their sums meet in shared memory in
-// a fixed order. Latency bounds a small grid: four groups read its parts in
-// as few rounds as they allow (one row of 128 heads, 16 parts: 12.8 us for the
-// whole call against 13.7 with one group, 64 parts: 17.1 against 21.2); a
-// large one fills the SMs and takes one (16 rows: 23.2 us against 26.6). The
+// GROUPS-th part, and their sums meet in shared memory in a fixed order. Latency
+// bounds a small grid: four groups read its parts in as few rounds as they allow
+// (one row of 128 heads, 16 parts: 12.8 us for the whole call against 13.7 with one
+// group, 64 parts: 17.1 against 21.2); a large one fills the SMs and takes one
+// (16 rows: 23.2 us against 26.6). A group's first parts (all of up to SMALL) are
+// loaded together with the weights' logarithms; of up to SMALL parts every thread
+// makes the weights by itself, of more the block, once, in shared memory. Before,
+// every thread walked the parts' logarithms twice: q4 rows, 1 x 128 x 8192 keys 16.6
+// us, now 13.6; 1 x 16 x 8192 (128 parts) 16.6, now 9.4; 1 x 16 x 2048 9.0, now 7.4;
+// 43 x 16 x 1001 (7 parts) 16.4, now 15.2; 30 x 128 x 2048 (2) 30.2, now 29. The
 // parts are written while this kernel may already run (until the wait), so they
 // are not read-only to it: no __restrict__, which would let the compiler take
 // the non-coherent path.
-template <int GROUPS>
+template <int GROUPS, int SMALL>
 __global__ void __launch_bounds__(GROUPS * DV / 4)
     k_attn_join(const float *o, const float *part_lse, int32_t n, int64_t rows, __nv_bfloat16 *out, float *lse) {
+  constexpr int NT = GROUPS * DV / 4, AHEAD = SMALL ? (SMALL + GROUPS - 1) / GROUPS : 8;
   // a programmatic dependent launch of the kernel that writes the parts
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int64_t row = blockIdx.x;
   const int g = threadIdx.x / (DV / 4), t = threadIdx.x % (DV / 4);
   const float4 *src = reinterpret_cast<const float4 *>(o + row * DV) + t;
-  float top = -INFINITY;
-  for (int s = 0; s < n; ++s) top = fmaxf(top, part_lse[s * rows + row]);
-  const float ref = top == -INFINITY ? 0.f : top;
+  // a group's first parts are on their way while the weights are made
+  float4 v[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (g + k * GROUPS < n) v[k] = src[(g + k * GROUPS) * rows * (DV / 4)];
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  float w_sum = 0.f;
-#pragma unroll 4
-  for (int s = g; s < n; s += GROUPS) {
-    const float w = exp2f((part_lse[s * rows + row] - ref) * 1.4426950408889634f);
-    const float4 v = src[s * rows * (DV / 4)];
+  float w_sum = 0.f, ref;
+  auto add = [&](float w, const float4 &x) {
     w_sum += w;
-    a.x += w * v.x;
-    a.y += w * v.y;
-    a.z += w * v.z;
-    a.w += w * v.w;
+    a.x += w * x.x;
+    a.y += w * x.y;
+    a.z += w * x.z;
+    a.w += w * x.w;
+  };
+  if constexpr (SMALL > 0) {
+    float x[SMALL], top = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < SMALL; ++s) {
+      x[s] = s < n ? part_lse[s * rows + row] : -INFINITY;
+      top = fmaxf(top, x[s]);
+    }
+    ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int s = 0; s < SMALL; ++s)
+      if (s < n && s % GROUPS == g) add(exp2f((x[s] - ref) * 1.4426950408889634f), v[s / GROUPS]);
+  } else {
+    __shared__ float weight[JOIN_MOST], most[NT / 32];
+    float top = -INFINITY;
+    for (int s = threadIdx.x; s < n; s += NT) {
+      const float x = part_lse[s * rows + row];
+      weight[s] = x;
+      top = fmaxf(top, x);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x / 32] = top;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NT / 32; ++k) top = fmaxf(top, most[k]);
+    ref = top == -INFINITY ? 0.f : top;
+    for (int s = threadIdx.x; s < n; s += NT) weight[s] = exp2f((weight[s] - ref) * 1.4426950408889634f);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (g + k * GROUPS < n) add(weight[g + k * GROUPS], v[k]);
+#pragma unroll 8
+    for (int s = g + AHEAD * GROUPS; s < n; s += GROUPS) add(weight[s], src[s * rows * (DV / 4)]);
   }
   if constexpr (GROUPS > 1) {
     __shared__ float4 acc[GROUPS][DV / 4];
@@ -1750,6 +1791,7 @@ static int attn_quantised(const void *q, const void *kv, int64_t n_kv_rows, cons
     if (n > tiles / least) n = tiles / least;
     const int64_t room = (int64_t)(workspace_bytes / (rows * (DV + 1) * sizeof(float)));
     if (n > room) n = room;
+    if (n > JOIN_MOST) n = JOIN_MOST;
     if (n > 1) {
       const int per = (int)((tiles + n - 1) / n);
       parts.n = (tiles + per - 1) / per;      // every part has keys
@@ -1774,7 +1816,13 @@ static int attn_quantised(const void *q, const void *kv, int64_t n_kv_rows, cons
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  HS_CUDA_TRY(cudaLaunchKernelEx(&cfg, few ? k_attn_join<4> : k_attn_join<1>, (const float *)parts.o,
+  const int n = parts.n;
+  const auto join = few ? (n <= 2 ? k_attn_join<4, 2> : n <= 4 ? k_attn_join<4, 4>
+                                  : n <= 8 ? k_attn_join<4, 8> : k_attn_join<4, 0>)
+                        : (n <= 2 ? k_attn_join<1, 2> : n <= 4 ? k_attn_join<1, 4>
+                                  : n <= 8 ? k_attn_join<1, 8> : k_attn_join<1, 0>);
+  HS_CUDA_TRY(cudaLaunchKernelEx(&cfg, join,
+                                 (const float *)parts.o,
                                  (const float *)parts.lse, parts.n, (int64_t)R * H,
                                  reinterpret_cast<__nv_bfloat16 *>(out), lse));
   HS_LAUNCH_CHECK("k_attn_join");
