@@ -628,8 +628,8 @@ struct HalfRow<HS_ROWS_Q8> {
 };
 
 // A q4 chunk holds 32 dims and two scales. Its values, 2^-15 of theirs (hs_q4.cuh),
-// go to four neighbouring chunks of a key's 128 bytes in block `block` at `at`:
-// chunks 4 odd .. 4 odd + 3, swizzled.
+// go to four neighbouring chunks of a key's 128 bytes in a block: chunks 4 odd ..
+// 4 odd + 3, swizzled.
 __device__ __forceinline__ void put_q4(uint32_t block, int key, int odd, const uint4 w, uint32_t bytes) {
   const uint32_t s0 = q4_scale2(bytes & 0xFFu), s1 = q4_scale2(bytes >> 8 & 0xFFu);
   const uint32_t to = block + sw128(key, 4 * odd);
@@ -891,7 +891,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
           ++ig;
           return true;
         };
-        for (int pass = 0; pass < 2 && begins(pass); ++pass) {
+        for (int pass = 0; pass < 2 && !timed_out && begins(pass); ++pass) {
           OwnRow<F> row;
           int32_t id = load_id(c);
           if constexpr (L::RINGS) {
@@ -1354,7 +1354,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
   // the same blocks leave an SM at some 20 bytes a clock, and the closing
   // barrier waited behind them: 7.9 us against 7.5 on 8 rows of 64 keys, 94.9
   // against 93.8 on 128 of 2048; one bulk copy per head and 128 dims, with no
-  // tensor map, is as slow (a copy issues every ten clocks).
+  // tensor map, is as slow (a copy issues every ten clocks). Sixteen warps of 64
+  // columns (q4) took 0.3 us more a row.
   if (warp < 8) {
     if (warp == 0 && !warp_wait(bar(B_QLOAD + 3), 0)) timed_out = true;   // Q, where O is staged
     if (timed_out) atomicOr((uint32_t *)s_fail, 1u);

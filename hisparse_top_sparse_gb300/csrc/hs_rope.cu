@@ -322,7 +322,9 @@ extern "C" int hs_rope_rows(const void *src, int64_t src_row_stride, int64_t src
   // no two heads or rows of the destination share an element: the heads of a row
   // lie within its stride, or the rows of a head within the head's
   const auto within = [&](int64_t inner, int64_t count, int64_t outer, int64_t outers) {
-    return (count <= 1 || inner >= head_dim) && (outers <= 1 || outer >= (count - 1) * inner + head_dim);
+    // (in floating point: the product of any count and stride has a place there)
+    return (count <= 1 || inner >= head_dim) &&
+           (outers <= 1 || (double)outer >= ((double)count - 1.) * (double)inner + head_dim);
   };
   if (!within(dst_head_stride, heads, dst_row_stride, dst_rows) &&
       !within(dst_row_stride, dst_rows, dst_head_stride, heads))

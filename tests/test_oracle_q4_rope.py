@@ -149,6 +149,7 @@ def test_call_refusals_without_a_gpu():
                dict(pos=ctypes.c_void_p(18)), dict(ss=ctypes.c_void_p(2)), dict(ds=ctypes.c_void_p(2)),
                dict(st=ctypes.c_void_p(2)),
                dict(drow=63), dict(heads=2, drow=128, dhead=63), dict(heads=2, drow=127, dhead=64),
-               dict(heads=2, drow=64, dhead=255)):            # rows or heads of dst share elements
+               dict(heads=2, drow=64, dhead=255),             # rows or heads of dst share elements
+               dict(heads=2, drow=64, dhead=1 << 40, drows=1 << 62), dict(heads=65535, drow=1 << 40, dhead=1 << 40, dim=64)):
         assert rope(**kw) == bad, kw
     assert rope(heads=40000, dim=40000, dhead=40000, drow=40000 * 40000, n=4) == hs.HS_ERR_UNSUPPORTED
