@@ -73,6 +73,8 @@ class _Desc(ctypes.Structure):
 
 
 _lib = None
+_native = None          # the short way of calls that take microseconds (csrc/hs_call.c), where it is built
+_ADDR = {}              # and the functions that it calls
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -81,7 +83,7 @@ _D = ctypes.c_double
 
 def lib() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
-    global _lib
+    global _lib, _native
     if _lib is None:
         if not os.path.exists(_LIB_PATH):
             raise RuntimeError(
@@ -136,8 +138,20 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
+            _ADDR[name] = ctypes.cast(f, _P).value
+        _native = _short_way()
         _lib = L
     return _lib
+
+
+def _short_way():
+    try:
+        from . import _call
+        _call.setup(torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8,
+                    torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    except (ImportError, AttributeError):
+        return None
+    return _call
 
 
 def _check(rc: int, what: str) -> None:
@@ -540,7 +554,9 @@ def hs_backup_indexer(src_caches, dst_caches, src_slots, host_slots, positions,
 
 # The calls below take microseconds, and so must their checks: one test of all
 # that is wanted of a tensor, and the reasons only once it has failed. Every
-# CUDA tensor must be on the current device, where the call launches.
+# CUDA tensor must be on the current device, where the call launches. The calls
+# over quantised rows and the rotation go through _native first, which checks and
+# calls at once and answers None where anything is not plainly right.
 
 def _on(t, name, dtype, shape, cur):
     """Pointer of a contiguous CUDA tensor of the current device."""
@@ -637,7 +653,12 @@ def _entries(src_slots, dst_slots, src_rows, dst_rows, cur):
     return sp, dp, n
 
 
-def _quant(f, what, row_bytes, src, cache, src_slots, dst_slots, status, stream) -> None:
+def _quant(what, row_bytes, src, cache, src_slots, dst_slots, status, stream) -> None:
+    f = getattr(lib(), what)
+    if _native is not None:
+        rc = _native.quant(_ADDR[what], row_bytes, src, cache, src_slots, dst_slots, status, stream)
+        if rc is not None:
+            return _check(rc, what)
     cur = _device()
     sp, dt, stride, src_rows = _wide_rows(src, "src", cur)
     dp, rows = _quantised(cache, "cache", row_bytes, cur)
@@ -647,7 +668,12 @@ def _quant(f, what, row_bytes, src, cache, src_slots, dst_slots, status, stream)
              _on_stream(stream, cur)), what)
 
 
-def _dequant(f, what, row_bytes, cache, dst, src_slots, dst_slots, status, stream) -> None:
+def _dequant(what, row_bytes, cache, dst, src_slots, dst_slots, status, stream) -> None:
+    f = getattr(lib(), what)
+    if _native is not None:
+        rc = _native.dequant(_ADDR[what], row_bytes, cache, dst, src_slots, dst_slots, status, stream)
+        if rc is not None:
+            return _check(rc, what)
     cur = _device()
     sp, rows = _quantised(cache, "cache", row_bytes, cur)
     dp, dt, stride, dst_rows = _wide_rows(dst, "dst", cur)
@@ -657,7 +683,12 @@ def _dequant(f, what, row_bytes, cache, dst, src_slots, dst_slots, status, strea
              _on_stream(stream, cur)), what)
 
 
-def _attend(f, what, row_bytes, q, kv, idx, scale, out, lse, workspace, status, stream) -> None:
+def _attend(what, row_bytes, q, kv, idx, scale, out, lse, workspace, status, stream) -> None:
+    f = getattr(lib(), what)
+    if _native is not None:
+        rc = _native.attend(_ADDR[what], row_bytes, q, kv, idx, scale, out, lse, workspace, status, stream)
+        if rc is not None:
+            return _check(rc, what)
     R, H, D = q.shape
     if D != LATENT_DIM:
         raise ValueError("q must be [R][H][576]")
@@ -682,14 +713,14 @@ def hs_quant_rows(src, cache, src_slots=None, dst_slots=None, status=None, strea
     """Row dst_slots[i] of the q8 cache (uint8 [rows][656]) = row src_slots[i]
     of src (bf16 / f32 [rows][576]), quantised; without a list entry i is row
     i, negative slots are skipped."""
-    _quant(lib().hs_quant_rows, "hs_quant_rows", Q8_ROW_BYTES, src, cache, src_slots, dst_slots,
+    _quant("hs_quant_rows", Q8_ROW_BYTES, src, cache, src_slots, dst_slots,
            status, stream)
 
 
 def hs_dequant_rows(cache, dst, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
     """Row dst_slots[i] of dst (bf16 / f32 [rows][576]) = the values of row
     src_slots[i] of the q8 cache."""
-    _dequant(lib().hs_dequant_rows, "hs_dequant_rows", Q8_ROW_BYTES, cache, dst, src_slots,
+    _dequant("hs_dequant_rows", Q8_ROW_BYTES, cache, dst, src_slots,
              dst_slots, status, stream)
 
 
@@ -698,7 +729,7 @@ def hs_sparse_attn_decode_q8(q, kv, idx, scale: float, out, lse=None, workspace=
     """hs_sparse_attn_decode over a q8 cache (uint8 [rows][656]). workspace:
     uint8 CUDA tensor (ATTN_Q8_WORKSPACE_BYTES is enough for every call) with
     which few rows run split over the SMs; one per call in flight."""
-    _attend(lib().hs_sparse_attn_decode_q8, "hs_sparse_attn_decode_q8", Q8_ROW_BYTES, q, kv, idx,
+    _attend("hs_sparse_attn_decode_q8", Q8_ROW_BYTES, q, kv, idx,
             scale, out, lse, workspace, status, stream)
 
 
@@ -706,21 +737,21 @@ def hs_sparse_attn_decode_q8(q, kv, idx, scale: float, out, lse=None, workspace=
 
 def hs_quant_rows_q4(src, cache, src_slots=None, dst_slots=None, status=None, stream=None) -> None:
     """hs_quant_rows into a q4 cache (uint8 [rows][416])."""
-    _quant(lib().hs_quant_rows_q4, "hs_quant_rows_q4", Q4_ROW_BYTES, src, cache, src_slots,
+    _quant("hs_quant_rows_q4", Q4_ROW_BYTES, src, cache, src_slots,
            dst_slots, status, stream)
 
 
 def hs_dequant_rows_q4(cache, dst, src_slots=None, dst_slots=None, status=None,
                        stream=None) -> None:
     """hs_dequant_rows from a q4 cache (uint8 [rows][416])."""
-    _dequant(lib().hs_dequant_rows_q4, "hs_dequant_rows_q4", Q4_ROW_BYTES, cache, dst, src_slots,
+    _dequant("hs_dequant_rows_q4", Q4_ROW_BYTES, cache, dst, src_slots,
              dst_slots, status, stream)
 
 
 def hs_sparse_attn_decode_q4(q, kv, idx, scale: float, out, lse=None, workspace=None, status=None,
                              stream=None) -> None:
     """hs_sparse_attn_decode_q8 over a q4 cache (uint8 [rows][416])."""
-    _attend(lib().hs_sparse_attn_decode_q4, "hs_sparse_attn_decode_q4", Q4_ROW_BYTES, q, kv, idx,
+    _attend("hs_sparse_attn_decode_q4", Q4_ROW_BYTES, q, kv, idx,
             scale, out, lse, workspace, status, stream)
 
 
@@ -749,6 +780,12 @@ def hs_rope_rows(src, dst, positions, freqs, factor: float = 1.0, rot_off: int =
     dims from rot_off on rotated by positions[i]; freqs and factor as
     hs_rope_freqs gives them. dst may be src. Without a list entry i is row i,
     negative slots are skipped. See include/hisparse.h."""
+    f = lib().hs_rope_rows
+    if _native is not None:
+        rc = _native.rope(_ADDR["hs_rope_rows"], src, dst, positions, freqs, factor, rot_off, layout, inverse,
+                          src_slots, dst_slots, status, stream)
+        if rc is not None:
+            return _check(rc, "hs_rope_rows")
     cur = _device()
     sp, src_rows, src_row, heads, src_head, dims = _heads(src, "src", cur)
     dp, dst_rows, dst_row, dst_heads, dst_head, dst_dims = _heads(dst, "dst", cur)
@@ -771,7 +808,7 @@ def hs_rope_rows(src, dst, positions, freqs, factor: float = 1.0, rot_off: int =
     fp, pairs = _on(freqs, "freqs", torch.int64, None, cur), freqs.shape
     if len(pairs) != 1:
         raise ValueError("freqs must be int64 [pairs]")
-    _check(lib().hs_rope_rows(
+    _check(f(
         sp, src_row, src_head, src_rows, dp, dst_row, dst_head, dst_rows, _WIDE[src.dtype], ss, ds,
         pp, n, heads, dims, rot_off, 2 * pairs[0], layout, fp, factor, 1 if inverse else 0,
         None if status is None else _on(status, "status", torch.int32, (1,), cur),

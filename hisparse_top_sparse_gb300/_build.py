@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhisparse.so")
 INCLUDE = os.path.join(ROOT, "include")
+CALL_SRC = os.path.join(CSRC, "hs_call.c")     # the binding's short way (a Python module)
+CALL = os.path.join(HERE, "_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
@@ -30,16 +33,21 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is needed to build libhisparse")
 
 
+def _no_headers() -> bool:
+    """No C headers of this Python: the binding then does without its short way."""
+    return not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
 def sources() -> list:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not (os.path.exists(CALL) or _no_headers()):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(p) for p in (LIB, CALL) if os.path.exists(p))
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(INCLUDE, "hisparse.h"), __file__]
+        CALL_SRC, os.path.join(INCLUDE, "hisparse.h"), __file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
@@ -59,6 +67,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                             stderr=subprocess.STDOUT)))
+    if not _no_headers():
+        cmd = [os.environ.get("CC", "cc"), "-O2", "-fPIC", "-shared", "-I" + sysconfig.get_paths()["include"],
+               "-I" + INCLUDE, CALL_SRC, "-o", CALL + ".tmp"]
+        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     errors = []
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -72,6 +84,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError("link failed:\n" + res.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
+    if os.path.exists(CALL + ".tmp"):
+        os.replace(CALL + ".tmp", CALL)
     return LIB
 
 

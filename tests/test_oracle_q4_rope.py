@@ -153,3 +153,29 @@ def test_call_refusals_without_a_gpu():
                dict(heads=2, drow=64, dhead=1 << 40, drows=1 << 62), dict(heads=65535, drow=1 << 40, dhead=1 << 40, dim=64)):
         assert rope(**kw) == bad, kw
     assert rope(heads=40000, dim=40000, dhead=40000, drow=40000 * 40000, n=4) == hs.HS_ERR_UNSUPPORTED
+
+
+def test_the_bindings_short_way_leaves_to_the_long_one_what_it_does_not_take():
+    import torch
+    hs = _lib()
+    hs.lib()
+    if hs._native is None:
+        pytest.skip("no headers of this Python: the native module is not built")
+    N, addr = hs._native, hs._ADDR
+    x, c = torch.zeros((4, 576)), torch.zeros((4, 416), dtype=torch.uint8)
+    pos, freqs = torch.zeros(4, dtype=torch.int32), torch.zeros(32, dtype=torch.int64)
+    q, idx = torch.zeros((2, 3, 576), dtype=torch.bfloat16), torch.zeros((2, 5), dtype=torch.int32)
+    out = torch.zeros((2, 3, 512), dtype=torch.bfloat16)
+    for _ in range(3):
+        # tensors of the host (whatever the current device is), and what are no tensors
+        assert N.quant(addr["hs_quant_rows_q4"], 416, x, c, None, None, None, 0) is None
+        assert N.dequant(addr["hs_dequant_rows_q4"], 416, c, x, pos, None, None, None) is None
+        assert N.attend(addr["hs_sparse_attn_decode_q4"], 416, q, c, idx, 1.0, out, None, None, None, 0) is None
+        assert N.rope(addr["hs_rope_rows"], x, x, pos, freqs, 1.0, 0, 0, False, None, None, None, 0) is None
+        assert N.quant(addr["hs_quant_rows_q4"], 416, "x", 7, None, None, None, 0) is None
+        assert N.rope(addr["hs_rope_rows"], None, x, 3, [], "f", 0, 0, 1, None, None, None, 0) is None
+        assert N.quant() is None and N.attend(1, 2) is None
+    with pytest.raises(ValueError):
+        hs.hs_quant_rows_q4(x, c)
+    with pytest.raises(TypeError):
+        N.setup(1)
