@@ -385,7 +385,8 @@ int hs_dequant_rows_q4(const void *src, int64_t src_rows, void *dst, int32_t dst
 /* hs_sparse_attn_decode_q8 over a q4 cache, kv [n_kv_rows][416]: its arguments,
  * formulas, workspace and launch. With H > 16 and each row in one part the
  * results are those of hs_sparse_attn_decode over the rows read back, bit for
- * bit, for rope dims that are 0 or not below 2^-110 in magnitude.
+ * bit, for rope dims that are 0 or not below 2^-110 in magnitude and products q k
+ * that are finite there.
  * 0 <= scale <= 2^100. */
 int hs_sparse_attn_decode_q4(const void *q, const void *kv, int64_t n_kv_rows,
                              const int32_t *idx, int32_t R, int32_t H, int32_t K, float scale,
