@@ -84,9 +84,9 @@
 // 17 to 64 heads take what 128 take (128 rows x 2048 keys: 17 / 32 / 64 / 128 heads
 // 90.5 / 90.7 / 91.4 / 93.2 us, 8 rows of 64 keys 7.5 / 7.6 / 7.7 / 8.0): the hand-offs
 // that bound the kernel are per tile, whatever the heads.
-// The kernel is a programmatic dependent launch: its prologue (barriers, TMEM,
-// Q) overlaps the previous kernel (hs_resolve_topk releases it at entry), and
-// it reads the indices and request flags after griddepcontrol.wait.
+// The kernel is a programmatic dependent launch: its prologue (barriers, TMEM)
+// overlaps the previous kernel (hs_resolve_topk releases it at entry), and it
+// reads its inputs, q among them, after griddepcontrol.wait.
 // Every mbarrier wait is bounded; a wait that gives up sets HS_STATUS_TIMEOUT
 // in the caller's status word and the CTA winds down.
 
@@ -777,6 +777,14 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
   fence_after();
   cluster_arrive();
   const uint32_t tmem = *tmem_slot;
+  // Up to here the kernel has read nothing. It is launched as a programmatic
+  // dependent of the kernel before it (hs_resolve_topk lets it start at once), so
+  // that its barriers and its tensor memory overlap that kernel. What that kernel
+  // wrote, q among it, is sure to be seen only behind this wait: a kernel that
+  // releases nothing lets this one start when its blocks have ended, which is not
+  // yet when their writes are in place. Every thread takes it, before any bounded
+  // wait: the kernel before may run for longer than those.
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // Q by nine tensor copies of 128 heads x 64 dims (16 KB, 128-byte swizzle,
   // rows past H filled with zeros), all issued by this CTA into its own
   // shared memory: dims 384..575 land in SMEM as the MMA's A operand, dims
@@ -791,7 +799,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
   // (Tried: each CTA copying half of Q to both by multicast, and copies issued
   // before the CTA's first barrier: no faster.)
   if (warp == 12 + NSB && lane == 0) {
-    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    // (of all state spaces: q was written by ordinary stores)
+    asm volatile("fence.proxy.async;\n" ::: "memory");
 #pragma unroll
     for (int g = 0; g < 4; ++g) arrive_expect_tx(bar(B_QLOAD + g), (g < 3 ? 2 : 3) * HG * 128);
 #pragma unroll
@@ -831,11 +840,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
     __syncwarp();
   }
 
-  // Up to here the kernel has read only q. It is launched as a programmatic
-  // dependent of the kernel before it (hs_resolve_topk lets it start at once),
-  // so that its prologue overlaps that kernel: the indices and the request
-  // flags are read only after that kernel has finished.
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // the row's cache: the paged resident cache while its request is fully
   // resident, else the hot buffer its swap-in indices address
   // (a request id outside [0, n_reqs) leaves the row without a valid entry)
@@ -1603,8 +1607,8 @@ static int attn_launch(const void *q, const void *kv_resident, int64_t n_residen
                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (eo != CUDA_SUCCESS) return hs_set_error(HS_ERR_CUDA, "tensor map of the output failed (%d)", (int)eo);
-  // a programmatic dependent launch: the prologue (barriers, TMEM, Q) may
-  // run while the previous kernel in the stream finishes
+  // a programmatic dependent launch: the prologue (barriers, TMEM) may run while
+  // the previous kernel in the stream finishes
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(Lay<F>::RAW ? RAW_THREADS : THREADS);
