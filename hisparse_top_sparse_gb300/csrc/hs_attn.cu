@@ -1342,10 +1342,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
     constexpr float out_scale = F == HS_ROWS_Q4 ? (float)(1 << Q4_SHIFT) : 1.f;
     const int h = h0 + hrow;
     const float lt = l + l_peer;
-    reinterpret_cast<volatile float *>(sm + L::XMAX_OFF)[hrow] = lt > 0.f ? out_scale / lt : 0.f;
+    // (lt <= 0: no key; a sum that is NaN stays NaN)
+    reinterpret_cast<volatile float *>(sm + L::XMAX_OFF)[hrow] = lt <= 0.f ? 0.f : out_scale / lt;
     float *lse_to = RAW && parts.n > 1 ? parts.lse + (int64_t)part * parts.R * H : lse;
     if (lse_to && c == 0 && h < H)
-      lse_to[(int64_t)r * H + h] = lt > 0.f ? (ref + log2f(lt)) * 0.69314718055994530942f : -INFINITY;
+      lse_to[(int64_t)r * H + h] = lt <= 0.f ? -INFINITY : (ref + log2f(lt)) * 0.69314718055994530942f;
     if (tid == 0) *s_last = (uint32_t)last_pass;
     own_sent = ig;
   }

@@ -249,7 +249,9 @@ int hs_swap_in(hs_buffer *buf, const int32_t *req_id_per_row,
  * dims;  out[r,h,:] = sum_j softmax(s)_j * kv[idx[r,j], 0:512];
  * lse[r,h] = ln(sum_j exp(s_j)). Entries of idx outside [0, n_kv_rows) are
  * skipped; repeated entries count each time; a row with no valid entry gives
- * out = 0 and lse = -inf. bf16 inputs, fp32 accumulation, bf16 output.
+ * out = 0 and lse = -inf. A NaN in a selected entry, or in a head of q, is NaN in
+ * out and lse of the heads that it reaches. bf16 inputs, fp32 accumulation, bf16
+ * output.
  *   q      device bf16 [R][H][576], 16-byte aligned
  *   kv     device bf16 [n_kv_rows][576], 16-byte aligned (the paged cache for
  *          resolve indices, hot_kv for swap-in indices)
