@@ -24,11 +24,12 @@ namespace {
 
 constexpr int RT = 256;               // threads of a block, at most
 // A thread has HEAD_BATCH heads of a row in flight, of at most most_heads(), or copies
-// dims of ROW_BATCH rows. Measured, before the closing fence: 65535 rows of 576
-// dims, 2 / 4 / 8 rows in flight 36 / 29 / 26 us (the floor is 22.3); 8192 rows x 128
-// heads x 64 dims, with it: interleaved, five blocks an SM, at most 8 / 16 / 32 heads
-// 52 / 48.5 / 49.5 us; half, three blocks (16 bytes of either half take registers),
-// 8 heads 50, four blocks and 16 heads 57 (the floor is 39.5).
+// dims of ROW_BATCH rows. Measured: 65535 rows of 576 dims, 2 / 4 / 8 rows in flight
+// 36 / 29 / 26.6 us (the floor is 22.3); 8192 rows x 128 heads x 64 dims, interleaved,
+// 46.2 us (the floor is 39.5). The numbers of heads and blocks were chosen when every
+// thread ended with a fence that is gone: interleaved, five blocks an SM, at most 8 / 16
+// / 32 heads 52 / 48.5 / 49.5 us; half, three blocks (16 bytes of either half take
+// registers), 8 heads 50, four blocks and 16 heads 57.
 constexpr int HEAD_BATCH = 4, ROW_BATCH = 8;
 constexpr int most_heads(bool half) { return half ? 8 : 16; }
 
@@ -270,11 +271,6 @@ __global__ void __launch_bounds__(RT, HALF || ROWS ? 3 : 5) k_rope_rows(const __
       }
     }
   }
-  // An attention call behind this one (a programmatic dependent launch) reads q, by
-  // tensor copies, once every block here has ended, without waiting for the end of
-  // the grid: what was written is in place by then. (5 us of the largest calls.)
-  __threadfence();
-  asm volatile("fence.proxy.async.global;\n" ::: "memory");
 }
 
 template <typename T, bool HALF, bool VECTOR>
