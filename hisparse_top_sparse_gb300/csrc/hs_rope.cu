@@ -180,6 +180,8 @@ __global__ void __launch_bounds__(RT, HALF || ROWS ? 3 : 5) k_rope_rows(const __
         sn[k] *= a.sign;
       }
     };
+    // (which product of a sum is fused is written down: left to the compiler it differed
+    // between the variants, and a row's last bits with its alignment)
     auto turn = [&](Raw &x, Raw &y) {
       float f[N];
       A::unpack(x, f);
@@ -189,16 +191,16 @@ __global__ void __launch_bounds__(RT, HALF || ROWS ? 3 : 5) k_rope_rows(const __
 #pragma unroll
         for (int k = 0; k < PAIRS; ++k) {
           const float u = f[k], v = g[k];
-          f[k] = u * c[k] - v * sn[k];
-          g[k] = v * c[k] + u * sn[k];
+          f[k] = fmaf(u, c[k], -(v * sn[k]));
+          g[k] = fmaf(u, sn[k], v * c[k]);
         }
         y = A::pack(g);
       } else {
 #pragma unroll
         for (int k = 0; k < PAIRS; ++k) {
           const float u = f[2 * k], v = f[2 * k + 1];
-          f[2 * k] = u * c[k] - v * sn[k];
-          f[2 * k + 1] = v * c[k] + u * sn[k];
+          f[2 * k] = fmaf(u, c[k], -(v * sn[k]));
+          f[2 * k + 1] = fmaf(u, sn[k], v * c[k]);
         }
       }
       x = A::pack(f);

@@ -425,8 +425,8 @@ int hs_sparse_attn_decode_q4(const void *q, const void *kv, int64_t n_kv_rows,
  * Requirements: n >= 0, 1 <= heads <= 65535, rot_dim even, 2 <= rot_dim, rot_off +
  * rot_dim <= head_dim <= 65536, heads * head_dim <= 2^30, strides (in elements)
  * in 0..2^40, no two rows or heads of dst overlapping, factor finite, arrays
- * aligned to their elements. Any alignment and stride will do; where they allow
- * 16-byte accesses those are used.
+ * aligned to their elements. Any alignment and stride will do, with the same
+ * results; where they allow 16-byte accesses those are used.
  */
 int hs_rope_rows(const void *src, int64_t src_row_stride, int64_t src_head_stride, int64_t src_rows,
                  void *dst, int64_t dst_row_stride, int64_t dst_head_stride, int64_t dst_rows,
