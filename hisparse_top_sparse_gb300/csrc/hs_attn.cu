@@ -69,13 +69,14 @@
 // k_attn_pair<HS_ROWS_Q4> reads q4 rows (hs_q4.cuh), whose values enter the tiles as
 // 2^-15 of themselves (exactly; the softmax's scale and the output's make up for
 // it). Its rows come straight into registers, a tile ahead: 18 KB of them are in
-// flight a tile pair, which the L1 holds, and without raw rings a pair moves some
-// 190 KB through shared memory, not 230. 128 / 512 rows x 128 heads x 2048 keys 81.3 /
-// 281 us (through raw rings 91.6 / 316), a tile pair per 1.05 us. That bandwidth is
-// what bounds it: the products' operands (124 KB, 48 of them Q's dims 384..575 read
-// anew for every tile), the decoded rows (52), P (32) and the loads take 1850 of a
-// pair's 2070 cycles at 128 bytes each; per-warp stamps show Q K^T of one tile or
-// the other in issue all the time, 1960 cycles for what takes 860 alone. Measured
+// flight a tile pair, which the L1 holds, and without raw rings a pair moves, by
+// count, 244 KB through shared memory and the L1, 40 less. 128 / 512 rows x 128 heads
+// x 2048 keys 81.4 / 281 us (through raw rings 91.6 / 316), a tile pair per 1.05 us.
+// That bandwidth is what bounds it: the products' operands (124 KB, 48 of them Q's
+// dims 384..575 read anew for every tile), the decoded rows (52), P (32) and the
+// loads (36) take 1900 of a pair's 2070 cycles at 128 bytes each; per-warp stamps
+// show Q K^T of one tile or the other in issue all the time, 1960 cycles for what
+// takes 860 alone. Measured
 // and not kept: P V's operand P from shared memory, so that S is free once it is
 // read, 85.5 us; two exchange slots 82.9; ring A, VP or VO a slot longer 83, 84.7,
 // 82.8 (of 81.8).
@@ -177,7 +178,7 @@ struct Lay {
   // TMEM, outside the slots of the first tiles, which are gathered meanwhile:
   // ring A behind slot 0 (bf16: two blocks in its two slots, else one), ring VO
   // behind slot 0, the P buffers (the sixth block of bf16), and for quantised rows
-  // ring VP behind slot 0 and (q8) the raw ring of own tiles.
+  // ring VP (q8: behind slot 0) and (q8) the raw ring of own tiles.
   __host__ __device__ static constexpr uint32_t q_stage_off(int a) {
     constexpr int BLK = HG * 128, in_a = (RA_SLOTS - 1) * RA_SLOT_BYTES / BLK;
     if (a < in_a) return RA_OFF + RA_SLOT_BYTES + a * BLK;
@@ -788,10 +789,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(F == HS_ROWS_BF16 ? ATTN_M
   // Q by nine tensor copies of 128 heads x 64 dims (16 KB, 128-byte swizzle,
   // rows past H filled with zeros), all issued by this CTA into its own
   // shared memory: dims 384..575 land in SMEM as the MMA's A operand, dims
-  // 0..383 in a staging area over the (still empty) slots 1 and 2 of ring
-  // A, 1 to 3 of ring VO and the P buffers, from where one lane moves them
-  // into TMEM. Slot 0 of rings A and VO and ring VP stay free, so the first
-  // own and the first peer tiles are gathered while Q comes in.
+  // 0..383 in a staging area over still empty places (Lay::q_stage_off: the later
+  // slots of rings A and VO, the P buffers, of the kernels for quantised rows ring VP
+  // and the raw ring as well), from where one lane moves them into TMEM. Slot 0 of
+  // rings A and VO, and in bf16 ring VP, stay free, so the first own and (bf16) the
+  // first peer tiles are gathered while Q comes in.
   // The copies are issued by the P V issuer warp, whose first MMA waits for
   // the first P anyway: issuing them can stall the issuing thread for
   // microseconds while the other CTAs of the wave load their Q. They land on

@@ -79,8 +79,9 @@ int hs_sm_count(int *sms);
 // Formats of a cache's rows, as the attention kernels are told them.
 enum { HS_ROWS_BF16 = 0, HS_ROWS_Q8 = 1, HS_ROWS_Q4 = 2 };
 // Attention over q8 or q4 rows (format) for up to HS_ATTN_FEW_HEADS heads, its
-// arguments checked (scale: of the values as the kernel has them): n parts of `keys` keys a row (n > 1: O / l and the log-sum-exp of a
-// part in f32 to part_o and part_lse); blocks that run at once.
+// arguments checked (scale: of the values as the kernel has them): n parts of `keys`
+// keys a row (n > 1: O / l and the log-sum-exp of a part in f32 to part_o and
+// part_lse); blocks that run at once.
 constexpr int HS_ATTN_FEW_HEADS = 16;
 int hs_attn_few_places(int *places);
 int hs_attn_few_launch(int format, const void *q, const void *kv, int64_t n_kv, const int32_t *idx, int32_t R,

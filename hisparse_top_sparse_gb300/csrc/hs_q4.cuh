@@ -49,9 +49,9 @@ __device__ __forceinline__ float q4_scale(uint32_t byte) { return __uint_as_floa
 // Computation of elementary functions on the IBM RISC System/6000 processor,
 // 1990): the result's error before its rounding is the reciprocal's times the
 // correction, some 2^-45, where a middle is exact and any other quotient of a float
-// by a four-bit scale is further than half a unit from it. (Checked on the host
-// for the eight fractions, reciprocals off by up to two units, and the 20000 floats
-// on either side of every middle.)
+// by a four-bit scale is further than half a unit from it. (tests/test_q4_codes.py
+// goes through the eight fractions, reciprocals off by up to two units, and the 20000
+// floats on either side of every middle.)
 __device__ __forceinline__ float q4_reciprocal(float s) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(s));

@@ -11,8 +11,9 @@
 // 69.5, 87 %; 131072 f32 rows 62 and 62; 4 rows 1.9 and 1.6. Reading back is bound by
 // HBM; quantising by it and by the ALU pipe, busy for 59 % of the cycles (93 us with
 // maxima value by value, a rounded reciprocal a group and codes put together by
-// shifts). Two bf16 rows of a warp in flight and four blocks an SM: three blocks 81 us,
-// three rows 81, five blocks spill.
+// shifts). Two bf16 rows of a warp in flight and four blocks an SM (64 registers, one
+// word of the bf16 kernel spilled): three blocks 81 us, three rows 81, five blocks spill
+// more.
 
 #include "hs_q4.cuh"
 #include "hs_rows.cuh"

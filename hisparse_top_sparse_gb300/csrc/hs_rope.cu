@@ -25,8 +25,8 @@ namespace {
 constexpr int RT = 256;               // threads of a block, at most
 // A thread has HEAD_BATCH heads of a row in flight, of at most most_heads(), or copies
 // dims of ROW_BATCH rows. Measured: 65535 rows of 576 dims, 2 / 4 / 8 rows in flight
-// 36 / 29 / 26.6 us (the floor is 22.3); 8192 rows x 128 heads x 64 dims, interleaved,
-// 46.2 us (the floor is 39.5). The numbers of heads and blocks were chosen when every
+// 36 / 29 / 26.5 us (the floor is 22.3); 8192 rows x 128 heads x 64 dims, interleaved,
+// 47.4 us (the floor is 39.5). The numbers of heads and blocks were chosen when every
 // thread ended with a fence that is gone: interleaved, five blocks an SM, at most 8 / 16
 // / 32 heads 52 / 48.5 / 49.5 us; half, three blocks (16 bytes of either half take
 // registers), 8 heads 50, four blocks and 16 heads 57.
@@ -377,7 +377,7 @@ extern "C" int hs_rope_rows(const void *src, int64_t src_row_stride, int64_t src
   a.copy_units = same ? 0 : (head_dim - rot_dim) / per;
   // Units of a thread: one up to 512 threads an SM, then up to most_heads() heads of a
   // row or, where there are fewer heads than a batch, ROW_BATCH rows (with one unit up
-  // to 2048 threads an SM 8191 rows of 576 dims took 10.7 us, now 5.1, and 512 rows of
+  // to 2048 threads an SM 8191 rows of 576 dims took 10.7 us, now 4.7, and 512 rows of
   // 128 heads 9.1, now 5).
   int sms = 0;
   if ((rc = hs_sm_count(&sms))) return rc;
