@@ -1553,8 +1553,7 @@ static int check_attn(const void *q, const void *kv_resident, int64_t n_resident
   if (((uintptr_t)q & 15) || ((uintptr_t)kv_resident & 15) || ((uintptr_t)kv_hot & 15) ||
       ((uintptr_t)out & 15))
     return hs_set_error(HS_ERR_INVALID_ARG, "q, kv and out must be 16-byte aligned");
-  if (!(scale == scale)) return hs_set_error(HS_ERR_INVALID_ARG, "scale is NaN");
-  return HS_OK;
+  return hs_check_scale(scale, 127);
 }
 
 // Launches k_attn_pair<F>, its arguments checked (parts: the split of the rows'
@@ -1639,6 +1638,7 @@ int hs_attn_launch(const void *q, const void *kv_resident, int64_t n_resident, c
   const int rc = check_attn(q, kv_resident, n_resident, kv_hot, n_hot, fully_resident, n_reqs, idx, R, H, K,
                             scale, out);
   if (rc || R == 0) return rc;
+  if (scale < FLT_MIN) scale = FLT_MIN;      // equal weights all the same; 0 times a masked -inf is NaN
   const Parts whole = {1, K, R, nullptr, nullptr};
   return attn_launch<HS_ROWS_BF16>(q, kv_resident, n_resident, kv_hot, n_hot, row_req, fully_resident,
                             n_reqs, idx, R, H, K, scale, out, lse, status, whole, pdl, stream);
@@ -1774,14 +1774,10 @@ static int attn_quantised(const void *q, const void *kv, int64_t n_kv_rows, cons
     return hs_set_error(HS_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   if (((uintptr_t)idx | (uintptr_t)lse | (uintptr_t)status) & 3)
     return hs_set_error(HS_ERR_INVALID_ARG, "idx, lse and status must be 4-byte aligned");
-  // the softmax reference is the scaled maximum, which a negative scale would not
-  // give; times log2(e), as the kernels take it, the scale is to be finite too
-  // (and so is it for scores that are 2^-15 of theirs)
-  const int most = F == HS_ROWS_Q4 ? 100 : 127;
-  if (!(scale >= 0.f) || scale > ldexpf(1.f, most))
-    return hs_set_error(HS_ERR_INVALID_ARG, "scale must be in [0, 2^%d]", most);
+  int rc = hs_check_scale(scale, F == HS_ROWS_Q4 ? 100 : 127);   // (q4: for scores that are 2^-15 of theirs)
+  if (rc) return rc;
   if (scale < FLT_MIN) scale = FLT_MIN;      // equal weights all the same; 0 times a masked -inf is NaN
-  int rc = check_attn(q, kv, n_kv_rows, nullptr, 0, nullptr, 0, idx, R, H, K, scale, out);
+  rc = check_attn(q, kv, n_kv_rows, nullptr, 0, nullptr, 0, idx, R, H, K, scale, out);
   if (rc || R == 0) return rc;
   if (F == HS_ROWS_Q4) scale *= (float)(1 << Q4_SHIFT);
   const bool few_heads = H <= HS_ATTN_FEW_HEADS;

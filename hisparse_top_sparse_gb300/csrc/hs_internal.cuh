@@ -149,6 +149,15 @@ int hs_swap_gather_launch(hs_buffer *buf, const int32_t *req_id_per_row,
 
 // ---- attention launcher (hs_attn.cu) ----------------------------------------
 
+// The softmax reference is the scaled maximum, which a negative scale would not give
+// (and masked keys' -inf would turn round); times log2(e), as the kernels take it,
+// the scale is to be finite too.
+static inline int hs_check_scale(float scale, int most) {
+  if (!(scale >= 0.f) || scale > ldexpf(1.f, most))
+    return hs_set_error(HS_ERR_INVALID_ARG, "scale must be in [0, 2^%d]", most);
+  return HS_OK;
+}
+
 // hs_sparse_attn_decode_mixed with the launch made a programmatic dependent
 // one (pdl) or a plain one.
 int hs_attn_launch(const void *q, const void *kv_resident, int64_t n_resident, const void *kv_hot,

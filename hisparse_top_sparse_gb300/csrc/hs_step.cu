@@ -119,7 +119,8 @@ extern "C" int hs_swap_in_attn_decode(hs_buffer *buf, const int32_t *req_id_per_
     return hs_set_error(HS_ERR_INVALID_ARG, "NULL topk or out_slot_idx");
   if (((uintptr_t)q & 15) || ((uintptr_t)out & 15))
     return hs_set_error(HS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
-  if (!(scale == scale)) return hs_set_error(HS_ERR_INVALID_ARG, "scale is NaN");
+  rc = hs_check_scale(scale, 127);
+  if (rc) return rc;
   int32_t ends[HS_MAX_GROUPS];
   int G = n_groups;
   if (n_groups < 0 || n_groups > HS_MAX_GROUPS || (n_groups > 0 && !group_row_end))

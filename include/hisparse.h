@@ -260,7 +260,8 @@ int hs_swap_in(hs_buffer *buf, const int32_t *req_id_per_row,
  *   lse    device float [R][H] or NULL
  *   status device uint32 or NULL: HS_STATUS_TIMEOUT is OR-ed in if one of
  *          the kernel's bounded internal waits gives up (never expected)
- * Requirements: R >= 0, 1 <= H <= 1024, K >= 0.
+ * Requirements: R >= 0, 1 <= H <= 1024, K >= 0, 0 <= scale <= 2^127 (0: equal
+ * weights).
  * Launch: a programmatic dependent launch on `stream`: it may begin before the
  * previous kernel in the stream has finished, if that kernel lets its dependents
  * start early, as hs_resolve_topk does, or has no blocks left to run. It reads its
